@@ -234,6 +234,82 @@ Q4LIN_API int64_t q4lin_fmt_weight_bytes(int fmt, int64_t n, int64_t k);
  * for the others), or a negative status.  Pure host function. */
 Q4LIN_API int64_t q4lin_fmt_workspace_bytes(int fmt, int64_t n, int64_t k, int64_t t);
 
+/* Low-rank adapters of many requests beside one shared weight:
+ *
+ *     y[t][n] = sum_k W[n][k] x[t][k] + s_a sum_r B_a[n][r] (sum_k A_a[r][k] x[t][k]),
+ *     a = adapter_ids[t],
+ *
+ * without the second term where adapter_ids[t] is outside 0..adapters-1 (-1:
+ * the base weight alone).  W, x and y as for q4lin_linear_fmt (any format).
+ *
+ *   lora_a       bf16 [adapters][rank][K], 16-byte aligned
+ *   lora_b       bf16 [adapters][N][rank], 16-byte aligned
+ *   lora_scale   float [adapters], 4-byte aligned; NULL: every s_a is 1
+ *   adapter_ids  int32 [T] in device memory, 4-byte aligned, any order
+ *
+ * rank: a multiple of 8 from 8 to 256 (an adapter of a smaller rank is
+ * padded with zeros); adapters: 1 to 2^20; T up to 2^19.  Both terms are
+ * binary32 and y is rounded once.  workspace: q4lin_lora_workspace_bytes()
+ * bytes, 256-byte aligned.  An infinity or NaN in one adapter stays in its
+ * own tokens' rows.  y must not overlap any input or the workspace.  Errors
+ * as for q4lin_linear_fmt. */
+Q4LIN_API int q4lin_linear_lora(int fmt, const void *x, const void *w, const void *w_hi, const void *scales,
+                      const void *lora_a, const void *lora_b, const void *lora_scale, const void *adapter_ids,
+                      void *y, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_t rank,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace q4lin_linear_lora needs (0 for an empty product), or a
+ * negative status.  Pure host function. */
+Q4LIN_API int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters,
+                      int64_t rank);
+
+/* A mixture-of-experts layer for few tokens, its experts in q4lin_linear's
+ * weight format.  With l[t][e] = sum_k router[e][k] x[t][k] and p the softmax
+ * of a token's l over the experts, a token takes the top_k experts of the
+ * largest l (equal ones: the lowest e first; a NaN counts as the lowest) with
+ * weights p, divided by the sum of the chosen p where renormalize is not 0:
+ *
+ *     h_j = silu(Wg_e x) * (Wu_e x)     y[t] = sum_j weights[t][j] Wd_e h_j,  e = ids[t][j]
+ *
+ *   x            bf16 [T][K], 16-byte aligned
+ *   router       bf16 [experts][K], 16-byte aligned
+ *   codes_gate, codes_up    uint8 [experts][inner][K/2]; scales_gate,
+ *                scales_up  fp16 [experts][inner][K/64]
+ *   codes_down   uint8 [experts][K][inner/2]; scales_down fp16
+ *                [experts][K][inner/64]; codes 16-byte, scales 2-byte aligned
+ *   y            bf16 [T][K], 2-byte aligned
+ *   ids          int32 [T][top_k], weights float [T][top_k], largest l first,
+ *                4-byte aligned: written by q4lin_moe_route and q4lin_moe,
+ *                read by q4lin_moe_experts
+ *
+ * q4lin_moe is the whole layer; q4lin_moe_route gives ids and weights alone;
+ * q4lin_moe_experts takes them (routing rules of one's own; one process's
+ * share of the experts): there an id outside 0..experts-1 contributes
+ * nothing, a token without a valid id gets zeros, and an expert that a token
+ * names twice counts twice.  The sums are binary32 or wider, h keeps 16
+ * significant bits, y is rounded once.  The weights of an expert are read
+ * once for up to 32 of its tokens.
+ *
+ * K and inner: positive multiples of 64; 1 <= experts <= 1024; 1 <= top_k <=
+ * experts; T K 2 bytes, 4 T top_k inner bytes and T top_k K each below 2^31.  workspace (not for q4lin_moe_route):
+ * q4lin_moe_workspace_bytes() bytes, 256-byte aligned.  T = 0 is an empty
+ * call.  No output may overlap an input, another output or the workspace.
+ * Errors as for q4lin_linear. */
+Q4LIN_API int q4lin_moe(const void *x, const void *router, const void *codes_gate, const void *scales_gate,
+                      const void *codes_up, const void *scales_up, const void *codes_down, const void *scales_down,
+                      void *y, void *ids, void *weights, int64_t inner, int64_t k, int64_t experts, int64_t top_k,
+                      int64_t t, int renormalize, void *workspace, size_t workspace_bytes, void *stream);
+Q4LIN_API int q4lin_moe_route(const void *x, const void *router, void *ids, void *weights, int64_t k,
+                      int64_t experts, int64_t top_k, int64_t t, int renormalize, void *stream);
+Q4LIN_API int q4lin_moe_experts(const void *x, const void *ids, const void *weights, const void *codes_gate,
+                      const void *scales_gate, const void *codes_up, const void *scales_up, const void *codes_down,
+                      const void *scales_down, void *y, int64_t inner, int64_t k, int64_t experts, int64_t top_k,
+                      int64_t t, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace q4lin_moe and q4lin_moe_experts need (0 for T = 0), or
+ * -Q4LIN_E_SHAPE.  Pure host function. */
+Q4LIN_API int64_t q4lin_moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t);
+
 /* Static, human-readable text for a status code (never NULL). */
 Q4LIN_API const char *q4lin_status_string(int status);
 

@@ -46,7 +46,8 @@ EXPORTED = ("q4lin_workspace_bytes", "q4lin_linear", "q4lin_linear_add", "q4lin_
             "q4lin_pair_workspace_bytes", "q4lin_linear_swiglu", "q4lin_swiglu_workspace_bytes",
             "q4lin_status_string", "q4lin_route", "q4lin_version", "q4lin_linear_noalloc",
             "q4lin_noalloc_scratch_bytes", "q4lin_linear_fmt", "q4lin_fmt_weight_bytes",
-            "q4lin_fmt_workspace_bytes")
+            "q4lin_fmt_workspace_bytes", "q4lin_linear_lora", "q4lin_lora_workspace_bytes", "q4lin_moe",
+            "q4lin_moe_route", "q4lin_moe_experts", "q4lin_moe_workspace_bytes")
 
 
 class Q4LinError(RuntimeError):
@@ -101,6 +102,19 @@ def _load() -> ctypes.CDLL:
     lib.q4lin_fmt_weight_bytes.restype = i64
     lib.q4lin_fmt_workspace_bytes.argtypes = [ci, i64, i64, i64]
     lib.q4lin_fmt_workspace_bytes.restype = i64
+    cz = ctypes.c_size_t
+    lib.q4lin_linear_lora.argtypes = [ci] + [vp] * 9 + [i64] * 5 + [vp, cz, vp]
+    lib.q4lin_linear_lora.restype = ci
+    lib.q4lin_lora_workspace_bytes.argtypes = [ci] + [i64] * 5
+    lib.q4lin_lora_workspace_bytes.restype = i64
+    lib.q4lin_moe.argtypes = [vp] * 11 + [i64] * 5 + [ci, vp, cz, vp]
+    lib.q4lin_moe.restype = ci
+    lib.q4lin_moe_route.argtypes = [vp] * 4 + [i64] * 4 + [ci, vp]
+    lib.q4lin_moe_route.restype = ci
+    lib.q4lin_moe_experts.argtypes = [vp] * 10 + [i64] * 5 + [vp, cz, vp]
+    lib.q4lin_moe_experts.restype = ci
+    lib.q4lin_moe_workspace_bytes.argtypes = [i64] * 5
+    lib.q4lin_moe_workspace_bytes.restype = i64
     return lib
 
 
@@ -184,6 +198,46 @@ def q4lin_fmt_weight_bytes(fmt: int, n: int, k: int) -> int:
 
 def q4lin_fmt_workspace_bytes(fmt: int, n: int, k: int, t: int) -> int:
     return int(load().q4lin_fmt_workspace_bytes(int(fmt), int(n), int(k), int(t)))
+
+
+def q4lin_linear_lora(fmt: int, x: int, w: int, w_hi: int, scales: int, lora_a: int, lora_b: int, lora_scale: int,
+                      adapter_ids: int, y: int, n: int, k: int, t: int, adapters: int, rank: int, workspace: int,
+                      workspace_bytes: int, stream: int) -> int:
+    """Raw call of the low-rank-adapter entry point; returns the status."""
+    return int(load().q4lin_linear_lora(fmt, x, w, w_hi, scales, lora_a, lora_b, lora_scale, adapter_ids, y,
+                                        n, k, t, adapters, rank, workspace, workspace_bytes, stream))
+
+
+def q4lin_lora_workspace_bytes(fmt: int, n: int, k: int, t: int, adapters: int, rank: int) -> int:
+    return int(load().q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank))
+
+
+def q4lin_moe(x: int, router: int, codes_gate: int, scales_gate: int, codes_up: int, scales_up: int, codes_down: int,
+              scales_down: int, y: int, ids: int, weights: int, inner: int, k: int, experts: int, top_k: int, t: int,
+              renormalize: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    """Raw call of the mixture-of-experts layer; returns the status."""
+    return int(load().q4lin_moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down, y,
+                                ids, weights, inner, k, experts, top_k, t, renormalize, workspace, workspace_bytes,
+                                stream))
+
+
+def q4lin_moe_route(x: int, router: int, ids: int, weights: int, k: int, experts: int, top_k: int, t: int,
+                    renormalize: int, stream: int) -> int:
+    """Raw call of the experts' router; returns the status."""
+    return int(load().q4lin_moe_route(x, router, ids, weights, k, experts, top_k, t, renormalize, stream))
+
+
+def q4lin_moe_experts(x: int, ids: int, weights: int, codes_gate: int, scales_gate: int, codes_up: int,
+                      scales_up: int, codes_down: int, scales_down: int, y: int, inner: int, k: int, experts: int,
+                      top_k: int, t: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    """Raw call of the experts on given routing; returns the status."""
+    return int(load().q4lin_moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, codes_down,
+                                        scales_down, y, inner, k, experts, top_k, t, workspace, workspace_bytes,
+                                        stream))
+
+
+def q4lin_moe_workspace_bytes(inner: int, k: int, experts: int, top_k: int, t: int) -> int:
+    return int(load().q4lin_moe_workspace_bytes(inner, k, experts, top_k, t))
 
 
 def q4lin_status_string(status: int) -> str:
@@ -350,3 +404,181 @@ def linear_fmt(fmt, x, w, w_hi=None, scales=None, y=None, stream=None):
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return y
+
+
+def _checked(name, ten, shape, size):
+    """The tensor's address; it must be contiguous, of this shape and element size."""
+    if tuple(ten.shape) != shape or ten.element_size() != size or not ten.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s with %d-byte elements, got %s of %s" % (
+            name, shape, size, tuple(ten.shape), ten.dtype))
+    return ten.data_ptr()
+
+
+def _workspace(need, workspace, device):
+    """(address, bytes, tensor to keep) of the caller's workspace or a new one of ``need`` bytes."""
+    import torch
+
+    if need < 0:
+        raise Q4LinError(-need)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _stream_of(stream, device, *made):
+    """The handle of ``stream`` (None: the current one).  Tensors ``made`` by
+    this call belong to the current stream; on another one they are kept from
+    reuse until its work is done."""
+    import torch
+
+    current = torch.cuda.current_stream(device).cuda_stream
+    if stream is None or stream == current:
+        return current
+    other = torch.cuda.ExternalStream(stream, device=device)
+    for ten in made:
+        if ten is not None:
+            ten.record_stream(other)
+    return stream
+
+
+_FMT_PLANES = {  # bytes per row of K weights: codes, high plane, scales
+    Q4LIN_FMT_Q4G64_F16S: lambda k: (k // 2, 0, k // 32),
+    Q4LIN_FMT_Q5G64_F16S: lambda k: (k // 2, k // 8, k // 32),
+    Q4LIN_FMT_Q6G64_F16S: lambda k: (k // 2, k // 4, k // 32),
+    Q4LIN_FMT_W8G32_F16S: lambda k: (k, 0, k // 16),
+    Q4LIN_FMT_NVFP4: lambda k: (k // 2, 0, k // 16),
+    Q4LIN_FMT_BF16: lambda k: (2 * k, 0, 0),
+}
+
+
+def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, fmt=Q4LIN_FMT_Q4G64_F16S,
+                codes_hi=None, y=None, workspace=None, stream=None):
+    """Y = W x X plus each token's own low-rank adapter, on torch device
+    tensors: ``y[t] = W x[t] + s_a B_a (A_a x[t])`` with ``a = adapter_ids[t]``
+    (outside ``0..L-1``: the base weight alone).
+
+    ``x`` ``[T, K]`` bf16; ``codes``, ``codes_hi``, ``scales`` the weight's
+    planes in format ``fmt`` (Q4LIN_FMT_*; read as bytes, ``codes`` gives N);
+    ``lora_a`` bf16 ``[L, R, K]``, ``lora_b`` bf16 ``[L, N, R]`` (R a multiple
+    of 8 up to 256), ``adapter_ids`` int32 ``[T]``, ``lora_scale`` float32
+    ``[L]`` or None for ones.  Returns ``y`` ``[T, N]``.
+    """
+    import torch
+
+    t, k = x.shape
+    n = codes.shape[0]
+    adapters, rank = lora_a.shape[0], lora_a.shape[1]
+    if fmt not in _FMT_PLANES:
+        raise Q4LinError(Q4LIN_E_FORMAT)
+    ptr = []
+    for name, ten, per_row in zip(("codes", "codes_hi", "scales"), (codes, codes_hi, scales), _FMT_PLANES[fmt](k)):
+        if per_row == 0:
+            ptr.append(None)
+            continue
+        if ten is None or not ten.is_contiguous() or ten.numel() * ten.element_size() != n * per_row:
+            raise ValueError("%s must be a contiguous plane of %d bytes for each of the %d rows" % (name, per_row, n))
+        ptr.append(ten.data_ptr())
+    xp = _checked("x", x, (t, k), 2)
+    ap = _checked("lora_a", lora_a, (adapters, rank, k), 2)
+    bp = _checked("lora_b", lora_b, (adapters, n, rank), 2)
+    ip = _checked("adapter_ids", adapter_ids, (t,), 4)
+    sp = _checked("lora_scale", lora_scale, (adapters,), 4) if lora_scale is not None else None
+    if y is None:
+        y = torch.empty((t, n), dtype=torch.bfloat16, device=x.device)
+    yp = _checked("y", y, (t, n), 2)
+    lib = load()
+    wp, wb, workspace = _workspace(lib.q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank), workspace, x.device)
+    stream = _stream_of(stream, x.device, y, workspace)
+    st = lib.q4lin_linear_lora(fmt, xp, ptr[0], ptr[1], ptr[2], ap, bp, sp, ip, yp, n, k, t, adapters, rank, wp, wb,
+                               stream)
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return y
+
+
+def _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down):
+    """(experts, inner, the six addresses) of a layer's expert weights."""
+    experts, inner = codes_gate.shape[0], codes_gate.shape[1]
+    return experts, inner, (
+        _checked("codes_gate", codes_gate, (experts, inner, k // 2), 1),
+        _checked("scales_gate", scales_gate, (experts, inner, k // 64), 2),
+        _checked("codes_up", codes_up, (experts, inner, k // 2), 1),
+        _checked("scales_up", scales_up, (experts, inner, k // 64), 2),
+        _checked("codes_down", codes_down, (experts, k, inner // 2), 1),
+        _checked("scales_down", scales_down, (experts, k, inner // 64), 2))
+
+
+def moe_route(x, router, top_k, renormalize=True, stream=None):
+    """The experts of each token, on torch device tensors: softmax over
+    ``x router^T``, the ``top_k`` largest (ties: the lowest index), weights
+    divided by their sum where ``renormalize``.  ``x`` bf16 ``[T, K]``,
+    ``router`` bf16 ``[E, K]``.  Returns ``(ids int32 [T, top_k], weights
+    float32 [T, top_k])``."""
+    import torch
+
+    t, k = x.shape
+    experts = router.shape[0]
+    xp = _checked("x", x, (t, k), 2)
+    rp = _checked("router", router, (experts, k), 2)
+    ids = torch.empty((t, top_k), dtype=torch.int32, device=x.device)
+    weights = torch.empty((t, top_k), dtype=torch.float32, device=x.device)
+    stream = _stream_of(stream, x.device, ids, weights)
+    st = load().q4lin_moe_route(xp, rp, ids.data_ptr(), weights.data_ptr(), k, experts, top_k, t,
+                                1 if renormalize else 0, stream)
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return ids, weights
+
+
+def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down, y=None,
+                workspace=None, stream=None):
+    """``y[t] = sum_j weights[t, j] Wd_e (silu(Wg_e x[t]) * (Wu_e x[t]))`` with
+    ``e = ids[t, j]`` (outside ``0..E-1``: nothing), on torch device tensors.
+    ``x`` bf16 ``[T, K]``; ``ids`` int32, ``weights`` float32 ``[T, top_k]``;
+    gate and up codes uint8 ``[E, I, K/2]``, scales fp16 ``[E, I, K/64]``;
+    down codes ``[E, K, I/2]``, scales ``[E, K, I/64]``.  Returns ``y`` bf16
+    ``[T, K]``."""
+    import torch
+
+    t, k = x.shape
+    top_k = ids.shape[1]
+    xp = _checked("x", x, (t, k), 2)
+    ip = _checked("ids", ids, (t, top_k), 4)
+    vp = _checked("weights", weights, (t, top_k), 4)
+    experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
+    if y is None:
+        y = torch.empty((t, k), dtype=torch.bfloat16, device=x.device)
+    yp = _checked("y", y, (t, k), 2)
+    lib = load()
+    wp, wb, workspace = _workspace(lib.q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)
+    stream = _stream_of(stream, x.device, y, workspace)
+    st = lib.q4lin_moe_experts(xp, ip, vp, *planes, yp, inner, k, experts, top_k, t, wp, wb, stream)
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return y
+
+
+def moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down, top_k, renormalize=True,
+        y=None, workspace=None, stream=None):
+    """A whole mixture-of-experts layer on torch device tensors: ``moe_route``
+    and ``moe_experts`` in one call (their arguments).  Returns ``(y, ids,
+    weights)``."""
+    import torch
+
+    t, k = x.shape
+    xp = _checked("x", x, (t, k), 2)
+    experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
+    rp = _checked("router", router, (experts, k), 2)
+    ids = torch.empty((t, top_k), dtype=torch.int32, device=x.device)
+    weights = torch.empty((t, top_k), dtype=torch.float32, device=x.device)
+    if y is None:
+        y = torch.empty((t, k), dtype=torch.bfloat16, device=x.device)
+    yp = _checked("y", y, (t, k), 2)
+    lib = load()
+    wp, wb, workspace = _workspace(lib.q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)
+    stream = _stream_of(stream, x.device, y, workspace, ids, weights)
+    st = lib.q4lin_moe(xp, rp, *planes, yp, ids.data_ptr(), weights.data_ptr(), inner, k, experts, top_k, t,
+                       1 if renormalize else 0, wp, wb, stream)
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return y, ids, weights

@@ -170,6 +170,19 @@ int run_linear(const void* x, const void* codes, const void* scales, const void*
   return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
 }
 
+// The planes of a weight in one of the formats beside its activations and
+// output: NULL and alignment (the planes a format lacks are not looked at).
+int check_planes(int fmt, const void* x, const void* w, const void* w_hi, const void* scales, const void* y) {
+  const bool has_hi = fmt == Q4LIN_FMT_Q5G64_F16S || fmt == Q4LIN_FMT_Q6G64_F16S;
+  const bool has_sc = fmt != Q4LIN_FMT_BF16;
+  if (!x || !w || !y || (has_hi && !w_hi) || (has_sc && !scales)) return Q4LIN_E_NULL;
+  const uintptr_t hi_align = fmt == Q4LIN_FMT_Q5G64_F16S ? 4 : 8;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2) || (has_hi && !aligned(w_hi, hi_align)) ||
+      (has_sc && !aligned(scales, 2)))
+    return Q4LIN_E_ALIGN;
+  return Q4LIN_OK;
+}
+
 size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // LinearSwiGLU's plan: how the gate and up sums are made, and the workspace.
@@ -235,6 +248,64 @@ hipError_t launch_sums(int route, const q4lin::GemvArgs& a, hipStream_t s) {
   return q4lin::launch_gemv(a, s);
 }
 
+// The low-rank adapters' limits, and where the base product's binary32 sums
+// and the tokens' rank values lie in the workspace.
+constexpr int64_t kMaxLoraT = int64_t(1) << 19;
+constexpr int64_t kMaxRank = 256;
+constexpr int64_t kMaxAdapters = int64_t(1) << 20;
+struct LoraPlan {
+  int route;       // Q4: the base product's route
+  size_t u_bytes;  // the rank values, before the base product's part
+  size_t total;
+};
+int lora_plan(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_t rank, LoraPlan* p) {
+  if (fmt < Q4LIN_FMT_Q4G64_F16S || fmt > Q4LIN_FMT_BF16) return Q4LIN_E_FORMAT;
+  if (!shape_ok(n, k, t) || t > kMaxLoraT || n * t * 4 >= kMaxBytes) return Q4LIN_E_SHAPE;
+  if (fmt != Q4LIN_FMT_Q4G64_F16S && 2 * n * k >= kMaxBytes) return Q4LIN_E_SHAPE;
+  if (adapters < 1 || adapters > kMaxAdapters || rank < 8 || rank > kMaxRank || (rank % 8) != 0) return Q4LIN_E_SHAPE;
+  *p = LoraPlan{Q4LIN_ROUTE_NONE, 0, 0};
+  if (n == 0 || t == 0) return Q4LIN_OK;
+  size_t base = al256((size_t)(n * t * 4));
+  if (fmt == Q4LIN_FMT_Q4G64_F16S) {
+    p->route = pick_route(n, k, t);
+    if (p->route == Q4LIN_ROUTE_TILED) {
+      if (!q4lin::tiled_shape_ok(n, k, t)) return Q4LIN_E_SHAPE;
+      base = q4lin::tiled_pair_workspace_bytes(n, 0, k, t, true);
+    }
+  } else {
+    q4lin::FmtPlan fp;
+    if (!q4lin::fmt_plan(fmt, n, k, t, &fp)) return Q4LIN_E_SHAPE;
+  }
+  p->u_bytes = q4lin::lora_u_bytes(k, t, rank, adapters);
+  p->total = p->u_bytes + base;
+  return Q4LIN_OK;
+}
+
+// The mixture of experts' limits: 32-bit buffer offsets over the activations
+// and over the pairs' gated values.
+bool moe_shape_ok(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t) {
+  if (!shape_ok(inner, k, t) || !shape_ok(k, inner, t) || inner < 64) return false;
+  if (experts < 1 || experts > 1024 || top_k < 1 || top_k > experts) return false;
+  const int64_t most = int64_t(1) << 31;
+  return t * k * 2 < most && t * top_k < most / 64 && t * top_k * inner * 4 < most && t * top_k * k < most;
+}
+bool route_shape_ok(int64_t k, int64_t experts, int64_t top_k, int64_t t) {
+  return shape_ok(experts, k, t) && experts >= 1 && experts <= 1024 && top_k >= 1 && top_k <= experts;
+}
+
+int check_experts(const void* x, const void* ids, const void* weights, const void* const (&planes)[6], const void* y,
+                  const void* workspace, size_t workspace_bytes, size_t need) {
+  if (!x || !ids || !weights || !y) return Q4LIN_E_NULL;
+  for (const void* p : planes)
+    if (!p) return Q4LIN_E_NULL;
+  if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(y, 2)) return Q4LIN_E_ALIGN;
+  for (int i = 0; i < 6; ++i)
+    if (!aligned(planes[i], (i & 1) ? 2 : 16)) return Q4LIN_E_ALIGN;
+  if (workspace_bytes < need) return Q4LIN_E_WORKSPACE;
+  if (!workspace) return Q4LIN_E_NULL;
+  return aligned(workspace, 256) ? Q4LIN_OK : Q4LIN_E_ALIGN;
+}
+
 // ---------------------------------------------------------------------------
 // The no-allocation variant's scratch: a static device array (each GPU the
 // library runs on holds its own copy until the process ends).  Host code
@@ -295,13 +366,8 @@ int q4lin_linear_fmt(int fmt, const void* x, const void* w, const void* w_hi, co
   if (fmt < Q4LIN_FMT_Q5G64_F16S || fmt > Q4LIN_FMT_BF16) return Q4LIN_E_FORMAT;
   if (!shape_ok(n, k, t) || 2 * n * k >= kMaxBytes) return Q4LIN_E_SHAPE;
   if (n == 0 || t == 0) return Q4LIN_OK;
-  const bool has_hi = fmt == Q4LIN_FMT_Q5G64_F16S || fmt == Q4LIN_FMT_Q6G64_F16S;
-  const bool has_sc = fmt != Q4LIN_FMT_BF16;
-  if (!x || !w || !y || (has_hi && !w_hi) || (has_sc && !scales)) return Q4LIN_E_NULL;
-  const uintptr_t hi_align = fmt == Q4LIN_FMT_Q5G64_F16S ? 4 : 8;
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2) || (has_hi && !aligned(w_hi, hi_align)) ||
-      (has_sc && !aligned(scales, 2)))
-    return Q4LIN_E_ALIGN;
+  const int st = check_planes(fmt, x, w, w_hi, scales, y);
+  if (st != Q4LIN_OK) return st;
   q4lin::FmtPlan plan;
   if (!q4lin::fmt_plan(fmt, n, k, t, &plan)) return Q4LIN_E_SHAPE;
   (void)workspace;
@@ -516,6 +582,114 @@ int q4lin_linear_add(const void* x, const void* codes, const void* scales, const
   return run_linear(x, codes, scales, residual, y, n, k, t, workspace, workspace_bytes, stream);
 }
 
+int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_t rank) {
+  LoraPlan p;
+  const int st = lora_plan(fmt, n, k, t, adapters, rank, &p);
+  return st == Q4LIN_OK ? (int64_t)p.total : -(int64_t)st;
+}
+
+int q4lin_linear_lora(int fmt, const void* x, const void* w, const void* w_hi, const void* scales,
+                      const void* lora_a, const void* lora_b, const void* lora_scale, const void* adapter_ids,
+                      void* y, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_t rank,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  LoraPlan p;
+  int st = lora_plan(fmt, n, k, t, adapters, rank, &p);
+  if (st != Q4LIN_OK || n == 0 || t == 0) return st;
+  st = check_planes(fmt, x, w, w_hi, scales, y);
+  if (st != Q4LIN_OK) return st;
+  if (!lora_a || !lora_b || !adapter_ids) return Q4LIN_E_NULL;
+  if (!aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(lora_scale, 4) || !aligned(adapter_ids, 4))
+    return Q4LIN_E_ALIGN;
+  if (workspace_bytes < p.total) return Q4LIN_E_WORKSPACE;
+  if (!workspace) return Q4LIN_E_NULL;
+  if (!aligned(workspace, 256)) return Q4LIN_E_ALIGN;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  float* u = static_cast<float*>(workspace);
+  uint8_t* sums = static_cast<uint8_t*>(workspace) + p.u_bytes;
+  const q4lin::LoraArgs la{x, lora_a, lora_b, lora_scale, adapter_ids, y, n, k, t, adapters, rank};
+  hipError_t e = q4lin::launch_lora_shrink(la, u, s);
+  if (e != hipSuccess) return Q4LIN_E_LAUNCH;
+  // the base product as binary32 sums
+  q4lin::SumSource base{reinterpret_cast<const float*>(sums), nullptr, nullptr, 1, 0};
+  if (p.route == Q4LIN_ROUTE_TILED) {
+    q4lin::TiledArgs a{x, w, scales, y, n, k, t, sums, q4lin::tiled_pick_config(n, k, t)};
+    a.f32 = true;
+    e = q4lin::launch_tiled_pair(q4lin::TiledPairArgs{a, nullptr, nullptr, nullptr, 0}, &base, nullptr, s);
+  } else if (p.route == Q4LIN_ROUTE_DECODE || p.route == Q4LIN_ROUTE_GEMV ||
+             (p.route == Q4LIN_ROUTE_SKINNY && !small_uses_fmt(n, k, t))) {
+    q4lin::GemvArgs a{x, w, scales, sums, n, k, t};
+    a.f32 = true;
+    e = launch_sums(p.route, a, s);
+  } else {
+    q4lin::FmtArgs a{fmt, x, w, w_hi, scales, sums, n, k, t};
+    a.f32 = true;
+    e = q4lin::launch_fmt(a, s);
+  }
+  if (e == hipSuccess) e = q4lin::launch_lora_finish(la, u, base, s);
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int q4lin_moe_route(const void* x, const void* router, void* ids, void* weights, int64_t k, int64_t experts,
+                    int64_t top_k, int64_t t, int renormalize, void* stream) {
+  if (!route_shape_ok(k, experts, top_k, t)) return Q4LIN_E_SHAPE;
+  if (t == 0) return Q4LIN_OK;
+  if (!x || !router || !ids || !weights) return Q4LIN_E_NULL;
+  if (!aligned(x, 16) || !aligned(router, 16) || !aligned(ids, 4) || !aligned(weights, 4)) return Q4LIN_E_ALIGN;
+  q4lin::MoeArgs a{};
+  a.x = x;
+  a.router = router;
+  a.ids = ids;
+  a.weights = weights;
+  a.k = k;
+  a.experts = experts;
+  a.top_k = top_k;
+  a.t = t;
+  a.renorm = renormalize ? 1 : 0;
+  const hipError_t e = q4lin::launch_moe_route(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int64_t q4lin_moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t) {
+  if (!moe_shape_ok(inner, k, experts, top_k, t)) return -Q4LIN_E_SHAPE;
+  return t == 0 ? 0 : (int64_t)q4lin::moe_workspace_bytes(inner, k, experts, top_k, t);
+}
+
+int q4lin_moe_experts(const void* x, const void* ids, const void* weights, const void* codes_gate,
+                      const void* scales_gate, const void* codes_up, const void* scales_up, const void* codes_down,
+                      const void* scales_down, void* y, int64_t inner, int64_t k, int64_t experts, int64_t top_k,
+                      int64_t t, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!moe_shape_ok(inner, k, experts, top_k, t)) return Q4LIN_E_SHAPE;
+  if (t == 0) return Q4LIN_OK;
+  const void* const planes[6] = {codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down};
+  const int st = check_experts(x, ids, weights, planes, y, workspace, workspace_bytes,
+                               q4lin::moe_workspace_bytes(inner, k, experts, top_k, t));
+  if (st != Q4LIN_OK) return st;
+  const q4lin::MoeArgs a{x, nullptr, const_cast<void*>(ids), const_cast<void*>(weights), codes_gate, scales_gate,
+                         codes_up, scales_up, codes_down, scales_down, y, inner, k, experts, top_k, t, 0};
+  const hipError_t e = q4lin::launch_moe_experts(a, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int q4lin_moe(const void* x, const void* router, const void* codes_gate, const void* scales_gate,
+              const void* codes_up, const void* scales_up, const void* codes_down, const void* scales_down, void* y,
+              void* ids, void* weights, int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t,
+              int renormalize, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!moe_shape_ok(inner, k, experts, top_k, t) || !route_shape_ok(k, experts, top_k, t)) return Q4LIN_E_SHAPE;
+  if (t == 0) return Q4LIN_OK;
+  if (!router) return Q4LIN_E_NULL;
+  if (!aligned(router, 16)) return Q4LIN_E_ALIGN;
+  const void* const planes[6] = {codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down};
+  const int st = check_experts(x, ids, weights, planes, y, workspace, workspace_bytes,
+                               q4lin::moe_workspace_bytes(inner, k, experts, top_k, t));
+  if (st != Q4LIN_OK) return st;
+  const q4lin::MoeArgs a{x, router, ids, weights, codes_gate, scales_gate, codes_up, scales_up, codes_down,
+                         scales_down, y, inner, k, experts, top_k, t, renormalize ? 1 : 0};
+  hipError_t e = q4lin::launch_moe_route(a, static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) e = q4lin::launch_moe_experts(a, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
 const char* q4lin_status_string(int status) {
   switch (status) {
     case Q4LIN_OK: return "ok";
@@ -529,6 +703,6 @@ const char* q4lin_status_string(int status) {
   }
 }
 
-int q4lin_version(void) { return 220; }
+int q4lin_version(void) { return 300; }
 
 }  // extern "C"

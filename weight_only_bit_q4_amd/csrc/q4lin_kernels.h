@@ -201,4 +201,45 @@ struct FmtPlan {
 bool fmt_plan(int fmt, int64_t n, int64_t k, int64_t t, FmtPlan* p, bool glu = false);
 hipError_t launch_fmt(const FmtArgs& a, hipStream_t stream);
 
+// Low-rank adapters beside a projection (q4lin_lora.hip).  a: bf16
+// [adapters][rank][k], b: bf16 [adapters][n][rank], scale: float [adapters]
+// (nullptr: ones), ids: int32 [t], the token's adapter or a number outside
+// 0..adapters-1 for none.
+struct LoraArgs {
+  const void* x;
+  const void* a;
+  const void* b;
+  const void* scale;
+  const void* ids;
+  void* y;
+  int64_t n, k, t, adapters, rank;
+};
+// bytes of u, the tokens' rank values in parts of a K split
+size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank, int64_t adapters);
+hipError_t launch_lora_shrink(const LoraArgs& a, float* u, hipStream_t stream);
+// y = bf16(base + s B u)
+hipError_t launch_lora_finish(const LoraArgs& a, const float* u, const SumSource& base, hipStream_t stream);
+
+// A mixture-of-experts layer with Q4 experts (q4lin_moe.hip): gate and up
+// [experts][inner][k], down [experts][k][inner], each as its codes and
+// scales planes; ids int32 and weights float [t][top_k].
+struct MoeArgs {
+  const void* x;
+  const void* router;  // bf16 [experts][k] (launch_moe_route)
+  void* ids;
+  void* weights;
+  const void* codes_gate;
+  const void* scales_gate;
+  const void* codes_up;
+  const void* scales_up;
+  const void* codes_down;
+  const void* scales_down;
+  void* y;
+  int64_t inner, k, experts, top_k, t;
+  int renorm;
+};
+hipError_t launch_moe_route(const MoeArgs& a, hipStream_t stream);
+size_t moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t);
+hipError_t launch_moe_experts(const MoeArgs& a, void* workspace, hipStream_t stream);
+
 }  // namespace q4lin

@@ -288,7 +288,7 @@ Q4LIN_API int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int6
  * nothing, a token without a valid id gets zeros, and an expert that a token
  * names twice counts twice.  The sums are binary32 or wider, h keeps 16
  * significant bits, y is rounded once.  The weights of an expert are read
- * once for up to 32 of its tokens.
+ * once for up to 32 (down: 16) of its tokens.
  *
  * K and inner: positive multiples of 64; 1 <= experts <= 1024; 1 <= top_k <=
  * experts; T K 2 bytes, 4 T top_k inner bytes and T top_k K each below 2^31.  workspace (not for q4lin_moe_route):

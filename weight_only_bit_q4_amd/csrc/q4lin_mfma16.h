@@ -19,6 +19,31 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // a buffer offset past every range
 
+// 16 bytes per lane from memory straight into LDS, lane l to lds_base + 16 l
+// (lds_base wave-uniform)
+__device__ __forceinline__ void dma16(rsrc_t r, uint32_t voffset, uint32_t soffset, void* lds_base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 16, voffset,
+                                           soffset, 0, 0);
+}
+
+// waits until at most N of the wave's loads are outstanding (gfx9 encoding:
+// vmcnt bits 3:0 and 15:14, expcnt 6:4 and lgkmcnt 11:8 left at "no wait");
+// until its LDS operations are done
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N <= 63, "vmcnt holds 0..63");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (((N >> 4) & 3) << 14) | (7 << 4) | (15 << 8));
+}
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (7 << 4)); }
+
+// the value of the lane at byte address src4 (four times its number)
+__device__ __forceinline__ u32x4_t lane_piece(u32x4_t v, int src4) {
+  return u32x4_t{(uint32_t)__builtin_amdgcn_ds_bpermute(src4, (int)v.x),
+                 (uint32_t)__builtin_amdgcn_ds_bpermute(src4, (int)v.y),
+                 (uint32_t)__builtin_amdgcn_ds_bpermute(src4, (int)v.z),
+                 (uint32_t)__builtin_amdgcn_ds_bpermute(src4, (int)v.w)};
+}
+
 // D = A B + C on one wave, K = 32.  Lane l = 16 q + i holds row i of A and
 // column i of B, both at k = 8 q .. 8 q + 7; D: column i, rows 4 q .. 4 q + 3.
 __device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c) {

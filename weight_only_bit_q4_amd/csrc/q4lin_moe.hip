@@ -12,16 +12,16 @@
 // whose id is outside 0..E-1 takes part in nothing.
 //
 // Expert products, bound by the weight stream (34 bytes per 64 weights of
-// each expert that some token chose, read once for up to 16 NT pairs): a
-// workgroup takes 32 rows of one expert (16 gate rows and the same 16 up
-// rows, or 32 down rows), all of its pairs, and its eight waves split K; no
-// loop over experts, so the chip's workgroups are (rows / 32) x experts and
-// the loads of many resident workgroups cover each other's latency.  The
-// arithmetic is that of the library's other matrix-core routes: exact bf16
-// values 128 + q, products of a constant all-8 operand through the same
-// instructions subtracted, the group's scale applied in binary32; the eight
-// waves' partials are summed in binary64.  h is kept as two bf16 parts (16
-// significant bits): one bf16 would cost as much precision as the store of y.
+// each expert that some token chose, read once for up to 32 activation
+// rows): a wave takes 64 rows of one expert (32 gate rows and the same 32 up
+// rows, or 64 down rows) and all of its pairs, and streams its share of K
+// through an LDS ring; the four waves of a workgroup share K or the rows.
+// The arithmetic is that of the library's other matrix-core routes: exact
+// bf16 values 128 + q, products of a constant all-8 operand through the same
+// instructions subtracted, the group's scale applied in binary32; the waves'
+// partials are summed in binary64.  h is kept as two bf16 parts (16
+// significant bits), as two activation rows per pair: one bf16 would cost as
+// much precision as the store of y.
 #include "q4lin_kernels.h"
 #include "q4lin_mfma16.h"
 
@@ -114,7 +114,7 @@ moe_route_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ ro
 // ---------------------------------------------------------------------------
 // Expert products
 // ---------------------------------------------------------------------------
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 // up to this many pairs the grid has a row of workgroups per pair (that of
 // an expert's first pair works), beyond it one per expert
@@ -122,7 +122,7 @@ constexpr int kPairGrid = 64;
 
 // Code dword w (k0..k7) -> exact bf16 128 + q in natural order: byte b gives
 // its low nibble and, through w >> 4, its high nibble
-__device__ __forceinline__ u32x4_t q4_operand(uint32_t w) {
+__device__ __forceinline__ u32x4_t q4_natural(uint32_t w) {
   const uint32_t u = w >> 4;
   u32x4_t r;
   r.x = and_or(__builtin_amdgcn_perm(u, w, 0x04040000u), 0x000F000Fu, 0x43004300u);
@@ -131,215 +131,375 @@ __device__ __forceinline__ u32x4_t q4_operand(uint32_t w) {
   r.w = and_or(__builtin_amdgcn_perm(u, w, 0x07070303u), 0x000F000Fu, 0x43004300u);
   return r;
 }
+// the same in the order k0 k4 k1 k5 k2 k6 k3 k7 (two instructions fewer):
+// for activations that were written in that order
+__device__ __forceinline__ u32x4_t q4_paired(uint32_t w) {
+  return u32x4_t{and_or(w, 0x000F000Fu, 0x43004300u), and_or(w >> 4, 0x000F000Fu, 0x43004300u),
+                 and_or(w >> 8, 0x000F000Fu, 0x43004300u), and_or(w >> 12, 0x000F000Fu, 0x43004300u)};
+}
+// place of value k (0..7) in that order
+__device__ __forceinline__ int paired_place(int k) { return k < 4 ? 2 * k : 2 * k - 7; }
 
-// What a wave loads for one unit (128 k, two scale groups): the codes and
-// scales of its two 16-row tiles, the activations of its 16 NT pairs
-template <int NT, bool DOWN>
-struct Unit {
-  static constexpr int XP = DOWN ? 4 : 2;  // 16-byte pieces of activations per group
-  u32x4_t c[2];
-  uint16_t s[2];
-  u32x4_t x[NT][2][XP];
+// Loads before it are issued before loads after it, so that a wait for one
+// stage's loads need not wait for those of the stage behind it
+__device__ __forceinline__ void in_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// bf16 values k0..k7 into the paired order
+__device__ __forceinline__ u32x4_t to_paired(u32x4_t v) {
+  return u32x4_t{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                 __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+}
+
+// The K loop works in stages of 256 k (four scale groups), two in flight.
+// What a wave holds of a stage: the codes of its R row tiles (16 weight rows
+// each) in its LDS ring, the activations of its activation tiles and the
+// rows' scales in registers.
+//   * Codes: eight lanes copy 128 bytes of one row (a load in which
+//     neighbouring lanes take different rows occupies the address unit
+//     several times as long); piece p of row i lies at 16-byte position
+//     8 i + (p ^ (i & 7)), so that the sixteen rows of an operand read
+//     spread over the banks.
+//   * Scales: every second stage lane r loads the eight of the wave's row r,
+//     16 bytes from the dword that holds the first, and the dword behind
+//     them where rows of an odd number of groups start in the middle of one.
+//   * Activations, GP = 1 (NT tiles of 16 activation rows): four lanes load
+//     from one row; a lane exchange hands them over.
+//   * Activations, GP = 2 or 4 (at most 8 or 4 activation rows): a tile's 16
+//     rows are those rows times GP scale groups, zero but for the products
+//     of the own group.  A product of GP groups' codes with such operands
+//     keeps the groups' sums apart in different rows of one accumulator, so
+//     that the scales (lane l: row l % 16, the group of its accumulator
+//     rows) cost one multiplication for GP groups.
+constexpr int kTileStage = 16 * 128;  // code bytes of a row tile in a stage
+
+template <int NT, int GP>
+struct Acts {
+  u32x4_t v[NT][8 / GP];
+};
+template <bool DOWN>
+struct Scales {
+  u32x4_t v[DOWN ? 1 : 2];
+  uint32_t next[DOWN ? 1 : 2];
 };
 
 // Gate and up (DOWN false): act = x, codes[0]/[1] the gate and up weights,
-// out = h in two parts [pair][rows / 8][hi 8 | lo 8].  Down: act = h,
-// codes[0] the down weight (the workgroup's rows 0..15 and 16..31), out
-// float [pair][rows].  K: the inner dimension of this product, rows: the
-// rows of one expert.
-template <int NT, bool DOWN>
-__global__ void __launch_bounds__(kThreads)
-moe_expert_kernel(const uint16_t* __restrict__ act, const uint8_t* __restrict__ codes0,
-                  const uint16_t* __restrict__ scales0, const uint8_t* __restrict__ codes1,
-                  const uint16_t* __restrict__ scales1, const int* __restrict__ ids, void* __restrict__ out, int K,
-                  int rows, int E, int P, int top_k, uint32_t act_bytes) {
-  using U = Unit<NT, DOWN>;
-  constexpr int BT = 16 * NT;  // pairs per pass
-  __shared__ float red[kWaves][2][16][20];
+// out = h in two parts, [pair][part][rows] in the paired order.  Down: act =
+// h, codes0 the down weight, out float [pair][rows].  K: the inner dimension
+// of this product, rows: the rows of one expert, wk: waves that share K (the
+// other kWaves / wk share the workgroup's rows).
+template <int R, bool DOWN>
+__global__ void __launch_bounds__(kThreads, 2)
+moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
+                  const uint16_t* scales1, const int* __restrict__ ids, void* out, int K, int rows, int E, int P,
+                  int top_k, uint32_t act_bytes, int wk) {
+  constexpr int RP = DOWN ? 2 : 1;       // activation rows per pair
+  constexpr int BT = 32 / RP;            // pairs per pass, at most
+  constexpr int RT = DOWN ? R : R / 2;   // row tiles of the output per wave
+  constexpr int SLOT = R * kTileStage;   // bytes of one stage's codes
+  typedef float Red[R][16][20];
+  static_assert(sizeof(Red) <= (size_t)SLOT, "the waves' sums reuse a ring slot");
+  // the rings' two slots (two objects, so that a read of one is known not to
+  // depend on a copy in flight into the other)
+  __shared__ __attribute__((aligned(16))) uint8_t ring0[kWaves * SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t ring1[kWaves * SLOT];
   __shared__ int list[kWaves][BT];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
+  const int wr = kWaves / wk, kp = wave % wk, rp = wave / wk;
 
-  // this workgroup's expert and how many pairs chose it
-  int e, m = 0;
-  uint64_t mask = 0;
+  int e = blockIdx.y;
   if (P <= kPairGrid) {
     const int id = lane < P ? ids[lane] : -1;
     e = __builtin_amdgcn_readlane(id, blockIdx.y);
     if ((uint32_t)e >= (uint32_t)E) return;
-    mask = __builtin_amdgcn_ballot_w64(id == e);
+    const uint64_t mask = __builtin_amdgcn_ballot_w64(id == e);
     if ((mask & ((1ull << blockIdx.y) - 1)) != 0) return;  // an earlier pair's workgroups serve it
-    m = __builtin_popcountll(mask);
-  } else {
-    e = blockIdx.y;
-    for (int p = 0; p < P; p += 64)
-      m += __builtin_popcountll(__builtin_amdgcn_ballot_w64(p + lane < P && ids[p + lane] == e));
-    if (m == 0) return;
   }
 
-  const int n0 = blockIdx.x * (DOWN ? 32 : 16);
-  const int G = K >> 6, units = (G + 1) >> 1;
-  const int ub = units * wave / kWaves, ue = units * (wave + 1) / kWaves;
+  const int n0 = (blockIdx.x * wr + rp) * (16 * RT);  // this wave's first output row
+  const int G = K >> 6, stages = (G + 3) >> 2;
+  const int sb = stages * kp / wk, se = stages * (kp + 1) / wk;
   const uint32_t crow = (uint32_t)K >> 1, srow = (uint32_t)G * 2;
-  const size_t r0 = (size_t)e * rows + n0, r1 = DOWN ? r0 + 16 : r0;
-  const rsrc_t rc0 = make_rsrc(codes0 + r0 * crow, 16 * crow), rc1 = make_rsrc(codes1 + r1 * crow, 16 * crow);
-  const rsrc_t rs0 = make_rsrc(scales0 + r0 * G, 16 * srow), rs1 = make_rsrc(scales1 + r1 * G, 16 * srow);
-  const rsrc_t rx = make_rsrc(act, act_bytes), rnull = make_rsrc(act, 0u);
-  const uint32_t c_off = (uint32_t)li * crow + 16u * lq;
-  const uint32_t s_off = (uint32_t)li * srow + 2u * (lq & 1);
-  // first activation of this lane in a group (the order that the exchange
-  // of code halves in unit_products gives), in bytes
-  constexpr int XB = DOWN ? 4 : 2;
-  const uint32_t x_in = (uint32_t)(32 * (lq & 1) + 16 * (lq >> 1)) * XB;
+  rsrc_t rc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int t0 = n0 + 16 * (r % RT);
+    // (rows are multiples of 16: a tile is whole or absent)
+    rc[r] = make_rsrc((r < RT ? codes0 : codes1) + ((size_t)e * rows + t0) * crow, t0 < rows ? 16u * crow : 0u);
+  }
+  const rsrc_t rx = make_rsrc(act, act_bytes);
+  const uint32_t c_off = (uint32_t)(lane >> 3) * crow + 16u * ((lane & 7) ^ (lane >> 3));
+  // the scales of row `lane` of the wave's 16 R rows: relative to the dword
+  // that holds the first of the wave's rows in its plane
+  const int srows = min(16 * RT, rows - n0);
+  const bool mine0 = lane < srows, mine1 = !DOWN && lane >= 16 * RT && lane - 16 * RT < srows;
+  const size_t s0 = ((size_t)e * rows + n0) * G;
+  const uintptr_t sa0 = reinterpret_cast<uintptr_t>(scales0 + s0), sa1 = reinterpret_cast<uintptr_t>(scales1 + s0);
+  const uint32_t skew0 = (uint32_t)(sa0 & 2), skew1 = (uint32_t)(sa1 & 2);
+  const rsrc_t rs0 = make_rsrc(reinterpret_cast<const void*>(sa0 - skew0),
+                               srows > 0 ? (skew0 + (uint32_t)srows * srow + 3u) & ~3u : 0u);
+  const rsrc_t rs1 = make_rsrc(reinterpret_cast<const void*>(sa1 - skew1),
+                               srows > 0 ? (skew1 + (uint32_t)srows * srow + 3u) & ~3u : 0u);
+  const uint32_t so0 = skew0 + (uint32_t)lane * srow, so1 = skew1 + (uint32_t)(lane - 16 * RT) * srow;
+  const uint32_t s_off0 = mine0 ? so0 & ~3u : kNowhere, s_off1 = mine1 ? so1 & ~3u : kNowhere;
+  const uint32_t s_shift = ((mine1 ? so1 : so0) & 2) * 8;
+  const bool skewed = (G & 1) != 0 || skew0 != 0 || skew1 != 0;
 
-  for (int b0 = 0; b0 < m; b0 += BT) {
-    // pairs b0 .. b0 + BT - 1 of the expert, in order (each wave its own copy)
-    if (P <= kPairGrid) {
-      const int r = __builtin_popcountll(mask & ((1ull << lane) - 1)) - b0;
-      if (((mask >> lane) & 1) != 0 && r >= 0 && r < BT) list[wave][r] = lane;
-    } else {
-      int seen = -b0;
-      for (int p = 0; p < P && seen < BT; p += 64) {
-        const bool hit = p + lane < P && ids[p + lane] == e;
-        const uint64_t bm = __builtin_amdgcn_ballot_w64(hit);
-        const int r = seen + __builtin_popcountll(bm & ((1ull << lane) - 1));
-        if (hit && r >= 0 && r < BT) list[wave][r] = p + lane;
-        seen += __builtin_popcountll(bm);
-      }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const int mb = min(BT, m - b0);
+  int rd[4];  // this lane's 8 code bytes of group g in a slot: row li, byte 32 g + 8 lq of a tile
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    rd[g] = wave * SLOT + li * 128 + 16 * ((2 * g + (lq >> 1)) ^ (li & 7)) + 8 * (lq & 1);
+  const int xsrc4 = (4 * li + lq) * 4;  // the lane holding this lane's activations after an exchange (byte address)
+
+  // One pass over the wave's share of K for the mr activation rows of the
+  // list, then the workgroup's sums
+  auto pass = [&](auto ntc, auto gpc, int mr) __device__ {
+    constexpr int NT = decltype(ntc)::value, GP = decltype(gpc)::value;
+    static_assert(GP == 1 || NT == 1, "packed groups take one tile");
+    constexpr int MT = 16 / GP;                 // activation rows of a tile
+    constexpr int LOADS = 2 * R + NT * 8 / GP;  // of one stage, the scales not counted
+    constexpr bool PAIRED = DOWN || NT == 1;    // code order of the products (x is permuted into it up to one tile)
     uint32_t x_off[NT];
-#pragma unroll
+  #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int p = list[wave][min(16 * nt + li, mb - 1)];  // places past the last repeat it and are not stored
-      x_off[nt] = (uint32_t)(DOWN ? p : p / top_k) * (uint32_t)K * XB + x_in;
+      const int a = GP == 1 ? 16 * nt + (lane >> 2) : li % MT;
+      const int p = list[wave][min(a, mr - 1) / RP];
+      const uint32_t row = DOWN ? 2u * p + (a & 1) : (uint32_t)(p / top_k);
+      // (rows past the last read as zeros)
+      x_off[nt] = a < mr ? row * (uint32_t)K * 2u + (GP == 1 ? 32u * (lane & 3) : 32u * lq + 128u * (li / MT)) : kNowhere;
     }
+    f32x4_t acc[NT][R];
+  #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+  #pragma unroll
+      for (int r = 0; r < R; ++r) acc[nt][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    f32x4_t acc[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    auto load = [&](U& L, int u) {
-      const bool live = u < ue;
-      L.c[0] = __builtin_amdgcn_raw_buffer_load_b128(live ? rc0 : rnull, c_off + 64u * u, 0, 0);
-      L.c[1] = __builtin_amdgcn_raw_buffer_load_b128(live ? rc1 : rnull, c_off + 64u * u, 0, 0);
-      // (the second group of an odd K's last unit does not exist: its scale
-      // is another row's and is not used)
-      L.s[0] = __builtin_amdgcn_raw_buffer_load_b16(live ? rs0 : rnull, s_off + 4u * u, 0, 0);
-      L.s[1] = __builtin_amdgcn_raw_buffer_load_b16(live ? rs1 : rnull, s_off + 4u * u, 0, 0);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const rsrc_t r = live && 2 * u + g < G ? rx : rnull;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < U::XP; ++i)
-            L.x[nt][g][i] = __builtin_amdgcn_raw_buffer_load_b128(r, x_off[nt], (uint32_t)(128 * u + 64 * g) * XB + 16u * i, 0);
+    // (a stage past the wave's share and groups past K: offsets past every
+    // range, which read as zeros)
+    auto load_scales = [&](Scales<DOWN>& L, int s) __device__ {
+      const uint32_t away = s < se ? 0u : kNowhere;
+      const uint32_t o0 = (s_off0 + 8u * (uint32_t)s) | away, o1 = (s_off1 + 8u * (uint32_t)s) | away;
+      L.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rs0, o0, 0, 0);
+      if constexpr (!DOWN) L.v[1] = __builtin_amdgcn_raw_buffer_load_b128(rs1, o1, 0, 0);
+      if (skewed) {
+        L.next[0] = __builtin_amdgcn_raw_buffer_load_b32(rs0, o0 + 16, 0, 0);
+        if constexpr (!DOWN) L.next[1] = __builtin_amdgcn_raw_buffer_load_b32(rs1, o1 + 16, 0, 0);
+      }
+      in_order();
+    };
+    auto load = [&](Acts<NT, GP>& L, uint8_t* ring, int s) __device__ {
+      const uint32_t away = s < se ? 0u : kNowhere;
+  #pragma unroll
+      for (int r = 0; r < R; ++r)
+  #pragma unroll
+        for (int h = 0; h < 2; ++h)
+          dma16(rc[r], (c_off + 8u * h * crow + 128u * (uint32_t)s) | away, 0,
+                ring + wave * SLOT + (2 * r + h) * (kTileStage / 2));
+      in_order();
+  #pragma unroll
+      for (int g = 0; g < 4 / GP; ++g) {
+        const uint32_t away_g = s < se && 4 * s + GP * g + (GP == 1 ? 0 : li / MT) < G ? 0u : kNowhere;
+  #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t o = (x_off[nt] + 512u * (uint32_t)s) | away_g;
+          L.v[nt][2 * g] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g, 0, 0);
+          L.v[nt][2 * g + 1] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g + 16, 0, 0);
+        }
+      }
+      in_order();
+    };
+    // the scales of row `lane`, groups 8 s2 .. 8 s2 + 7 of the wave's share, two a dword
+    auto row_scales = [&](const Scales<DOWN>& L, int s, uint32_t (&d)[4]) __device__ {
+      u32x4_t v = L.v[0];
+      if constexpr (!DOWN) v = v | L.v[1];
+      if (skewed) {
+        const uint32_t n = DOWN ? L.next[0] : L.next[0] | L.next[1 % (DOWN ? 1 : 2)];
+        v = u32x4_t{__builtin_amdgcn_alignbit(v.y, v.x, s_shift), __builtin_amdgcn_alignbit(v.z, v.y, s_shift),
+                    __builtin_amdgcn_alignbit(v.w, v.z, s_shift), __builtin_amdgcn_alignbit(n, v.w, s_shift)};
+      }
+  #pragma unroll
+      for (int i = 0; i < 4; ++i) {  // (groups past K belong to another row)
+        const int left = G - 4 * s - 2 * i;
+        d[i] = v[i] & (left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0xFFFFu : 0u);
       }
     };
-    auto compute = [&](const U& L, int u) {
+    auto compute = [&](const Acts<NT, GP>& L, const uint8_t* ring, uint32_t d0, uint32_t d1, int s) __device__ {
       const u32x4_t eights = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
       const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-      // lanes l and l + 32 exchange half of their 16 code bytes: then every
-      // lane holds 8 code bytes of each group; a scale row of 16 lanes holds
-      // one group, and the row swap gives every lane both
-      uint32_t cw[2][2][2];  // [tile][group][dword]
-      float sv[2][2];        // [tile][group]
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const auto sx = __builtin_amdgcn_permlane32_swap(L.c[i].x, L.c[i].z, false, false);
-        const auto sy = __builtin_amdgcn_permlane32_swap(L.c[i].y, L.c[i].w, false, false);
-        cw[i][0][0] = sx[0];
-        cw[i][0][1] = sy[0];
-        cw[i][1][0] = sx[1];
-        cw[i][1][1] = sy[1];
-        const uint32_t f = __builtin_bit_cast(uint32_t, f16_bits_to_f32(L.s[i]));
-        const auto ss = __builtin_amdgcn_permlane16_swap(f, f, false, false);
-        const uint32_t s0 = ss[0], s1 = ss[1];
-        sv[i][0] = __builtin_bit_cast(float, s0);
-        sv[i][1] = __builtin_bit_cast(float, s1);
+      uint32_t sc[R][2];
+  #pragma unroll
+      for (int r = 0; r < R; ++r) {
+        sc[r][0] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d0);
+        sc[r][1] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d1);
       }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g == 1 && 2 * u + 1 >= G) break;
-        u32x4_t w[2][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          w[i][0] = q4_operand(cw[i][g][0]);
-          w[i][1] = q4_operand(cw[i][g][1]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          auto product = [&](u32x4_t b0v, u32x4_t b1v) {
-            f32x4_t p;
-            if constexpr (DOWN) {
-              p = mfma(L.x[nt][g][0], b0v, zero);
-              p = mfma(L.x[nt][g][2], b1v, p);
-              p = mfma(L.x[nt][g][1], b0v, p);
-              p = mfma(L.x[nt][g][3], b1v, p);
-            } else {
-              p = mfma(L.x[nt][g][0], b0v, zero);
-              p = mfma(L.x[nt][g][1], b1v, p);
+      auto codes = [&](int r, int g, u32x4_t (&w)[2]) __device__ {
+        const u32x2_t cw = *reinterpret_cast<const u32x2_t*>(ring + rd[g] + r * kTileStage);
+        w[0] = PAIRED ? q4_paired(cw.x) : q4_natural(cw.x);
+        w[1] = PAIRED ? q4_paired(cw.y) : q4_natural(cw.y);
+      };
+      if constexpr (GP == 1) {
+  #pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g > 0 && 4 * s + g >= G) break;
+          u32x4_t x[NT][2];
+          f32x4_t cr[NT];
+  #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+  #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[nt][h] = lane_piece(L.v[nt][2 * g + h], xsrc4);
+              if constexpr (PAIRED && !DOWN) x[nt][h] = to_paired(x[nt][h]);
             }
-            return p;
-          };
-          const f32x4_t cr = product(eights, eights);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const f32x4_t p = product(w[i][0], w[i][1]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[nt][i][r] = __builtin_fmaf(sv[i][g], p[r] - cr[r], acc[nt][i][r]);
+            cr[nt] = mfma(x[nt][0], eights, zero);
+            cr[nt] = mfma(x[nt][1], eights, cr[nt]);
+          }
+  #pragma unroll
+          for (int r = 0; r < R; ++r) {
+            u32x4_t w[2];
+            codes(r, g, w);
+            const uint32_t sb16 = (g & 1) ? sc[r][g >> 1] >> 16 : sc[r][g >> 1] & 0xFFFFu;
+            const float sv = f16_bits_to_f32((uint16_t)sb16);
+  #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              f32x4_t p = mfma(x[nt][0], w[0], zero);
+              p = mfma(x[nt][1], w[1], p);
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) acc[nt][r][i] = __builtin_fmaf(sv, p[i] - cr[nt][i], acc[nt][r][i]);
+            }
+          }
+        }
+      } else {
+  #pragma unroll
+        for (int g = 0; g < 4 / GP; ++g) {
+          u32x4_t x[GP][2];
+          f32x4_t cr = zero;
+  #pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x4_t v = DOWN ? L.v[0][2 * g + h] : to_paired(L.v[0][2 * g + h]);
+  #pragma unroll
+            for (int j = 0; j < GP; ++j)
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) x[j][h][i] = li / MT == j ? v[i] : 0u;
+          }
+  #pragma unroll
+          for (int j = 0; j < GP; ++j) {
+            cr = mfma(x[j][0], eights, cr);
+            cr = mfma(x[j][1], eights, cr);
+          }
+          const int own = GP * g + 4 * lq / MT;  // the group of this lane's accumulator rows
+  #pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const uint32_t sd = GP == 4 ? (lq >> 1 ? sc[r][1] : sc[r][0]) : sc[r][g];
+            const float sv = f16_bits_to_f32((uint16_t)((own & 1) ? sd >> 16 : sd));
+            f32x4_t p = zero;
+  #pragma unroll
+            for (int j = 0; j < GP; ++j) {
+              u32x4_t w[2];
+              codes(r, GP * g + j, w);
+              p = mfma(x[j][0], w[0], p);
+              p = mfma(x[j][1], w[1], p);
+            }
+  #pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][r][i] = __builtin_fmaf(sv, p[i] - cr[i], acc[0][r][i]);
           }
         }
       }
     };
-    U L0, L1;
-    load(L0, ub);
-    load(L1, ub + 1);
-    for (int u = ub; u < ue; u += 2) {
-      compute(L0, u);
-      load(L0, u + 2);
-      if (u + 1 < ue) compute(L1, u + 1);
-      load(L1, u + 3);
+    Acts<NT, GP> L[2];
+    Scales<DOWN> S;
+    load_scales(S, sb);
+    load(L[0], ring0, sb);
+    load(L[1], ring1, sb + 1);
+    // the stage's copies have landed when only the next stage's loads are
+    // outstanding; a slot's reads are done before it is written again
+    for (int s = sb; s < se; s += 2) {
+      wait_vm<LOADS>();
+      in_order();
+      uint32_t d[4];
+      row_scales(S, s, d);
+      compute(L[0], ring0, d[0], d[1], s);
+      wait_lgkm0();
+      in_order();
+      load_scales(S, s + 2);
+      load(L[0], ring0, s + 2);
+      wait_vm<LOADS>();
+      in_order();
+      if (s + 1 < se) compute(L[1], ring1, d[2], d[3], s + 1);
+      wait_lgkm0();
+      in_order();
+      load(L[1], ring1, s + 3);
     }
+    wait_vm<0>();  // (nothing lands in the rings any more)
+    in_order();
 
-    // the eight waves' sums
-#pragma unroll
+    // the sums of the waves that share K (and of a tile's groups)
+  #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (16 * nt >= mb) break;
+      if (MT * nt >= mr) break;
+      if (nt > 0) __syncthreads();
+      Red& red = *reinterpret_cast<Red*>(ring0 + wave * SLOT);
+      if (MT * nt + 4 * lq % MT < mr)
+  #pragma unroll
+        for (int r = 0; r < R; ++r)
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) red[r][4 * lq + i][li] = acc[nt][r][i];
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave][i][4 * lq + r][li] = acc[nt][i][r];
-      __syncthreads();
-      const int t = (tid >> 4) & 15, c = tid & 15;
-      if (16 * nt + t < mb && (DOWN || tid < 256)) {
-        const int p = list[wave][16 * nt + t];
-        if constexpr (DOWN) {
-          const int i = tid >> 8;
+      const int tiles = wr * RT, pairs = min(MT, mr - MT * nt) / RP;
+      for (int o = tid; o < 16 * tiles * pairs; o += kThreads) {
+        const int c = o & 15, tile = (o >> 4) % tiles, t = (o >> 4) / tiles;
+        const int w0 = tile / RT * wk, r = tile % RT, n = (blockIdx.x * tiles + tile) * 16 + c;
+        if (n >= rows) continue;
+        const int p = list[wave][MT / RP * nt + t];
+        auto sum = [&](int rr, int tt) __device__ {
           double v = 0.0;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) v += (double)red[w][i][t][c];
-          static_cast<float*>(out)[(size_t)p * rows + n0 + 16 * i + c] = (float)v;
+          for (int w = 0; w < wk; ++w)
+  #pragma unroll
+            for (int j = 0; j < GP; ++j)
+              v += (double)(*reinterpret_cast<const Red*>(ring0 + (w0 + w) * SLOT))[rr][MT * j + tt][c];
+          return v;
+        };
+        if constexpr (DOWN) {
+          static_cast<float*>(out)[(size_t)p * rows + n] = (float)(sum(r, 2 * t) + sum(r, 2 * t + 1));
         } else {
-          double gv = 0.0, uv = 0.0;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
-            gv += (double)red[w][0][t][c];
-            uv += (double)red[w][1][t][c];
-          }
-          const float g = (float)gv;
+          const float g = (float)sum(r, t);
           uint32_t hi, lo;
-          split_bf16(g / (1.0f + expf(-g)) * (float)uv, hi, lo);
-          uint16_t* o = static_cast<uint16_t*>(out) + ((size_t)p * rows + ((n0 + c) & ~7)) * 2 + (c & 7);
-          o[0] = (uint16_t)hi;
-          o[8] = (uint16_t)lo;
+          split_bf16(g / (1.0f + expf(-g)) * (float)sum(RT + r, t), hi, lo);
+          uint16_t* o2 = static_cast<uint16_t*>(out) + (size_t)p * 2 * rows + (n & ~7) + paired_place(n & 7);
+          o2[0] = (uint16_t)hi;
+          o2[rows] = (uint16_t)lo;
         }
       }
     }
+  };
+
+  int m = 1;
+  for (int b0 = 0; b0 < m; b0 += BT) {
+    // pairs b0 .. b0 + BT - 1 of the expert, in order (each wave its own copy)
+    m = 0;
+    for (int p0 = 0; p0 < P; p0 += 512) {
+      int v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p0 + 64 * j + lane < P ? ids[p0 + 64 * j + lane] : -1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint64_t bm = __builtin_amdgcn_ballot_w64(v[j] == e);
+        const int r = m + __builtin_popcountll(bm & ((1ull << lane) - 1)) - b0;
+        if (v[j] == e && r >= 0 && r < BT) list[wave][r] = p0 + 64 * j + lane;
+        m += __builtin_popcountll(bm);
+      }
+    }
+    if (m == 0) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int mr = min(BT, m - b0) * RP;
+    // the smallest tiles that hold the rows
+    if (mr <= 4) pass(Slot<1>{}, Slot<4>{}, mr);
+    else if (mr <= 8) pass(Slot<1>{}, Slot<2>{}, mr);
+    else if (mr <= 16) pass(Slot<1>{}, Slot<1>{}, mr);
+    else pass(Slot<2>{}, Slot<1>{}, mr);
     __syncthreads();
   }
 }
@@ -375,19 +535,31 @@ moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids,
 
 size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-template <int NT>
-hipError_t launch_experts(const MoeArgs& a, uint16_t* h, float* parts, hipStream_t s) {
+constexpr int kRowTiles = 4;  // per wave
+
+template <bool DOWN>
+hipError_t launch_experts(const MoeArgs& a, void* h, float* parts, hipStream_t s) {
+  constexpr int R = kRowTiles, RT = DOWN ? R : R / 2;
   const int P = (int)(a.t * a.top_k);
   const unsigned slots = (unsigned)(P <= kPairGrid ? P : a.experts);
   const int* ids = static_cast<const int*>(a.ids);
   auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
-  moe_expert_kernel<NT, false><<<dim3((unsigned)(a.inner / 16), slots), dim3(kThreads), 0, s>>>(
-      u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up), ids, h, (int)a.k,
-      (int)a.inner, (int)a.experts, P, (int)a.top_k, (uint32_t)(a.t * a.k * 2));
-  moe_expert_kernel<NT, true><<<dim3((unsigned)(a.k / 32), slots), dim3(kThreads), 0, s>>>(
-      h, u8(a.codes_down), u16(a.scales_down), u8(a.codes_down), u16(a.scales_down), ids, parts, (int)a.inner,
-      (int)a.k, (int)a.experts, P, (int)a.top_k, (uint32_t)((int64_t)P * a.inner * 4));
+  const int64_t rows = DOWN ? a.k : a.inner;
+  // waves that share K: so many that about six waves per CU run (experts in
+  // use: at most one per pair)
+  const int64_t waves = rows / (16 * RT) * (P < a.experts ? P : a.experts);
+  const int wk = waves >= 1400 ? 1 : waves >= 700 ? 2 : 4;
+  const int64_t per = kWaves / wk * 16 * RT;
+  const dim3 grid((unsigned)((rows + per - 1) / per), slots);
+  if (DOWN)
+    moe_expert_kernel<R, true><<<grid, dim3(kThreads), 0, s>>>(
+        u16(h), u8(a.codes_down), u16(a.scales_down), u8(a.codes_down), u16(a.scales_down), ids, parts, (int)a.inner,
+        (int)rows, (int)a.experts, P, (int)a.top_k, (uint32_t)((int64_t)P * a.inner * 4), wk);
+  else
+    moe_expert_kernel<R, false><<<grid, dim3(kThreads), 0, s>>>(
+        u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up), ids, h, (int)a.k, (int)rows,
+        (int)a.experts, P, (int)a.top_k, (uint32_t)(a.t * a.k * 2), wk);
   return hipGetLastError();
 }
 
@@ -407,11 +579,10 @@ size_t moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t to
 }
 
 hipError_t launch_moe_experts(const MoeArgs& a, void* workspace, hipStream_t s) {
-  uint16_t* h = static_cast<uint16_t*>(workspace);
+  void* h = workspace;
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + al256((size_t)(a.t * a.top_k * a.inner * 4)));
-  // pairs per pass over an expert's rows: about the mean number of its pairs
-  const int64_t mean = a.t * a.top_k / a.experts;
-  const hipError_t e = mean <= 8 ? launch_experts<1>(a, h, parts, s) : launch_experts<2>(a, h, parts, s);
+  hipError_t e = launch_experts<false>(a, h, parts, s);
+  if (e == hipSuccess) e = launch_experts<true>(a, h, parts, s);
   if (e != hipSuccess) return e;
   const int64_t quads = a.t * (a.k / 4);
   const int vec = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;

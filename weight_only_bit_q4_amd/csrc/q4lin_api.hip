@@ -646,7 +646,7 @@ int q4lin_moe_route(const void* x, const void* router, void* ids, void* weights,
   a.top_k = top_k;
   a.t = t;
   a.renorm = renormalize ? 1 : 0;
-  const hipError_t e = q4lin::launch_moe_route(a, static_cast<hipStream_t>(stream));
+  const hipError_t e = q4lin::launch_moe_route(a, nullptr, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
 }
 
@@ -685,8 +685,7 @@ int q4lin_moe(const void* x, const void* router, const void* codes_gate, const v
   if (st != Q4LIN_OK) return st;
   const q4lin::MoeArgs a{x, router, ids, weights, codes_gate, scales_gate, codes_up, scales_up, codes_down,
                          scales_down, y, inner, k, experts, top_k, t, renormalize ? 1 : 0};
-  hipError_t e = q4lin::launch_moe_route(a, static_cast<hipStream_t>(stream));
-  if (e == hipSuccess) e = q4lin::launch_moe_experts(a, workspace, static_cast<hipStream_t>(stream));
+  const hipError_t e = q4lin::launch_moe(a, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
 }
 

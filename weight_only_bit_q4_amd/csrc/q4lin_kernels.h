@@ -238,8 +238,11 @@ struct MoeArgs {
   int64_t inner, k, experts, top_k, t;
   int renorm;
 };
-hipError_t launch_moe_route(const MoeArgs& a, hipStream_t stream);
+// with moe_route_workspace_bytes() of workspace, or none (slower on large routers)
+hipError_t launch_moe_route(const MoeArgs& a, void* workspace, hipStream_t stream);
+size_t moe_route_workspace_bytes(int64_t k, int64_t experts, int64_t t);
 size_t moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t);
 hipError_t launch_moe_experts(const MoeArgs& a, void* workspace, hipStream_t stream);
+hipError_t launch_moe(const MoeArgs& a, void* workspace, hipStream_t stream);
 
 }  // namespace q4lin

@@ -45,70 +45,185 @@ __device__ __forceinline__ float dot8(u32x4_t a, u32x4_t b) {
   return d;
 }
 
-// One workgroup per token.  The logits are sums of exact bf16 products,
-// eight at a time in binary32 and those in binary64, so that the order of
-// two experts is that of their exact logits but for differences near 2^-24
-// of the terms.  The rank of an expert is the number of experts before it,
-// counted by all threads; a NaN counts as the lowest.
+// Products of EPW rows of the router with TPW tokens over the k of one wave
+// (pieces of 8 from 8 (64 part + lane), 512 parts apart): exact bf16
+// products, eight at a time summed in binary32 and those in binary64, so
+// that the order of two experts is that of their exact logits but for
+// differences near 2^-24 of the terms.
+template <int EPW, int TPW>
+__device__ __forceinline__ void logit_sums(const uint16_t* const (&r)[EPW], const uint16_t* const (&x)[TPW], int K,
+                                           int part, int parts, int lane, double (&sum)[TPW][EPW]) {
+#pragma unroll
+  for (int t = 0; t < TPW; ++t)
+#pragma unroll
+    for (int i = 0; i < EPW; ++i) sum[t][i] = 0.0;
+#pragma unroll 4
+  for (int k = 8 * (64 * part + lane); k < K; k += 512 * parts) {
+    u32x4_t rv[EPW], xv[TPW];
+#pragma unroll
+    for (int i = 0; i < EPW; ++i) rv[i] = *reinterpret_cast<const u32x4_t*>(r[i] + k);
+#pragma unroll
+    for (int t = 0; t < TPW; ++t) xv[t] = *reinterpret_cast<const u32x4_t*>(x[t] + k);
+#pragma unroll
+    for (int t = 0; t < TPW; ++t)
+#pragma unroll
+      for (int i = 0; i < EPW; ++i) sum[t][i] += (double)dot8(rv[i], xv[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < TPW; ++t)
+#pragma unroll
+    for (int i = 0; i < EPW; ++i) sum[t][i] = sum64_lanes(sum[t][i]);
+}
+
+// One token's choice by a single wave, from its E logits.  An expert's key is
+// its logit's bits in an order-preserving form, the lowest eleven bits of the
+// fraction giving way to the expert's number (equals: the lowest first; a NaN
+// lowest).  Returns the expert of rank n - 1; with `chosen`, n numbers of LDS,
+// the whole choice of n experts is written to ids and weights.  E <= 64 B.
+__device__ __forceinline__ uint64_t max64_lanes(uint64_t v) {
+  auto step = [&](uint64_t o) __device__ { v = o > v ? o : v; };
+  auto dpp = [&](auto c) __device__ {
+    constexpr int C = decltype(c)::value;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, C, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), C, 0xF, 0xF, false);
+    return ((uint64_t)hi << 32) | lo;
+  };
+  step(dpp(Slot<0xB1>{}));
+  step(dpp(Slot<0x4E>{}));
+  step(dpp(Slot<0x141>{}));
+  step(dpp(Slot<0x140>{}));
+  auto rows = [&](const auto& l, const auto& h) __device__ {
+    const uint64_t a = ((uint64_t)h[0] << 32) | l[0], b = ((uint64_t)h[1] << 32) | l[1];
+    v = a > b ? a : b;
+  };
+  rows(__builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false),
+       __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false));
+  rows(__builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false),
+       __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false));
+  return v;
+}
+template <int B>
+__device__ __forceinline__ int choose_one(const double* lg, int E, int n, int lane, int renorm, int* chosen,
+                                          int* __restrict__ ids, float* __restrict__ weights) {
+  uint64_t key[B];  // of experts lane, lane + 64, ...
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const int i = 64 * b + lane;
+    const double l = lg[min(i, E - 1)];
+    const uint64_t u = __builtin_bit_cast(uint64_t, l);
+    const uint64_t o = l != l ? 0 : (u >> 63) ? ~u : u | 0x8000000000000000ull;
+    key[b] = i < E ? (o & ~2047ull) | (uint64_t)(64 * B - i) : 0;
+  }
+  int e = 0;
+  for (int j = 0; j < n; ++j) {
+    uint64_t best = key[0];
+#pragma unroll
+    for (int b = 1; b < B; ++b) best = key[b] > best ? key[b] : best;
+    best = max64_lanes(best);
+    e = 64 * B - (int)((uint32_t)best & 2047u);
+#pragma unroll
+    for (int b = 0; b < B; ++b) key[b] = key[b] == best ? 0 : key[b];
+    if (chosen != nullptr && lane == 0) chosen[j] = e;
+  }
+  if (chosen != nullptr) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    // the softmax runs over the chosen experts, or over all
+    const double top = lg[chosen[0]];
+    double sum = 0.0;
+    for (int i = lane; i < (renorm ? n : E); i += 64) sum += exp(lg[renorm ? chosen[i] : i] - top);
+    sum = sum64_lanes(sum);
+    for (int j = lane; j < n; j += 64) {
+      ids[j] = chosen[j];
+      weights[j] = (float)(exp(lg[chosen[j]] - top) / sum);
+    }
+  }
+  return e;
+}
+
+// Small routers: one workgroup per token makes the logits and the choice
 __global__ void __launch_bounds__(kRouteThreads)
 moe_route_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ router, int* __restrict__ ids,
                  float* __restrict__ weights, int K, int E, int top_k, int renorm) {
+  constexpr int kRouteWaves = kRouteThreads / 64;
   __shared__ double lg[kMaxExperts];
-  __shared__ int rank[kMaxExperts];
-  __shared__ double part[kRouteThreads / 64];
-  __shared__ double top;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ int chosen[kMaxExperts];
+  __shared__ double part[kRouteWaves][4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const size_t t = blockIdx.x;
-  const uint16_t* xr = x + t * K;
-  rank[tid] = 0;
-  for (int e0 = 4 * wave; e0 < E; e0 += 4 * (kRouteThreads / 64)) {
+  const uint16_t* xr[1] = {x + t * K};
+  // four experts a wave, the waves left over sharing their k
+  const int quads = (E + 3) / 4, parts = quads < kRouteWaves ? kRouteWaves / quads : 1;
+  for (int q = wave / parts; q < quads; q += kRouteWaves / parts) {
     const uint16_t* r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = router + (size_t)min(e0 + i, E - 1) * K;
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 2
-    for (int k = 8 * lane; k < K; k += 512) {
-      const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xr + k);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += (double)dot8(*reinterpret_cast<const u32x4_t*>(r[i] + k), xv);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const double s = sum64_lanes(acc[i]);
-      if (lane == 0 && e0 + i < E) lg[e0 + i] = s;
+    for (int i = 0; i < 4; ++i) r[i] = router + (size_t)min(4 * q + i, E - 1) * K;
+    double sum[1][4];
+    logit_sums<4, 1>(r, xr, K, wave % parts, parts, lane, sum);
+    if (lane < 4) {
+      const double v = lane == 0 ? sum[0][0] : lane == 1 ? sum[0][1] : lane == 2 ? sum[0][2] : sum[0][3];
+      if (parts > 1) part[wave][lane] = v;
+      else if (4 * q + lane < E) lg[4 * q + lane] = v;
     }
   }
-  __syncthreads();
-  // ranks: thread (part, e) counts the experts j = part, part + parts, ... before e
-  int ep = 64;
-  while (ep < E) ep <<= 1;
-  {
-    const int e = tid & (ep - 1), parts = kRouteThreads / ep;
+  if (parts > 1) {
+    __syncthreads();
+    const int e = threadIdx.x;
     if (e < E) {
-      const double le = lg[e], ke = le != le ? -__builtin_inf() : le;
-      int n = 0;
-      for (int j = tid / ep; j < E; j += parts) {
-        const double lj = lg[j], kj = lj != lj ? -__builtin_inf() : lj;
-        n += kj > ke || (kj == ke && j < e);
-      }
-      atomicAdd(&rank[e], n);  // (whole numbers: any order)
+      double v = 0.0;
+      for (int p = 0; p < parts; ++p) v += part[(e >> 2) * parts + p][e & 3];
+      lg[e] = v;
     }
   }
   __syncthreads();
-  const bool on = tid < E;
-  const int rk = on ? rank[tid] : kMaxExperts;
-  if (rk == 0) top = lg[tid];
+  if (wave != 0) return;
+  if (E <= 256) choose_one<4>(lg, E, top_k, lane, renorm, chosen, ids + t * top_k, weights + t * top_k);
+  else choose_one<kMaxExperts / 64>(lg, E, top_k, lane, renorm, chosen, ids + t * top_k, weights + t * top_k);
+}
+
+// Larger ones: the logits by waves over the whole chip, then the choices.
+// A wave takes EPW experts and TPW tokens; or (one_logit) a workgroup takes
+// one expert and one token, its four waves sharing K.
+__global__ void __launch_bounds__(256)
+moe_one_logit_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ router, double* __restrict__ lg,
+                     int K, int E) {
+  __shared__ double part[4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint16_t *r[1] = {router + (size_t)blockIdx.x * K}, *xr[1] = {x + (size_t)blockIdx.y * K};
+  double sum[1][1];
+  logit_sums<1, 1>(r, xr, K, wave, 4, lane, sum);
+  if (lane == 0) part[wave] = sum[0][0];
   __syncthreads();
-  const double pe = on && (rk < top_k || !renorm) ? exp(lg[tid] - top) : 0.0;
-  const double ps = sum64_lanes(pe);
-  if (lane == 0) part[wave] = ps;
-  __syncthreads();
-  if (rk < top_k) {
-    double sum = 0.0;
-    for (int w = 0; w < kRouteThreads / 64; ++w) sum += part[w];
-    ids[t * top_k + rk] = tid;
-    weights[t * top_k + rk] = (float)(pe / sum);
-  }
+  if (threadIdx.x == 0) lg[(size_t)blockIdx.y * E + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+template <int EPW, int TPW>
+__global__ void __launch_bounds__(256)
+moe_logits_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ router, double* __restrict__ lg, int K,
+                  int E, int T) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e0 = (blockIdx.x * 4 + wave) * EPW, t0 = blockIdx.y * TPW;
+  if (e0 >= E) return;
+  const uint16_t *r[EPW], *xr[TPW];
+#pragma unroll
+  for (int i = 0; i < EPW; ++i) r[i] = router + (size_t)min(e0 + i, E - 1) * K;
+#pragma unroll
+  for (int t = 0; t < TPW; ++t) xr[t] = x + (size_t)min(t0 + t, T - 1) * K;
+  double sum[TPW][EPW];
+  logit_sums<EPW, TPW>(r, xr, K, 0, 1, lane, sum);
+#pragma unroll
+  for (int t = 0; t < TPW; ++t)
+#pragma unroll
+    for (int i = 0; i < EPW; ++i)
+      if (lane == 0 && t0 + t < T && e0 + i < E) lg[(size_t)(t0 + t) * E + e0 + i] = sum[t][i];
+}
+// one wave per token
+template <int B>
+__global__ void __launch_bounds__(64)
+moe_choose_kernel(const double* __restrict__ lg, int* __restrict__ ids, float* __restrict__ weights, int E, int top_k,
+                  int renorm) {
+  __shared__ int chosen[64 * B];
+  const size_t t = blockIdx.x;
+  choose_one<B>(lg + t * E, E, top_k, threadIdx.x, renorm, chosen, ids + t * top_k, weights + t * top_k);
 }
 
 // ---------------------------------------------------------------------------
@@ -179,10 +294,274 @@ template <int NT, int GP>
 struct Acts {
   u32x4_t v[NT][8 / GP];
 };
-template <bool DOWN>
-struct Scales {
-  u32x4_t v[DOWN ? 1 : 2];
-  uint32_t next[DOWN ? 1 : 2];
+
+// The scales of a wave's rows: 16 RT rows of one plane (and, gate and up, of
+// a second one).  first: index of the first row's first scale in its plane.
+template <int R, bool DOWN>
+struct RowScales {
+  static constexpr int PL = DOWN ? 1 : 2, RT = R / PL;
+  static constexpr int LOADS = 2 * PL;
+  struct Regs {
+    u32x4_t v[PL];
+    uint32_t next[PL];
+  };
+  rsrc_t r[PL];
+  uint32_t off[PL], shift;
+  int G;
+  bool skewed;
+  __device__ __forceinline__ RowScales(const uint16_t* scales0, const uint16_t* scales1, size_t first, int rows,
+                                       int groups, int lane)
+      : G(groups) {
+    const uint32_t srow = (uint32_t)G * 2;
+    skewed = (G & 1) != 0;
+    shift = 0;
+#pragma unroll
+    for (int p = 0; p < PL; ++p) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>((p ? scales1 : scales0) + first);
+      const uint32_t skew = (uint32_t)(a & 2);  // the dword that holds the first scale starts 2 bytes before it
+      r[p] = make_rsrc(reinterpret_cast<const void*>(a - skew), rows > 0 ? (skew + (uint32_t)rows * srow + 3u) & ~3u : 0u);
+      const int row = lane - 16 * RT * p;
+      const bool mine = row >= 0 && row < rows && row < 16 * RT;
+      const uint32_t o = skew + (uint32_t)row * srow;
+      off[p] = mine ? o & ~3u : kNowhere;
+      shift = mine ? (o & 2) * 8 : shift;
+      skewed |= skew != 0;
+    }
+  }
+  // the scales of stages s and s + 1 (offsets past every range read as zeros)
+  __device__ __forceinline__ void load(Regs& L, int s, int se) const {
+    const uint32_t away = s < se ? 0u : kNowhere, away_next = s < se && skewed ? 0u : kNowhere;
+#pragma unroll
+    for (int p = 0; p < PL; ++p) {
+      const uint32_t o = off[p] + 8u * (uint32_t)s;
+      L.v[p] = __builtin_amdgcn_raw_buffer_load_b128(r[p], o | away, 0, 0);
+      L.next[p] = __builtin_amdgcn_raw_buffer_load_b32(r[p], (o + 16) | away_next, 0, 0);
+    }
+    in_order();
+  }
+  // those of row `lane`, two groups a dword, zero past K
+  __device__ __forceinline__ void rows(const Regs& L, int s, uint32_t (&d)[4]) const {
+    u32x4_t v = L.v[0];
+    uint32_t n = L.next[0];
+    if constexpr (PL > 1) {
+      v = v | L.v[1];
+      n |= L.next[1];
+    }
+    if (skewed)
+      v = u32x4_t{__builtin_amdgcn_alignbit(v.y, v.x, shift), __builtin_amdgcn_alignbit(v.z, v.y, shift),
+                  __builtin_amdgcn_alignbit(v.w, v.z, shift), __builtin_amdgcn_alignbit(n, v.w, shift)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int left = G - 4 * s - 2 * i;
+      d[i] = v[i] & (left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0xFFFFu : 0u);
+    }
+  }
+};
+
+// The pairs b0 .. b0 + BT - 1 that chose expert e, in order, into the wave's
+// list; returns how many there are in all.
+template <int BT>
+__device__ __forceinline__ int list_pairs(const int* __restrict__ ids, int P, int e, int b0, int lane, int* list) {
+  int m = 0;
+  for (int p0 = 0; p0 < P; p0 += 512) {
+    int v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = ids[min(p0 + 64 * j + lane, P - 1)];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = p0 + 64 * j + lane < P ? v[j] : -1;
+      const uint64_t bm = __builtin_amdgcn_ballot_w64(v[j] == e);
+      const int r = m + __builtin_popcountll(bm & ((1ull << lane) - 1)) - b0;
+      if (v[j] == e && r >= 0 && r < BT) list[r] = p0 + 64 * j + lane;
+      m += __builtin_popcountll(bm);
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return m;
+}
+
+// h = silu(g) u of pair p and row n in two bf16 parts
+__device__ __forceinline__ void store_gated(float g, float u, uint16_t* h, int p, int rows, int n) {
+  uint32_t hi, lo;
+  split_bf16(g / (1.0f + expf(-g)) * u, hi, lo);
+  uint16_t* o = h + (size_t)p * 2 * rows + (n & ~7) + paired_place(n & 7);
+  o[0] = (uint16_t)hi;
+  o[rows] = (uint16_t)lo;
+}
+
+// The activations of a pass: offset of the row that this lane loads from
+// (kNowhere: none), for GP = 1 of tile 0 row lane / 4, else row li % MT
+template <int GP>
+__device__ __forceinline__ uint32_t act_offset(uint32_t row, int K, int lane) {
+  const int li = lane & 15, lq = lane >> 4;
+  return row * (uint32_t)K * 2u + (GP == 1 ? 32u * (lane & 3) : 32u * lq + 128u * (li / (16 / GP)));
+}
+
+// acc[nt][r][i] = the sums over stages sb .. se - 1 of activation row
+// 16 nt + 4 lq + i (GP > 1: of group (4 lq + i) / MT of row (4 lq + i) % MT)
+// and weight row li of row tile r.  rc: the row tiles' codes, slot0 and
+// slot1: the wave's ring.
+template <int NT, int GP, int R, bool DOWN>
+__device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScales<R, DOWN>& rs, rsrc_t rx,
+                                            const uint32_t (&x_off)[NT], uint8_t* slot0, uint8_t* slot1, int K, int sb,
+                                            int se, int lane, f32x4_t (&acc)[NT][R]) {
+  static_assert(GP == 1 || NT == 1, "packed groups take one tile");
+  constexpr int MT = 16 / GP;                 // activation rows of a tile
+  constexpr int LOADS = 2 * R + NT * 8 / GP;  // of one stage, the scales not counted
+  constexpr bool PAIRED = DOWN || NT == 1;    // code order of the products (x is permuted into it up to one tile)
+  const int li = lane & 15, lq = lane >> 4, G = K >> 6;
+  const uint32_t crow = (uint32_t)K >> 1;
+  const uint32_t c_off = (uint32_t)(lane >> 3) * crow + 16u * ((lane & 7) ^ (lane >> 3));
+  int rd[4];  // this lane's 8 code bytes of group g in a slot: row li, byte 32 g + 8 lq of a tile
+#pragma unroll
+  for (int g = 0; g < 4; ++g) rd[g] = li * 128 + 16 * ((2 * g + (lq >> 1)) ^ (li & 7)) + 8 * (lq & 1);
+  const int xsrc4 = (4 * li + lq) * 4;  // the lane holding this lane's activations after an exchange (byte address)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[nt][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  // (a stage past the wave's share and groups past K: offsets past every
+  // range, which read as zeros)
+  auto load = [&](Acts<NT, GP>& L, uint8_t* ring, int s) __device__ {
+    const uint32_t away = s < se ? 0u : kNowhere;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        dma16(rc[r], (c_off + 8u * h * crow + 128u * (uint32_t)s) | away, 0,
+              ring + (2 * r + h) * (kTileStage / 2));
+    in_order();
+#pragma unroll
+    for (int g = 0; g < 4 / GP; ++g) {
+      const uint32_t away_g = s < se && 4 * s + GP * g + (GP == 1 ? 0 : li / MT) < G ? 0u : kNowhere;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t o = (x_off[nt] + 512u * (uint32_t)s) | away_g;
+        L.v[nt][2 * g] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g, 0, 0);
+        L.v[nt][2 * g + 1] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g + 16, 0, 0);
+      }
+    }
+    in_order();
+  };
+  auto compute = [&](const Acts<NT, GP>& L, const uint8_t* ring, uint32_t d0, uint32_t d1, int s) __device__ {
+    const u32x4_t eights = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    uint32_t sc[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sc[r][0] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d0);
+      sc[r][1] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d1);
+    }
+    auto codes = [&](int r, int g, u32x4_t (&w)[2]) __device__ {
+      const u32x2_t cw = *reinterpret_cast<const u32x2_t*>(ring + rd[g] + r * kTileStage);
+      w[0] = PAIRED ? q4_paired(cw.x) : q4_natural(cw.x);
+      w[1] = PAIRED ? q4_paired(cw.y) : q4_natural(cw.y);
+    };
+    if constexpr (GP == 1) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (g > 0 && 4 * s + g >= G) break;
+        u32x4_t x[NT][2];
+        f32x4_t cr[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[nt][h] = lane_piece(L.v[nt][2 * g + h], xsrc4);
+            if constexpr (PAIRED && !DOWN) x[nt][h] = to_paired(x[nt][h]);
+          }
+          cr[nt] = mfma(x[nt][0], eights, zero);
+          cr[nt] = mfma(x[nt][1], eights, cr[nt]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          u32x4_t w[2];
+          codes(r, g, w);
+          const uint32_t sb16 = (g & 1) ? sc[r][g >> 1] >> 16 : sc[r][g >> 1] & 0xFFFFu;
+          const float sv = f16_bits_to_f32((uint16_t)sb16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            f32x4_t p = mfma(x[nt][0], w[0], zero);
+            p = mfma(x[nt][1], w[1], p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][r][i] = __builtin_fmaf(sv, p[i] - cr[nt][i], acc[nt][r][i]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4 / GP; ++g) {
+        u32x4_t x[GP][2];
+        f32x4_t cr = zero;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4_t v = DOWN ? L.v[0][2 * g + h] : to_paired(L.v[0][2 * g + h]);
+#pragma unroll
+          for (int j = 0; j < GP; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][h][i] = li / MT == j ? v[i] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < GP; ++j) {
+          cr = mfma(x[j][0], eights, cr);
+          cr = mfma(x[j][1], eights, cr);
+        }
+        const int own = GP * g + 4 * lq / MT;  // the group of this lane's accumulator rows
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t sd = GP == 4 ? (lq >> 1 ? sc[r][1] : sc[r][0]) : sc[r][g];
+          const float sv = f16_bits_to_f32((uint16_t)((own & 1) ? sd >> 16 : sd));
+          f32x4_t p = zero;
+#pragma unroll
+          for (int j = 0; j < GP; ++j) {
+            u32x4_t w[2];
+            codes(r, GP * g + j, w);
+            p = mfma(x[j][0], w[0], p);
+            p = mfma(x[j][1], w[1], p);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[0][r][i] = __builtin_fmaf(sv, p[i] - cr[i], acc[0][r][i]);
+        }
+      }
+    }
+  };
+  Acts<NT, GP> L[2];
+  typename RowScales<R, DOWN>::Regs S;
+  rs.load(S, sb, se);
+  load(L[0], slot0, sb);
+  load(L[1], slot1, sb + 1);
+  // the stage's copies have landed when only the next stage's loads are
+  // outstanding; a slot's reads are done before it is written again
+  for (int s = sb; s < se; s += 2) {
+    wait_vm<LOADS>();
+    in_order();
+    uint32_t d[4];
+    rs.rows(S, s, d);
+    compute(L[0], slot0, d[0], d[1], s);
+    wait_lgkm0();
+    in_order();
+    rs.load(S, s + 2, se);
+    load(L[0], slot0, s + 2);
+    wait_vm<LOADS>();
+    in_order();
+    if (s + 1 < se) compute(L[1], slot1, d[2], d[3], s + 1);
+    wait_lgkm0();
+    in_order();
+    load(L[1], slot1, s + 3);
+  }
+  wait_vm<0>();  // (nothing lands in the ring any more)
+  in_order();
+}
+
+// The gate and up products of one token choose their expert themselves
+constexpr int kOneExperts = 256;  // at most
+struct OneToken {
+  const double* lg;
+  int* ids;
+  float* weights;
+  int renorm;
 };
 
 // Gate and up (DOWN false): act = x, codes[0]/[1] the gate and up weights,
@@ -190,11 +569,11 @@ struct Scales {
 // h, codes0 the down weight, out float [pair][rows].  K: the inner dimension
 // of this product, rows: the rows of one expert, wk: waves that share K (the
 // other kWaves / wk share the workgroup's rows).
-template <int R, bool DOWN>
+template <int R, bool DOWN, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2)
 moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
                   const uint16_t* scales1, const int* __restrict__ ids, void* out, int K, int rows, int E, int P,
-                  int top_k, uint32_t act_bytes, int wk) {
+                  int top_k, uint32_t act_bytes, int wk, OneToken one) {
   constexpr int RP = DOWN ? 2 : 1;       // activation rows per pair
   constexpr int BT = 32 / RP;            // pairs per pass, at most
   constexpr int RT = DOWN ? R : R / 2;   // row tiles of the output per wave
@@ -206,12 +585,20 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
   __shared__ __attribute__((aligned(16))) uint8_t ring0[kWaves * SLOT];
   __shared__ __attribute__((aligned(16))) uint8_t ring1[kWaves * SLOT];
   __shared__ int list[kWaves][BT];
+  static_assert(!ONE || kWaves * BT >= kPairGrid, "the single token's choice fits the lists");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int wr = kWaves / wk, kp = wave % wk, rp = wave / wk;
 
   int e = blockIdx.y;
-  if (P <= kPairGrid) {
+  if constexpr (ONE) {
+    if (e == P) {  // (a workgroup of its own writes the choice)
+      if (blockIdx.x == 0 && wave == 0)
+        choose_one<kOneExperts / 64>(one.lg, E, P, lane, one.renorm, &list[0][0], one.ids, one.weights);
+      return;
+    }
+    e = choose_one<kOneExperts / 64>(one.lg, E, e + 1, lane, 0, nullptr, nullptr, nullptr);
+  } else if (P <= kPairGrid) {
     const int id = lane < P ? ids[lane] : -1;
     e = __builtin_amdgcn_readlane(id, blockIdx.y);
     if ((uint32_t)e >= (uint32_t)E) return;
@@ -222,7 +609,7 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
   const int n0 = (blockIdx.x * wr + rp) * (16 * RT);  // this wave's first output row
   const int G = K >> 6, stages = (G + 3) >> 2;
   const int sb = stages * kp / wk, se = stages * (kp + 1) / wk;
-  const uint32_t crow = (uint32_t)K >> 1, srow = (uint32_t)G * 2;
+  const uint32_t crow = (uint32_t)K >> 1;
   rsrc_t rc[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -231,220 +618,35 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
     rc[r] = make_rsrc((r < RT ? codes0 : codes1) + ((size_t)e * rows + t0) * crow, t0 < rows ? 16u * crow : 0u);
   }
   const rsrc_t rx = make_rsrc(act, act_bytes);
-  const uint32_t c_off = (uint32_t)(lane >> 3) * crow + 16u * ((lane & 7) ^ (lane >> 3));
-  // the scales of row `lane` of the wave's 16 R rows: relative to the dword
-  // that holds the first of the wave's rows in its plane
-  const int srows = min(16 * RT, rows - n0);
-  const bool mine0 = lane < srows, mine1 = !DOWN && lane >= 16 * RT && lane - 16 * RT < srows;
-  const size_t s0 = ((size_t)e * rows + n0) * G;
-  const uintptr_t sa0 = reinterpret_cast<uintptr_t>(scales0 + s0), sa1 = reinterpret_cast<uintptr_t>(scales1 + s0);
-  const uint32_t skew0 = (uint32_t)(sa0 & 2), skew1 = (uint32_t)(sa1 & 2);
-  const rsrc_t rs0 = make_rsrc(reinterpret_cast<const void*>(sa0 - skew0),
-                               srows > 0 ? (skew0 + (uint32_t)srows * srow + 3u) & ~3u : 0u);
-  const rsrc_t rs1 = make_rsrc(reinterpret_cast<const void*>(sa1 - skew1),
-                               srows > 0 ? (skew1 + (uint32_t)srows * srow + 3u) & ~3u : 0u);
-  const uint32_t so0 = skew0 + (uint32_t)lane * srow, so1 = skew1 + (uint32_t)(lane - 16 * RT) * srow;
-  const uint32_t s_off0 = mine0 ? so0 & ~3u : kNowhere, s_off1 = mine1 ? so1 & ~3u : kNowhere;
-  const uint32_t s_shift = ((mine1 ? so1 : so0) & 2) * 8;
-  const bool skewed = (G & 1) != 0 || skew0 != 0 || skew1 != 0;
-
-  int rd[4];  // this lane's 8 code bytes of group g in a slot: row li, byte 32 g + 8 lq of a tile
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    rd[g] = wave * SLOT + li * 128 + 16 * ((2 * g + (lq >> 1)) ^ (li & 7)) + 8 * (lq & 1);
-  const int xsrc4 = (4 * li + lq) * 4;  // the lane holding this lane's activations after an exchange (byte address)
+  RowScales<R, DOWN> rs(scales0, scales1, ((size_t)e * rows + n0) * G, min(16 * RT, rows - n0), G, lane);
 
   // One pass over the wave's share of K for the mr activation rows of the
   // list, then the workgroup's sums
   auto pass = [&](auto ntc, auto gpc, int mr) __device__ {
     constexpr int NT = decltype(ntc)::value, GP = decltype(gpc)::value;
-    static_assert(GP == 1 || NT == 1, "packed groups take one tile");
-    constexpr int MT = 16 / GP;                 // activation rows of a tile
-    constexpr int LOADS = 2 * R + NT * 8 / GP;  // of one stage, the scales not counted
-    constexpr bool PAIRED = DOWN || NT == 1;    // code order of the products (x is permuted into it up to one tile)
+    constexpr int MT = 16 / GP;  // activation rows of a tile
     uint32_t x_off[NT];
-  #pragma unroll
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int a = GP == 1 ? 16 * nt + (lane >> 2) : li % MT;
       const int p = list[wave][min(a, mr - 1) / RP];
       const uint32_t row = DOWN ? 2u * p + (a & 1) : (uint32_t)(p / top_k);
       // (rows past the last read as zeros)
-      x_off[nt] = a < mr ? row * (uint32_t)K * 2u + (GP == 1 ? 32u * (lane & 3) : 32u * lq + 128u * (li / MT)) : kNowhere;
+      x_off[nt] = a < mr ? act_offset<GP>(row, K, lane) : kNowhere;
     }
     f32x4_t acc[NT][R];
-  #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-  #pragma unroll
-      for (int r = 0; r < R; ++r) acc[nt][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    // (a stage past the wave's share and groups past K: offsets past every
-    // range, which read as zeros)
-    auto load_scales = [&](Scales<DOWN>& L, int s) __device__ {
-      const uint32_t away = s < se ? 0u : kNowhere;
-      const uint32_t o0 = (s_off0 + 8u * (uint32_t)s) | away, o1 = (s_off1 + 8u * (uint32_t)s) | away;
-      L.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rs0, o0, 0, 0);
-      if constexpr (!DOWN) L.v[1] = __builtin_amdgcn_raw_buffer_load_b128(rs1, o1, 0, 0);
-      if (skewed) {
-        L.next[0] = __builtin_amdgcn_raw_buffer_load_b32(rs0, o0 + 16, 0, 0);
-        if constexpr (!DOWN) L.next[1] = __builtin_amdgcn_raw_buffer_load_b32(rs1, o1 + 16, 0, 0);
-      }
-      in_order();
-    };
-    auto load = [&](Acts<NT, GP>& L, uint8_t* ring, int s) __device__ {
-      const uint32_t away = s < se ? 0u : kNowhere;
-  #pragma unroll
-      for (int r = 0; r < R; ++r)
-  #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          dma16(rc[r], (c_off + 8u * h * crow + 128u * (uint32_t)s) | away, 0,
-                ring + wave * SLOT + (2 * r + h) * (kTileStage / 2));
-      in_order();
-  #pragma unroll
-      for (int g = 0; g < 4 / GP; ++g) {
-        const uint32_t away_g = s < se && 4 * s + GP * g + (GP == 1 ? 0 : li / MT) < G ? 0u : kNowhere;
-  #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t o = (x_off[nt] + 512u * (uint32_t)s) | away_g;
-          L.v[nt][2 * g] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g, 0, 0);
-          L.v[nt][2 * g + 1] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g + 16, 0, 0);
-        }
-      }
-      in_order();
-    };
-    // the scales of row `lane`, groups 8 s2 .. 8 s2 + 7 of the wave's share, two a dword
-    auto row_scales = [&](const Scales<DOWN>& L, int s, uint32_t (&d)[4]) __device__ {
-      u32x4_t v = L.v[0];
-      if constexpr (!DOWN) v = v | L.v[1];
-      if (skewed) {
-        const uint32_t n = DOWN ? L.next[0] : L.next[0] | L.next[1 % (DOWN ? 1 : 2)];
-        v = u32x4_t{__builtin_amdgcn_alignbit(v.y, v.x, s_shift), __builtin_amdgcn_alignbit(v.z, v.y, s_shift),
-                    __builtin_amdgcn_alignbit(v.w, v.z, s_shift), __builtin_amdgcn_alignbit(n, v.w, s_shift)};
-      }
-  #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // (groups past K belong to another row)
-        const int left = G - 4 * s - 2 * i;
-        d[i] = v[i] & (left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0xFFFFu : 0u);
-      }
-    };
-    auto compute = [&](const Acts<NT, GP>& L, const uint8_t* ring, uint32_t d0, uint32_t d1, int s) __device__ {
-      const u32x4_t eights = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
-      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-      uint32_t sc[R][2];
-  #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        sc[r][0] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d0);
-        sc[r][1] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d1);
-      }
-      auto codes = [&](int r, int g, u32x4_t (&w)[2]) __device__ {
-        const u32x2_t cw = *reinterpret_cast<const u32x2_t*>(ring + rd[g] + r * kTileStage);
-        w[0] = PAIRED ? q4_paired(cw.x) : q4_natural(cw.x);
-        w[1] = PAIRED ? q4_paired(cw.y) : q4_natural(cw.y);
-      };
-      if constexpr (GP == 1) {
-  #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if (g > 0 && 4 * s + g >= G) break;
-          u32x4_t x[NT][2];
-          f32x4_t cr[NT];
-  #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-  #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              x[nt][h] = lane_piece(L.v[nt][2 * g + h], xsrc4);
-              if constexpr (PAIRED && !DOWN) x[nt][h] = to_paired(x[nt][h]);
-            }
-            cr[nt] = mfma(x[nt][0], eights, zero);
-            cr[nt] = mfma(x[nt][1], eights, cr[nt]);
-          }
-  #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            u32x4_t w[2];
-            codes(r, g, w);
-            const uint32_t sb16 = (g & 1) ? sc[r][g >> 1] >> 16 : sc[r][g >> 1] & 0xFFFFu;
-            const float sv = f16_bits_to_f32((uint16_t)sb16);
-  #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              f32x4_t p = mfma(x[nt][0], w[0], zero);
-              p = mfma(x[nt][1], w[1], p);
-  #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[nt][r][i] = __builtin_fmaf(sv, p[i] - cr[nt][i], acc[nt][r][i]);
-            }
-          }
-        }
-      } else {
-  #pragma unroll
-        for (int g = 0; g < 4 / GP; ++g) {
-          u32x4_t x[GP][2];
-          f32x4_t cr = zero;
-  #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const u32x4_t v = DOWN ? L.v[0][2 * g + h] : to_paired(L.v[0][2 * g + h]);
-  #pragma unroll
-            for (int j = 0; j < GP; ++j)
-  #pragma unroll
-              for (int i = 0; i < 4; ++i) x[j][h][i] = li / MT == j ? v[i] : 0u;
-          }
-  #pragma unroll
-          for (int j = 0; j < GP; ++j) {
-            cr = mfma(x[j][0], eights, cr);
-            cr = mfma(x[j][1], eights, cr);
-          }
-          const int own = GP * g + 4 * lq / MT;  // the group of this lane's accumulator rows
-  #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t sd = GP == 4 ? (lq >> 1 ? sc[r][1] : sc[r][0]) : sc[r][g];
-            const float sv = f16_bits_to_f32((uint16_t)((own & 1) ? sd >> 16 : sd));
-            f32x4_t p = zero;
-  #pragma unroll
-            for (int j = 0; j < GP; ++j) {
-              u32x4_t w[2];
-              codes(r, GP * g + j, w);
-              p = mfma(x[j][0], w[0], p);
-              p = mfma(x[j][1], w[1], p);
-            }
-  #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[0][r][i] = __builtin_fmaf(sv, p[i] - cr[i], acc[0][r][i]);
-          }
-        }
-      }
-    };
-    Acts<NT, GP> L[2];
-    Scales<DOWN> S;
-    load_scales(S, sb);
-    load(L[0], ring0, sb);
-    load(L[1], ring1, sb + 1);
-    // the stage's copies have landed when only the next stage's loads are
-    // outstanding; a slot's reads are done before it is written again
-    for (int s = sb; s < se; s += 2) {
-      wait_vm<LOADS>();
-      in_order();
-      uint32_t d[4];
-      row_scales(S, s, d);
-      compute(L[0], ring0, d[0], d[1], s);
-      wait_lgkm0();
-      in_order();
-      load_scales(S, s + 2);
-      load(L[0], ring0, s + 2);
-      wait_vm<LOADS>();
-      in_order();
-      if (s + 1 < se) compute(L[1], ring1, d[2], d[3], s + 1);
-      wait_lgkm0();
-      in_order();
-      load(L[1], ring1, s + 3);
-    }
-    wait_vm<0>();  // (nothing lands in the rings any more)
-    in_order();
+    stream_sums<NT, GP, R, DOWN>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
 
     // the sums of the waves that share K (and of a tile's groups)
-  #pragma unroll
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (MT * nt >= mr) break;
       if (nt > 0) __syncthreads();
       Red& red = *reinterpret_cast<Red*>(ring0 + wave * SLOT);
       if (MT * nt + 4 * lq % MT < mr)
-  #pragma unroll
+#pragma unroll
         for (int r = 0; r < R; ++r)
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 4; ++i) red[r][4 * lq + i][li] = acc[nt][r][i];
       __syncthreads();
       const int tiles = wr * RT, pairs = min(MT, mr - MT * nt) / RP;
@@ -456,7 +658,7 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
         auto sum = [&](int rr, int tt) __device__ {
           double v = 0.0;
           for (int w = 0; w < wk; ++w)
-  #pragma unroll
+#pragma unroll
             for (int j = 0; j < GP; ++j)
               v += (double)(*reinterpret_cast<const Red*>(ring0 + (w0 + w) * SLOT))[rr][MT * j + tt][c];
           return v;
@@ -464,12 +666,7 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
         if constexpr (DOWN) {
           static_cast<float*>(out)[(size_t)p * rows + n] = (float)(sum(r, 2 * t) + sum(r, 2 * t + 1));
         } else {
-          const float g = (float)sum(r, t);
-          uint32_t hi, lo;
-          split_bf16(g / (1.0f + expf(-g)) * (float)sum(RT + r, t), hi, lo);
-          uint16_t* o2 = static_cast<uint16_t*>(out) + (size_t)p * 2 * rows + (n & ~7) + paired_place(n & 7);
-          o2[0] = (uint16_t)hi;
-          o2[rows] = (uint16_t)lo;
+          store_gated((float)sum(r, t), (float)sum(RT + r, t), static_cast<uint16_t*>(out), p, rows, n);
         }
       }
     }
@@ -477,23 +674,13 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
 
   int m = 1;
   for (int b0 = 0; b0 < m; b0 += BT) {
-    // pairs b0 .. b0 + BT - 1 of the expert, in order (each wave its own copy)
-    m = 0;
-    for (int p0 = 0; p0 < P; p0 += 512) {
-      int v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p0 + 64 * j + lane < P ? ids[p0 + 64 * j + lane] : -1;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint64_t bm = __builtin_amdgcn_ballot_w64(v[j] == e);
-        const int r = m + __builtin_popcountll(bm & ((1ull << lane) - 1)) - b0;
-        if (v[j] == e && r >= 0 && r < BT) list[wave][r] = p0 + 64 * j + lane;
-        m += __builtin_popcountll(bm);
-      }
+    if constexpr (ONE) {
+      list[wave][0] = blockIdx.y;
+      pass(Slot<1>{}, Slot<4>{}, 1);
+      return;
     }
+    m = list_pairs<BT>(ids, P, e, b0, lane, list[wave]);
     if (m == 0) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
     const int mr = min(BT, m - b0) * RP;
     // the smallest tiles that hold the rows
     if (mr <= 4) pass(Slot<1>{}, Slot<4>{}, mr);
@@ -504,10 +691,267 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
   }
 }
 
-// y[t][n .. n + 3] = bf16( sum_j weights[t][j] parts[t top_k + j][n .. n + 3] ), j in order
+// The down products of a single token and their weighted sum in one launch: a
+// workgroup of 16 waves takes 16 R rows; its waves share the chosen experts
+// and, where there are fewer than waves, each expert's K.
+constexpr int kOneWaves = 16;
+template <int R>
+__global__ void __launch_bounds__(64 * kOneWaves)
+moe_down_one_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* scales, const int* __restrict__ ids,
+                    const float* __restrict__ weights, uint16_t* y, int K, int rows, int E, int P,
+                    uint32_t act_bytes) {
+  constexpr int SLOT = R * kTileStage;
+  __shared__ __attribute__((aligned(16))) uint8_t ring0[kOneWaves * SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t ring1[kOneWaves * SLOT];
+  __shared__ float red[kOneWaves][R][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int n0 = blockIdx.x * (16 * R);
+  const int G = K >> 6, stages = (G + 3) >> 2;
+  const int wpp = P < kOneWaves ? kOneWaves / P : 1;  // waves per pair
+  const uint32_t crow = (uint32_t)K >> 1;
+  const rsrc_t rx = make_rsrc(h, act_bytes);
+  float sum[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) sum[r] = 0.f;
+  const int part = wave % wpp, sb = stages * part / wpp, se = stages * (part + 1) / wpp;
+  for (int p = wave / wpp; p < P; p += kOneWaves / wpp) {
+    const int e = __builtin_amdgcn_readfirstlane(ids[p]);
+    if ((uint32_t)e >= (uint32_t)E || sb >= se) continue;
+    const float wp = weights[p];
+    rsrc_t rc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int t0 = n0 + 16 * r;
+      rc[r] = make_rsrc(codes + ((size_t)e * rows + t0) * crow, t0 < rows ? 16u * crow : 0u);
+    }
+    const RowScales<R, true> rs(scales, scales, ((size_t)e * rows + n0) * G, min(16 * R, rows - n0), G, lane);
+    const int a = li % 4;  // the pair's two parts
+    const uint32_t x_off[1] = {a < 2 ? act_offset<4>(2u * p + a, K, lane) : kNowhere};
+    f32x4_t acc[1][R];
+    stream_sums<1, 4, R, true>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
+#pragma unroll
+    for (int r = 0; r < R; ++r) sum[r] = __builtin_fmaf(wp, acc[0][r][0] + acc[0][r][1], sum[r]);
+  }
+  // this lane: row li, group lq of every stage
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float v = sum[r];
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    if (lq == 0) red[wave][r][li] = v;
+  }
+  __syncthreads();
+  if (tid < 16 * R && n0 + tid < rows) {
+    double v = 0.0;
+    for (int w = 0; w < kOneWaves; ++w) v += (double)red[w][tid >> 4][tid & 15];
+    y[n0 + tid] = f32_to_bf16_rne((float)v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Experts with many rows each: the four waves of a workgroup take different
+// rows of the weight over the same K and share the activations, which go
+// through LDS once per workgroup (two slots of one stage, a barrier per
+// stage), up to 64 activation rows a pass.  The codes go straight to
+// registers, lane (li, lq) 16 bytes of row li; lanes l and l + 32 swap half
+// of them, so that every lane holds 8 code bytes of each of two groups.
+// blockIdx.z shares K (down only: parts of the sums, added by the combine).
+// Bound: the weight stream up to about 16 rows; above it the conversion of
+// the codes and the scaling of the sums, for which a row tile's codes are
+// converted once for all activation rows.
+// ---------------------------------------------------------------------------
+template <int R, bool DOWN>
+__global__ void __launch_bounds__(kThreads, 2)
+moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
+                const uint16_t* scales1, const int* __restrict__ ids, void* out, int K, int rows, int P, int top_k,
+                uint32_t act_bytes) {
+  constexpr int RP = DOWN ? 2 : 1;      // activation rows per pair
+  constexpr int BT = 64 / RP;           // pairs per pass, at most
+  constexpr int RT = DOWN ? R : R / 2;  // row tiles of the output per wave
+  constexpr int XROW = 512;             // bytes of an activation row in a stage
+  __shared__ __attribute__((aligned(16))) uint8_t xs0[64 * XROW];
+  __shared__ __attribute__((aligned(16))) uint8_t xs1[64 * XROW];
+  __shared__ int list[kWaves][BT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int e = blockIdx.y;
+  const int n0 = (blockIdx.x * kWaves + wave) * (16 * RT);  // this wave's first output row
+  const int G = K >> 6, stages = (G + 3) >> 2;
+  const int sb = stages * blockIdx.z / gridDim.z, se = stages * (blockIdx.z + 1) / gridDim.z;
+  const uint32_t crow = (uint32_t)K >> 1;
+  rsrc_t rc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int t0 = n0 + 16 * (r % RT);
+    rc[r] = make_rsrc((r < RT ? codes0 : codes1) + ((size_t)e * rows + t0) * crow, t0 < rows ? 16u * crow : 0u);
+  }
+  const rsrc_t rx = make_rsrc(act, act_bytes);
+  const uint32_t c_off = (uint32_t)li * crow + 16u * lq;
+  RowScales<R, DOWN> rs(scales0, scales1, ((size_t)e * rows + n0) * G, min(16 * RT, rows - n0), G, lane);
+
+  int m = 1;
+  for (int b0 = 0; b0 < m; b0 += BT) {
+    m = list_pairs<BT>(ids, P, e, b0, lane, list[wave]);
+    if (m == 0) return;
+    auto pass = [&](auto ntc, int mr) __device__ {
+      constexpr int NT = decltype(ntc)::value;
+      // code order of the products (x is permuted into the paired one for a single tile)
+      constexpr bool PAIRED = DOWN || NT == 1;
+      // activation rows: copy j of a wave moves two rows, lane l the piece of
+      // 16 bytes that lies at position l % 32 of row l / 32; piece p of row a
+      // at position p ^ (a % 16), so that sixteen rows' reads of one piece
+      // spread over the banks
+      uint32_t x_off[2 * NT];
+#pragma unroll
+      for (int j = 0; j < 2 * NT; ++j) {
+        const int a = 4 * NT * wave + 2 * j + (lane >> 5);
+        const int p = list[wave][min(a, mr - 1) / RP];
+        const uint32_t row = DOWN ? 2u * p + (a & 1) : (uint32_t)(p / top_k);
+        x_off[j] = a < mr ? row * (uint32_t)K * 2u + 16u * ((lane & 31) ^ (a & 15)) : kNowhere;
+      }
+      f32x4_t acc[NT][R];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[nt][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      int rd[2];  // piece 4 (lq & 1) + 2 (lq >> 1) + h of the first group, row li
+#pragma unroll
+      for (int h = 0; h < 2; ++h) rd[h] = 4 * (lq & 1) + 2 * (lq >> 1) + h;
+
+      auto load_x = [&](uint8_t* xs, int s) __device__ {
+        const uint32_t away = s < se ? 0u : kNowhere;
+#pragma unroll
+        for (int j = 0; j < 2 * NT; ++j)
+          dma16(rx, (x_off[j] + 512u * (uint32_t)s) | away, 0, xs + (4 * NT * wave + 2 * j) * XROW);
+        in_order();
+      };
+      auto load_c = [&](u32x4_t (&c)[R][2], int s) __device__ {
+        const uint32_t o = (c_off + 128u * (uint32_t)s) | (s < se ? 0u : kNowhere);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) c[r][v] = __builtin_amdgcn_raw_buffer_load_b128(rc[r], o + 64 * v, 0, 0);
+        in_order();
+      };
+      auto compute = [&](const u32x4_t (&c)[R][2], const uint8_t* xs, uint32_t d0, uint32_t d1, int s) __device__ {
+        const u32x4_t eights = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (v == 1 && 4 * s + 2 >= G) break;
+          uint32_t cx[R][2], cy[R][2], sc[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const auto sx = __builtin_amdgcn_permlane32_swap(c[r][v].x, c[r][v].z, false, false);
+            const auto sy = __builtin_amdgcn_permlane32_swap(c[r][v].y, c[r][v].w, false, false);
+            cx[r][0] = sx[0], cx[r][1] = sx[1], cy[r][0] = sy[0], cy[r][1] = sy[1];
+            sc[r] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)(v ? d1 : d0));
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (g == 1 && 4 * s + 2 * v + 1 >= G) break;
+            u32x4_t x[NT][2];
+            f32x4_t cr[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                x[nt][h] = *reinterpret_cast<const u32x4_t*>(xs + (16 * nt + li) * XROW +
+                                                             16 * ((8 * (2 * v + g) + rd[h]) ^ li));
+                if constexpr (PAIRED && !DOWN) x[nt][h] = to_paired(x[nt][h]);
+              }
+              cr[nt] = mfma(x[nt][0], eights, zero);
+              cr[nt] = mfma(x[nt][1], eights, cr[nt]);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const u32x4_t w0 = PAIRED ? q4_paired(cx[r][g]) : q4_natural(cx[r][g]);
+              const u32x4_t w1 = PAIRED ? q4_paired(cy[r][g]) : q4_natural(cy[r][g]);
+              const float sv = f16_bits_to_f32((uint16_t)(g ? sc[r] >> 16 : sc[r] & 0xFFFFu));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                f32x4_t p = mfma(x[nt][0], w0, zero);
+                p = mfma(x[nt][1], w1, p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[nt][r][i] = __builtin_fmaf(sv, p[i] - cr[nt][i], acc[nt][r][i]);
+              }
+            }
+          }
+        }
+      };
+      // Per stage: the next stage's activations are asked for when every
+      // wave has left their slot (the barrier), the codes of the stage after
+      // it when their registers are free; before the next barrier the
+      // activations have landed (only loads issued after them outstanding).
+      u32x4_t c0[R][2], c1[R][2];
+      typename RowScales<R, DOWN>::Regs S;
+      rs.load(S, sb, se);
+      load_x(xs0, sb);
+      load_c(c0, sb);
+      load_c(c1, sb + 1);
+      wait_vm<4 * R>();
+      in_order();
+      __builtin_amdgcn_s_barrier();
+      in_order();
+      for (int s = sb; s < se; s += 2) {
+        uint32_t d[4];
+        rs.rows(S, s, d);
+        load_x(xs1, s + 1);
+        compute(c0, xs0, d[0], d[1], s);
+        wait_lgkm0();
+        in_order();
+        load_c(c0, s + 2);
+        rs.load(S, s + 2, se);
+        wait_vm<2 * R + RowScales<R, DOWN>::LOADS>();
+        in_order();
+        __builtin_amdgcn_s_barrier();
+        in_order();
+        load_x(xs0, s + 2);
+        if (s + 1 < se) compute(c1, xs1, d[2], d[3], s + 1);
+        wait_lgkm0();
+        in_order();
+        load_c(c1, s + 3);
+        wait_vm<2 * R>();
+        in_order();
+        __builtin_amdgcn_s_barrier();
+        in_order();
+      }
+      wait_vm<0>();  // (nothing lands in the slots any more)
+      in_order();
+
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; i += RP) {
+          const int a = 16 * nt + 4 * lq + i;
+          if (a >= mr) continue;
+          const int p = list[wave][a / RP];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int n = n0 + 16 * r + li;
+            if (n >= rows) continue;
+            if constexpr (DOWN) {
+              static_cast<float*>(out)[((size_t)blockIdx.z * P + p) * rows + n] = acc[nt][r][i] + acc[nt][r][i + 1];
+            } else {
+              store_gated(acc[nt][r][i], acc[nt][RT + r][i], static_cast<uint16_t*>(out), p, rows, n);
+            }
+          }
+        }
+    };
+    const int mr = min(BT, m - b0) * RP;
+    if (mr <= 16) pass(Slot<1>{}, mr);
+    else if (mr <= 32) pass(Slot<2>{}, mr);
+    else if (mr <= 48) pass(Slot<3>{}, mr);
+    else pass(Slot<4>{}, mr);
+    __syncthreads();
+  }
+}
+
+// y[t][n .. n + 3] = bf16( sum_j weights[t][j] sum_k parts[k][t top_k + j][n .. n + 3] ), in order
 __global__ void __launch_bounds__(256)
 moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids, const float* __restrict__ weights,
-                   uint16_t* __restrict__ y, int rows, int E, int top_k, int T, int vec) {
+                   uint16_t* __restrict__ y, int rows, int E, int top_k, int T, int ks, int vec) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = rows >> 2;
   if (i >= (int64_t)T * per) return;
@@ -516,7 +960,9 @@ moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids,
   for (int j = 0; j < top_k; ++j) {
     const int p = t * top_k + j;
     if ((uint32_t)ids[p] >= (uint32_t)E) continue;
-    const f32x4_t d = *reinterpret_cast<const f32x4_t*>(parts + (size_t)p * rows + n);
+    f32x4_t d = *reinterpret_cast<const f32x4_t*>(parts + (size_t)p * rows + n);
+    for (int k = 1; k < ks; ++k)
+      d += *reinterpret_cast<const f32x4_t*>(parts + ((size_t)k * T * top_k + p) * rows + n);
     const float w = weights[p];
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(w, d[r], v[r]);
@@ -536,60 +982,156 @@ moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids,
 size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 constexpr int kRowTiles = 4;  // per wave
+constexpr int64_t kWideFrom = 40;  // activation rows per expert
+constexpr int kOneRowTiles = 2;  // of a single token's down products
+
+// How the expert products run.  P pairs on `hit` experts in use (at most;
+// the routing is not known here).  Up to kWideFrom activation rows per expert
+// the waves of a workgroup share K, so many that about six waves per CU run
+// (at 32 rows a pass both kinds take the same time, 220 us for eight experts
+// of 2 x 14336 x 5120; with 8 of them used the first takes 27 us where the
+// second takes 35 on 16 experts of 5120 x 1536); above, they share the
+// activations, and workgroups share K where there are few (48 rows on eight
+// experts of 5120 x 14336: 166 us against 214).
+struct ExpertPlan {
+  bool wide;
+  int split;  // of K
+};
+template <bool DOWN>
+ExpertPlan expert_plan(int64_t rows, int64_t inner_dim, int64_t P, int64_t experts) {
+  constexpr int RT = DOWN ? kRowTiles : kRowTiles / 2;
+  const int64_t hit = P < experts ? P : experts;
+  const int64_t waves = (rows + 16 * RT - 1) / (16 * RT) * hit, stages = (inner_dim + 255) / 256;
+  int split = waves >= 1400 ? 1 : waves >= 700 ? 2 : 4;
+  if (P * (DOWN ? 2 : 1) / hit < kWideFrom) return ExpertPlan{false, split};
+  if (!DOWN) split = 1;
+  if (split > stages) split = (int)stages;
+  return ExpertPlan{true, split};
+}
 
 template <bool DOWN>
-hipError_t launch_experts(const MoeArgs& a, void* h, float* parts, hipStream_t s) {
+hipError_t launch_experts(const MoeArgs& a, void* h, float* parts, const double* lg, hipStream_t s) {
   constexpr int R = kRowTiles, RT = DOWN ? R : R / 2;
   const int P = (int)(a.t * a.top_k);
-  const unsigned slots = (unsigned)(P <= kPairGrid ? P : a.experts);
   const int* ids = static_cast<const int*>(a.ids);
   auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
-  const int64_t rows = DOWN ? a.k : a.inner;
-  // waves that share K: so many that about six waves per CU run (experts in
-  // use: at most one per pair)
-  const int64_t waves = rows / (16 * RT) * (P < a.experts ? P : a.experts);
-  const int wk = waves >= 1400 ? 1 : waves >= 700 ? 2 : 4;
-  const int64_t per = kWaves / wk * 16 * RT;
-  const dim3 grid((unsigned)((rows + per - 1) / per), slots);
-  if (DOWN)
-    moe_expert_kernel<R, true><<<grid, dim3(kThreads), 0, s>>>(
-        u16(h), u8(a.codes_down), u16(a.scales_down), u8(a.codes_down), u16(a.scales_down), ids, parts, (int)a.inner,
-        (int)rows, (int)a.experts, P, (int)a.top_k, (uint32_t)((int64_t)P * a.inner * 4), wk);
-  else
-    moe_expert_kernel<R, false><<<grid, dim3(kThreads), 0, s>>>(
-        u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up), ids, h, (int)a.k, (int)rows,
-        (int)a.experts, P, (int)a.top_k, (uint32_t)(a.t * a.k * 2), wk);
+  const int64_t rows = DOWN ? a.k : a.inner, K = DOWN ? a.inner : a.k;
+  const ExpertPlan plan = expert_plan<DOWN>(rows, K, P, a.experts);
+  const uint16_t* act = DOWN ? u16(h) : u16(a.x);
+  const uint32_t act_bytes = (uint32_t)(DOWN ? (int64_t)P * a.inner * 4 : a.t * a.k * 2);
+  const uint8_t* c0 = u8(DOWN ? a.codes_down : a.codes_gate);
+  const uint16_t* s0 = u16(DOWN ? a.scales_down : a.scales_gate);
+  void* out = DOWN ? static_cast<void*>(parts) : h;
+  if (plan.wide) {
+    const int64_t per = kWaves * 16 * RT;
+    moe_wide_kernel<R, DOWN><<<dim3((unsigned)((rows + per - 1) / per), (unsigned)a.experts, (unsigned)plan.split),
+                               dim3(kThreads), 0, s>>>(act, c0, s0, u8(a.codes_up), u16(a.scales_up), ids, out, (int)K,
+                                                       (int)rows, P, (int)a.top_k, act_bytes);
+  } else {
+    const int64_t per = kWaves / plan.split * 16 * RT;
+    const unsigned blocks = (unsigned)((rows + per - 1) / per);
+    auto go = [&](auto kern, unsigned slots) {
+      kern<<<dim3(blocks, slots), dim3(kThreads), 0, s>>>(
+          act, c0, s0, u8(a.codes_up), u16(a.scales_up), ids, out, (int)K, (int)rows, (int)a.experts, P, (int)a.top_k,
+          act_bytes, plan.split, OneToken{lg, static_cast<int*>(a.ids), static_cast<float*>(a.weights), a.renorm});
+    };
+    if (!DOWN && lg != nullptr) go(moe_expert_kernel<R, DOWN, !DOWN>, (unsigned)P + 1);
+    else go(moe_expert_kernel<R, DOWN, false>, (unsigned)(P <= kPairGrid ? P : a.experts));
+  }
   return hipGetLastError();
+}
+
+// parts of the down products' sums
+int down_parts(int64_t inner, int64_t k, int64_t experts, int64_t pairs) {
+  const ExpertPlan plan = expert_plan<true>(k, inner, pairs, experts);
+  return plan.wide ? plan.split : 1;
 }
 
 }  // namespace
 
-hipError_t launch_moe_route(const MoeArgs& a, hipStream_t s) {
-  moe_route_kernel<<<dim3((unsigned)a.t), dim3(kRouteThreads), 0, s>>>(
-      static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.router), static_cast<int*>(a.ids),
-      static_cast<float*>(a.weights), (int)a.k, (int)a.experts, (int)a.top_k, a.renorm);
+// Up to this many router values one workgroup per token makes them all
+// (one launch).
+constexpr int64_t kSmallRouter = 64 * 1024;
+constexpr int64_t kFewLogits = 1024;
+
+size_t moe_route_workspace_bytes(int64_t k, int64_t experts, int64_t t) {
+  return experts * k <= kSmallRouter ? 0 : al256((size_t)(t * experts * 8));
+}
+
+hipError_t launch_moe_route(const MoeArgs& a, void* workspace, hipStream_t s) {
+  const auto x = static_cast<const uint16_t*>(a.x), router = static_cast<const uint16_t*>(a.router);
+  int* ids = static_cast<int*>(a.ids);
+  float* weights = static_cast<float*>(a.weights);
+  const int K = (int)a.k, E = (int)a.experts, T = (int)a.t, top_k = (int)a.top_k;
+  if (workspace == nullptr || moe_route_workspace_bytes(a.k, a.experts, a.t) == 0) {
+    moe_route_kernel<<<dim3((unsigned)T), dim3(kRouteThreads), 0, s>>>(x, router, ids, weights, K, E, top_k, a.renorm);
+    return hipGetLastError();
+  }
+  double* lg = static_cast<double*>(workspace);
+  // few logits: a workgroup each; many: sixteen a wave
+  if ((int64_t)T * E <= kFewLogits) moe_one_logit_kernel<<<dim3((unsigned)E, (unsigned)T), dim3(256), 0, s>>>(x, router, lg, K, E);
+  else moe_logits_kernel<4, 4><<<dim3((unsigned)((E + 15) / 16), (unsigned)((T + 3) / 4)), dim3(256), 0, s>>>(x, router, lg, K, E, T);
+  if (E <= 256) moe_choose_kernel<4><<<dim3((unsigned)T), dim3(64), 0, s>>>(lg, ids, weights, E, top_k, a.renorm);
+  else moe_choose_kernel<kMaxExperts / 64><<<dim3((unsigned)T), dim3(64), 0, s>>>(lg, ids, weights, E, top_k, a.renorm);
   return hipGetLastError();
 }
 
-// h of every pair in two bf16 parts, then every pair's down products
+// h of every pair in two bf16 parts, then every pair's down products (the
+// router's logits lie where h comes to lie)
 size_t moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t) {
-  (void)experts;
-  return al256((size_t)(t * top_k * inner * 4)) + al256((size_t)(t * top_k * k * 4));
+  const size_t route = moe_route_workspace_bytes(k, experts, t);
+  const size_t sums = (size_t)down_parts(inner, k, experts, t * top_k) * (size_t)(t * top_k * k * 4);
+  // (a single token's logits lie where the sums would)
+  const size_t one = t == 1 ? (size_t)experts * 8 : 0;
+  const size_t all = al256((size_t)(t * top_k * inner * 4)) + al256(sums > one ? sums : one);
+  return route > all ? route : all;
 }
 
-hipError_t launch_moe_experts(const MoeArgs& a, void* workspace, hipStream_t s) {
+hipError_t launch_moe_experts(const MoeArgs& a, const double* lg, void* workspace, hipStream_t s) {
   void* h = workspace;
-  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + al256((size_t)(a.t * a.top_k * a.inner * 4)));
-  hipError_t e = launch_experts<false>(a, h, parts, s);
-  if (e == hipSuccess) e = launch_experts<true>(a, h, parts, s);
+  const int64_t h_bytes = a.t * a.top_k * a.inner * 4;
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + al256((size_t)h_bytes));
+  hipError_t e = launch_experts<false>(a, h, parts, lg, s);
+  if (e != hipSuccess) return e;
+  const int* ids = static_cast<const int*>(a.ids);
+  const float* weights = static_cast<const float*>(a.weights);
+  uint16_t* y = static_cast<uint16_t*>(a.y);
+  if (a.t == 1) {
+    moe_down_one_kernel<kOneRowTiles><<<dim3((unsigned)((a.k + 16 * kOneRowTiles - 1) / (16 * kOneRowTiles))),
+                                        dim3(64 * kOneWaves), 0, s>>>(
+        static_cast<const uint16_t*>(h), static_cast<const uint8_t*>(a.codes_down),
+        static_cast<const uint16_t*>(a.scales_down), ids, weights, y, (int)a.inner, (int)a.k, (int)a.experts,
+        (int)a.top_k, (uint32_t)h_bytes);
+    return hipGetLastError();
+  }
+  e = launch_experts<true>(a, h, parts, nullptr, s);
   if (e != hipSuccess) return e;
   const int64_t quads = a.t * (a.k / 4);
   const int vec = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
   moe_combine_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s>>>(
-      parts, static_cast<const int*>(a.ids), static_cast<const float*>(a.weights), static_cast<uint16_t*>(a.y),
-      (int)a.k, (int)a.experts, (int)a.top_k, (int)a.t, vec);
+      parts, ids, weights, y, (int)a.k, (int)a.experts, (int)a.top_k, (int)a.t,
+      down_parts(a.inner, a.k, a.experts, a.t * a.top_k), vec);
   return hipGetLastError();
+}
+
+hipError_t launch_moe_experts(const MoeArgs& a, void* workspace, hipStream_t s) {
+  return launch_moe_experts(a, nullptr, workspace, s);
+}
+
+// The whole layer.  A single token's logits lie behind h and the choice is
+// made where it is used (every workgroup of the gate and up products makes
+// it for itself): two launches fewer.
+hipError_t launch_moe(const MoeArgs& a, void* workspace, hipStream_t s) {
+  if (a.t > 1 || a.experts > kOneExperts || a.top_k > kPairGrid) {
+    const hipError_t e = launch_moe_route(a, workspace, s);
+    return e == hipSuccess ? launch_moe_experts(a, nullptr, workspace, s) : e;
+  }
+  double* lg = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + al256((size_t)(a.top_k * a.inner * 4)));
+  moe_one_logit_kernel<<<dim3((unsigned)a.experts), dim3(256), 0, s>>>(
+      static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.router), lg, (int)a.k, (int)a.experts);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? launch_moe_experts(a, lg, workspace, s) : e;
 }
 
 }  // namespace q4lin

@@ -408,10 +408,17 @@ def linear_fmt(fmt, x, w, w_hi=None, scales=None, y=None, stream=None):
 
 def _checked(name, ten, shape, size):
     """The tensor's address; it must be contiguous, of this shape and element size."""
-    if tuple(ten.shape) != shape or ten.element_size() != size or not ten.is_contiguous():
+    if ten.shape != shape or ten.element_size() != size or not ten.is_contiguous():
         raise ValueError("%s must be a contiguous tensor of shape %s with %d-byte elements, got %s of %s" % (
             name, shape, size, tuple(ten.shape), ten.dtype))
     return ten.data_ptr()
+
+
+def _new(shape, dtype, device):
+    """An uninitialised contiguous matrix (``empty_strided`` costs the host less than ``empty``)."""
+    import torch
+
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
 
 
 def _workspace(need, workspace, device):
@@ -421,7 +428,8 @@ def _workspace(need, workspace, device):
     if need < 0:
         raise Q4LinError(-need)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
+        return workspace.data_ptr(), need, workspace
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -431,6 +439,9 @@ def _stream_of(stream, device, *made):
     reuse until its work is done."""
     import torch
 
+    if stream is None and device.index is not None:
+        # the handle alone: the Stream object costs the host 2 us, as much as an allocation
+        return torch._C._cuda_getCurrentRawStream(device.index)
     current = torch.cuda.current_stream(device).cuda_stream
     if stream is None or stream == current:
         return current
@@ -484,7 +495,7 @@ def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, 
     ip = _checked("adapter_ids", adapter_ids, (t,), 4)
     sp = _checked("lora_scale", lora_scale, (adapters,), 4) if lora_scale is not None else None
     if y is None:
-        y = torch.empty((t, n), dtype=torch.bfloat16, device=x.device)
+        y = _new((t, n), torch.bfloat16, x.device)
     yp = _checked("y", y, (t, n), 2)
     lib = load()
     wp, wb, workspace = _workspace(lib.q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank), workspace, x.device)
@@ -520,8 +531,8 @@ def moe_route(x, router, top_k, renormalize=True, stream=None):
     experts = router.shape[0]
     xp = _checked("x", x, (t, k), 2)
     rp = _checked("router", router, (experts, k), 2)
-    ids = torch.empty((t, top_k), dtype=torch.int32, device=x.device)
-    weights = torch.empty((t, top_k), dtype=torch.float32, device=x.device)
+    ids = _new((t, top_k), torch.int32, x.device)
+    weights = _new((t, top_k), torch.float32, x.device)
     stream = _stream_of(stream, x.device, ids, weights)
     st = load().q4lin_moe_route(xp, rp, ids.data_ptr(), weights.data_ptr(), k, experts, top_k, t,
                                 1 if renormalize else 0, stream)
@@ -547,7 +558,7 @@ def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, c
     vp = _checked("weights", weights, (t, top_k), 4)
     experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
     if y is None:
-        y = torch.empty((t, k), dtype=torch.bfloat16, device=x.device)
+        y = _new((t, k), torch.bfloat16, x.device)
     yp = _checked("y", y, (t, k), 2)
     lib = load()
     wp, wb, workspace = _workspace(lib.q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)
@@ -569,10 +580,10 @@ def moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, sca
     xp = _checked("x", x, (t, k), 2)
     experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
     rp = _checked("router", router, (experts, k), 2)
-    ids = torch.empty((t, top_k), dtype=torch.int32, device=x.device)
-    weights = torch.empty((t, top_k), dtype=torch.float32, device=x.device)
+    ids = _new((t, top_k), torch.int32, x.device)
+    weights = _new((t, top_k), torch.float32, x.device)
     if y is None:
-        y = torch.empty((t, k), dtype=torch.bfloat16, device=x.device)
+        y = _new((t, k), torch.bfloat16, x.device)
     yp = _checked("y", y, (t, k), 2)
     lib = load()
     wp, wb, workspace = _workspace(lib.q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)

@@ -257,13 +257,14 @@ struct LoraPlan {
   int route;       // Q4: the base product's route
   size_t u_bytes;  // the rank values, before the base product's part
   size_t total;
+  bool tail;  // few tokens: u, then the base product with the adapters' term as its last step
 };
 int lora_plan(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_t rank, LoraPlan* p) {
   if (fmt < Q4LIN_FMT_Q4G64_F16S || fmt > Q4LIN_FMT_BF16) return Q4LIN_E_FORMAT;
   if (!shape_ok(n, k, t) || t > kMaxLoraT || n * t * 4 >= kMaxBytes) return Q4LIN_E_SHAPE;
   if (fmt != Q4LIN_FMT_Q4G64_F16S && 2 * n * k >= kMaxBytes) return Q4LIN_E_SHAPE;
   if (adapters < 1 || adapters > kMaxAdapters || rank < 8 || rank > kMaxRank || (rank % 8) != 0) return Q4LIN_E_SHAPE;
-  *p = LoraPlan{Q4LIN_ROUTE_NONE, 0, 0};
+  *p = LoraPlan{Q4LIN_ROUTE_NONE, 0, 0, false};
   if (n == 0 || t == 0) return Q4LIN_OK;
   size_t base = al256((size_t)(n * t * 4));
   if (fmt == Q4LIN_FMT_Q4G64_F16S) {
@@ -276,8 +277,13 @@ int lora_plan(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_
     q4lin::FmtPlan fp;
     if (!q4lin::fmt_plan(fmt, n, k, t, &fp)) return Q4LIN_E_SHAPE;
   }
-  p->u_bytes = q4lin::lora_u_bytes(k, t, rank, adapters);
-  p->total = p->u_bytes + base;
+  if (t <= 16 && q4lin::lora_few(t, rank)) {
+    q4lin::DecodePlan dp;
+    p->tail = fmt != Q4LIN_FMT_Q4G64_F16S || (p->route == Q4LIN_ROUTE_SKINNY && small_uses_fmt(n, k, t)) ||
+              (p->route == Q4LIN_ROUTE_DECODE && q4lin::decode_plan(n, k, t, &dp) && dp.waves == 8);
+  }
+  p->u_bytes = q4lin::lora_u_bytes(k, t, rank);
+  p->total = p->u_bytes + (p->tail ? 0 : base);
   return Q4LIN_OK;
 }
 
@@ -608,6 +614,22 @@ int q4lin_linear_lora(int fmt, const void* x, const void* w, const void* w_hi, c
   float* u = static_cast<float*>(workspace);
   uint8_t* sums = static_cast<uint8_t*>(workspace) + p.u_bytes;
   const q4lin::LoraArgs la{x, lora_a, lora_b, lora_scale, adapter_ids, y, n, k, t, adapters, rank};
+  if (p.tail) {  // the base product's kernel adds the adapters' term itself
+    hipError_t e = q4lin::launch_lora_dots(la, u, s);
+    if (e != hipSuccess) return Q4LIN_E_LAUNCH;
+    const q4lin::LoraTail tail{static_cast<const uint16_t*>(lora_b), static_cast<const float*>(lora_scale),
+                               static_cast<const int*>(adapter_ids), u, (int)rank, (int)adapters};
+    if (p.route == Q4LIN_ROUTE_DECODE) {
+      q4lin::GemvArgs a{x, w, scales, y, n, k, t};
+      a.lora = tail;
+      e = q4lin::launch_decode(a, s);
+    } else {
+      q4lin::FmtArgs a{fmt, x, w, w_hi, scales, y, n, k, t};
+      a.lora = tail;
+      e = q4lin::launch_fmt(a, s);
+    }
+    return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+  }
   hipError_t e = q4lin::launch_lora_shrink(la, u, s);
   if (e != hipSuccess) return Q4LIN_E_LAUNCH;
   // the base product as binary32 sums

@@ -36,6 +36,7 @@
 //     once.
 #include "q4lin_device.h"
 #include "q4lin_kernels.h"
+#include "q4lin_lora_tail.h"
 
 namespace q4lin {
 
@@ -164,10 +165,11 @@ __device__ __forceinline__ float piece_dot_pre(const uint32_t (&c)[16], const u3
 // cost little more than one).
 // WV: waves per workgroup (8, or 12 for long rows); GLU: LinearSwiGLU in one
 // pass (each workgroup takes the same rows of the gate and the up weight).
-template <int PL, int MAXR, int NT, int WV, bool GLU>
+// LORA: the low-rank adapters' term joins the final sum.
+template <int PL, int MAXR, int NT, int WV, bool GLU, bool LORA>
 __global__ void __launch_bounds__(64 * WV)
 decode_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
-              uint16_t* y, int N, int K, int BN, const uint16_t* res, SecondPlane p2) {
+              uint16_t* y, int N, int K, int BN, const uint16_t* res, SecondPlane p2, LoraTail lora) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int G = K >> 6;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -436,6 +438,7 @@ decode_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ codes,
     double v = __builtin_ldexp((double)((v0 + v1) + (v2 + v3)), wexp[wv * NT + t]);
     if constexpr (WV == 8) {
       // the eight threads of a (row, token) are eight consecutive lanes of one wave
+      if constexpr (LORA) v += (double)lora_share(lora, N, n0 + r, t, wv, 8);
       v = sum8_lanes(v);
       if (wv == 0) {
         if (glu) {
@@ -492,7 +495,11 @@ size_t decode_lds(int maxr, int nt, int wv, int64_t bn) {
 
 template <int PL, int MAXR, int NT, int WV = 8>
 hipError_t launch_pm(const DecodePlan& p, const GemvArgs& a, hipStream_t stream) {
-  auto kern = a.glu ? decode_kernel<PL, MAXR, NT, WV, WV == 8> : decode_kernel<PL, MAXR, NT, WV, false>;
+  auto kern = a.glu ? decode_kernel<PL, MAXR, NT, WV, WV == 8, false> : decode_kernel<PL, MAXR, NT, WV, false, false>;
+  if (a.lora.b != nullptr) {
+    if (WV != 8 || a.glu || a.n2 > 0 || a.f32) return hipErrorInvalidValue;
+    kern = decode_kernel<PL, MAXR, NT, WV, false, WV == 8>;
+  }
   const size_t lds = decode_lds(MAXR, NT, WV, p.bn);
   hipError_t e = allow_full_lds(reinterpret_cast<const void*>(kern));
   if (e != hipSuccess) return e;
@@ -502,7 +509,7 @@ hipError_t launch_pm(const DecodePlan& p, const GemvArgs& a, hipStream_t stream)
   kern<<<dim3((unsigned)(blocks1 + blocks2)), dim3(64 * WV), lds, stream>>>(
       static_cast<const uint16_t*>(a.x), static_cast<const uint8_t*>(a.codes), static_cast<const uint16_t*>(a.scales),
       static_cast<uint16_t*>(a.y), (int)a.n, (int)a.k, p.bn, static_cast<const uint16_t*>(a.res),
-      second_plane(a, blocks1));
+      second_plane(a, blocks1), a.lora);
   return hipGetLastError();
 }
 

@@ -66,6 +66,7 @@
 //     the range) is formed again exactly by its thread.
 #include "q4lin_device.h"
 #include "q4lin_kernels.h"
+#include "q4lin_lora_tail.h"
 
 namespace q4lin {
 
@@ -560,12 +561,13 @@ __host__ __device__ constexpr int red_cols(int bn, bool glu) { return glu ? 2 * 
 // partial reads; more outputs), each rounded once; an output that comes out
 // non-finite is formed again exactly.  GLU: the up weight's rows are columns BNP.. (BN rounded up to a
 // multiple of 4), and the output is bf16(silu(G) U) of the two sums.
-template <int F, int CT, int TT, bool GLU = false>
+template <int F, int CT, int TT, bool GLU = false, bool LORA = false>
 __device__ __forceinline__ void final_sum(const f32x4_t (&acc)[CT][TT], uint8_t* lds, int wave, int li, int lq,
                                           int tid, const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo,
                                           const uint8_t* __restrict__ hi, const uint8_t* __restrict__ sc,
                                           uint16_t* __restrict__ y, const uint16_t* __restrict__ res, int f32out,
-                                          int N, int K, int T, int BN, int n0, int rows) {
+                                          int N, int K, int T, int BN, int n0, int rows,
+                                          const LoraTail& lora = {}) {
   constexpr int BT = 16 * TT;
   constexpr int CTH = GLU ? CT / 2 : CT;
   const int BNP = GLU ? (BN + 3) & ~3 : BN;
@@ -592,6 +594,8 @@ __device__ __forceinline__ void final_sum(const f32x4_t (&acc)[CT][TT], uint8_t*
       const double g = (double)(float)v + 0.0, uv = (double)(float)u + 0.0;
       const double silu = g / (1.0 + exp(-g));
       return f32_to_bf16_rne((float)(silu * uv));
+    } else if constexpr (LORA) {
+      return f32_to_bf16_rne((float)(v + (double)lora_share(lora, N, n0 + col, t, 0, 1)));
     } else {
       if (res != nullptr) v += (double)bf16_bits_to_f32(res[o]);  // LinearAdd
       uint16_t h = f32_to_bf16_rne((float)v);
@@ -610,7 +614,7 @@ __device__ __forceinline__ void final_sum(const f32x4_t (&acc)[CT][TT], uint8_t*
         if constexpr (GLU) u += (double)red[(w * BT + t) * RS + BNP + col];
       }
       const size_t o = (size_t)t * N + n0 + col;
-      if (!GLU && f32out) {
+      if (!GLU && !LORA && f32out) {
         reinterpret_cast<float*>(y)[o] = (float)v;  // binary32 sums (the gate and up of LinearSwiGLU)
         continue;
       }
@@ -638,7 +642,7 @@ __device__ __forceinline__ void final_sum(const f32x4_t (&acc)[CT][TT], uint8_t*
       }
     }
     const size_t o = (size_t)t * N + n0 + c0;
-    if (!GLU && f32out) {
+    if (!GLU && !LORA && f32out) {
       // binary32 sums (the gate and up of LinearSwiGLU)
       float* yf = reinterpret_cast<float*>(y) + o;
       if (nv == 4 && (reinterpret_cast<uintptr_t>(yf) & 15) == 0) {
@@ -699,11 +703,11 @@ struct Plane2 {
 // pair's codes and activations go straight to registers, two register sets
 // taking turns (the next pair's loads in flight during a pair's products).
 // ---------------------------------------------------------------------------
-template <int F, int CT, bool GLU>
+template <int F, int CT, bool GLU, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
 fmt_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, const uint8_t* __restrict__ hi,
            const uint8_t* __restrict__ sc, uint16_t* __restrict__ y, const uint16_t* __restrict__ res, int f32out,
-           int N, int K, int T, int BN, Plane2 p2) {
+           int N, int K, int T, int BN, Plane2 p2, LoraTail lora) {
   using U = Unit<F>;
   constexpr int XH = Fmt<F>::XH, HB = Fmt<F>::HB;
   constexpr int NB = 2;  // pairs in flight (register sets)
@@ -834,7 +838,8 @@ fmt_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, const
     }
   }
   // (the partials area lies before the scale table: no wait for its readers)
-  final_sum<F, CT, 1, GLU>(acc, lds, wave, li, lq, tid, x, lo, hi, sc, y, res, f32out, N, K, T, BN, n0, rows);
+  final_sum<F, CT, 1, GLU, LORA>(acc, lds, wave, li, lq, tid, x, lo, hi, sc, y, res, f32out, N, K, T, BN, n0, rows,
+                                 lora);
 }
 
 // ---------------------------------------------------------------------------
@@ -1079,10 +1084,10 @@ fmt_tok_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, c
 // non-finite result is formed again exactly.
 // ---------------------------------------------------------------------------
 constexpr int kGemvWaves = 4;
-template <int CH>
+template <int CH, bool LORA>
 __global__ void __launch_bounds__(64 * kGemvWaves)
 bf16_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, uint16_t* __restrict__ y,
-                 const uint16_t* __restrict__ res, int f32out, int N, int K) {
+                 const uint16_t* __restrict__ res, int f32out, int N, int K, LoraTail lora) {
   const int lane = threadIdx.x & 63;
   const int gw = blockIdx.x * kGemvWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = gridDim.x * kGemvWaves;
@@ -1097,7 +1102,7 @@ bf16_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, 
   auto dot2 = [](uint32_t wv, uint32_t xv, float c) __device__ {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, wv), __builtin_bit_cast(bf16x2_t, xv), c, false);
   };
-  auto dot = [&](const u32x4_t (&a)[CH]) __device__ {
+  auto dot = [&](const u32x4_t (&a)[CH], float extra) __device__ {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -1108,7 +1113,7 @@ bf16_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, 
       s = dot2(w2, x2, s);
       s = dot2(w3, x3, s);
     }
-    return sum64_lanes((double)s);
+    return sum64_lanes(LORA ? (double)s + (double)extra : (double)s);
   };
   auto finish = [&](int n, double v) __device__ {
     if (f32out) {
@@ -1117,7 +1122,7 @@ bf16_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, 
     }
     if (res != nullptr) v += (double)bf16_bits_to_f32(res[n]);  // LinearAdd
     uint16_t h = f32_to_bf16_rne((float)v);
-    if ((h & 0x7F80u) == 0x7F80u) h = exact_output<FMT_BF16>(x, w, nullptr, nullptr, res, N, K, n, 0);  // rare
+    if (!LORA && (h & 0x7F80u) == 0x7F80u) h = exact_output<FMT_BF16>(x, w, nullptr, nullptr, res, N, K, n, 0);  // rare
     y[n] = h;
   };
   for (int r = gw; r < N; r += 2 * nw) {
@@ -1133,7 +1138,12 @@ bf16_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, 
     // itself the scheduler moves each load down to its use, one or two
     // loads in flight at a time)
     __builtin_amdgcn_sched_barrier(0);
-    const double va = dot(a), vb = dot(b);
+    float la = 0.f, lb = 0.f;
+    if constexpr (LORA) {
+      la = lora_share(lora, N, r, 0, lane, 64);
+      lb = lora_share(lora, N, r2, 0, lane, 64);
+    }
+    const double va = dot(a, la), vb = dot(b, lb);
     if (lane == 0) {
       finish(r, va);
       if (r + nw < N) finish(r + nw, vb);
@@ -1222,11 +1232,11 @@ __device__ __forceinline__ float piece_chain(u32x4_t c, uint64_t hbits, float s0
   return d;
 }
 
-template <int F, int CH>
+template <int F, int CH, bool LORA>
 __global__ void __launch_bounds__(64 * kGemvWaves)
 fmt_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, const uint8_t* __restrict__ hi,
                 const uint8_t* __restrict__ sc, uint16_t* __restrict__ y, const uint16_t* __restrict__ res,
-                int f32out, int N, int K) {
+                int f32out, int N, int K, LoraTail lora) {
   using P = GemvPiece<F>;
   const int lane = threadIdx.x & 63;
   const int gw = blockIdx.x * kGemvWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1269,7 +1279,7 @@ fmt_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, 
       w.sv[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, F == FMT_NVFP4 ? p * 2 : (p >> 1) * 2, 0, 0);
     }
   };
-  auto row_sum = [&](const Row& w) __device__ {
+  auto row_sum = [&](const Row& w, float extra) __device__ {
     float acc = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -1280,7 +1290,7 @@ fmt_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, 
         acc = __builtin_fmaf(f16_bits_to_f32(w.sv[i]), d - corr[i], acc);
       }
     }
-    return sum64_lanes((double)acc);
+    return sum64_lanes(LORA ? (double)acc + (double)extra : (double)acc);
   };
   auto finish = [&](int n, double v) __device__ {
     if (f32out) {
@@ -1289,7 +1299,7 @@ fmt_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, 
     }
     if (res != nullptr) v += (double)bf16_bits_to_f32(res[n]);  // LinearAdd
     uint16_t hv = f32_to_bf16_rne((float)v);
-    if ((hv & 0x7F80u) == 0x7F80u) hv = exact_output<F>(x, lo, hi, sc, res, N, K, n, 0);  // rare
+    if (!LORA && (hv & 0x7F80u) == 0x7F80u) hv = exact_output<F>(x, lo, hi, sc, res, N, K, n, 0);  // rare
     y[n] = hv;
   };
   // The grid gives every wave its two rows gw and gw + nw (2 nw >= N).  All
@@ -1310,7 +1320,12 @@ fmt_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, 
     }
     corr[i] = F == FMT_NVFP4 ? 0.0f : piece_chain<F>(u32x4_t{0u, 0u, 0u, 0u}, 0, 0.f, 0.f, xa[i], true);
   }
-  const double va = row_sum(wa), vb = row_sum(wb);
+  float la = 0.f, lb = 0.f;
+  if constexpr (LORA) {
+    la = lora_share(lora, N, r, 0, lane, 64);
+    lb = lora_share(lora, N, min(r + nw, N - 1), 0, lane, 64);
+  }
+  const double va = row_sum(wa, la), vb = row_sum(wb, lb);
   if (lane == 0) {
     finish(r, va);
     if (r + nw < N) finish(r + nw, vb);
@@ -1320,10 +1335,11 @@ fmt_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, 
 template <int F, int CH>
 hipError_t launch_fmt_gemv_ch(const FmtArgs& a, hipStream_t s) {
   const int64_t blocks = (a.n + 2 * kGemvWaves - 1) / (2 * kGemvWaves);  // two rows per wave
-  fmt_gemv_kernel<F, CH><<<dim3((unsigned)blocks), dim3(64 * kGemvWaves), 0, s>>>(
+  auto kern = a.lora.b != nullptr ? fmt_gemv_kernel<F, CH, true> : fmt_gemv_kernel<F, CH, false>;
+  kern<<<dim3((unsigned)blocks), dim3(64 * kGemvWaves), 0, s>>>(
       static_cast<const uint16_t*>(a.x), static_cast<const uint8_t*>(a.lo), static_cast<const uint8_t*>(a.hi),
       static_cast<const uint8_t*>(a.sc), static_cast<uint16_t*>(a.y), static_cast<const uint16_t*>(a.res),
-      a.f32 ? 1 : 0, (int)a.n, (int)a.k);
+      a.f32 ? 1 : 0, (int)a.n, (int)a.k, a.lora);
   return hipGetLastError();
 }
 template <int F>
@@ -1344,9 +1360,10 @@ hipError_t launch_fmt_gemv(const FmtArgs& a, hipStream_t s) {
 template <int CH>
 hipError_t launch_bf16_gemv_ch(const FmtArgs& a, hipStream_t s) {
   const int64_t blocks = (a.n + 2 * kGemvWaves - 1) / (2 * kGemvWaves);  // two rows per wave
-  bf16_gemv_kernel<CH><<<dim3((unsigned)blocks), dim3(64 * kGemvWaves), 0, s>>>(
+  auto kern = a.lora.b != nullptr ? bf16_gemv_kernel<CH, true> : bf16_gemv_kernel<CH, false>;
+  kern<<<dim3((unsigned)blocks), dim3(64 * kGemvWaves), 0, s>>>(
       static_cast<const uint16_t*>(a.x), static_cast<const uint8_t*>(a.lo), static_cast<uint16_t*>(a.y),
-      static_cast<const uint16_t*>(a.res), a.f32 ? 1 : 0, (int)a.n, (int)a.k);
+      static_cast<const uint16_t*>(a.res), a.f32 ? 1 : 0, (int)a.n, (int)a.k, a.lora);
   return hipGetLastError();
 }
 // pieces per lane: the smallest of these that covers K / 512
@@ -1467,7 +1484,8 @@ hipError_t launch_tok_ct(const FmtArgs& a, const TokLaunch& L, const Chunk& c, h
 
 template <int F, int CT, bool GLU>
 hipError_t launch_few(const FmtArgs& a, const FmtPlan& p, const Chunk& c, hipStream_t s) {
-  auto kern = fmt_kernel<F, CT, GLU>;
+  auto kern = fmt_kernel<F, CT, GLU, false>;
+  if (a.lora.b != nullptr) kern = fmt_kernel<F, CT, GLU, !GLU>;
   hipError_t e = allow_full_lds(reinterpret_cast<const void*>(kern));
   if (e != hipSuccess) return e;
   const size_t lds = fmt_lds(0, 1, p.bn, (a.k / Unit<F>::K) * Unit<F>::SB, GLU ? 2 : 1);
@@ -1475,7 +1493,7 @@ hipError_t launch_few(const FmtArgs& a, const FmtPlan& p, const Chunk& c, hipStr
   p2.first = (int)((a.n + p.bn - 1) / p.bn);
   kern<<<dim3((unsigned)p.blocks), dim3(kThreads), lds, s>>>(
       c.x, static_cast<const uint8_t*>(a.lo), static_cast<const uint8_t*>(a.hi), static_cast<const uint8_t*>(a.sc),
-      c.y, c.res, a.f32 ? 1 : 0, (int)a.n, (int)a.k, c.t, p.bn, p2);
+      c.y, c.res, a.f32 ? 1 : 0, (int)a.n, (int)a.k, c.t, p.bn, p2, a.lora);
   return hipGetLastError();
 }
 

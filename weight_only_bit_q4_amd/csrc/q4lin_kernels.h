@@ -12,6 +12,17 @@ namespace q4lin {
 // calls return the recorded result (thread-safe).
 hipError_t allow_full_lds(const void* kern);
 
+// Low-rank adapters as the last step of a base product (few tokens): y =
+// bf16(W x + s_a B_a u), u float [t][rank], b bf16 [adapters][n][rank],
+// scale float [adapters] or nullptr, ids int32 [t].  b == nullptr: none.
+struct LoraTail {
+  const uint16_t* b = nullptr;
+  const float* scale = nullptr;
+  const int* ids = nullptr;
+  const float* u = nullptr;
+  int rank = 0, adapters = 0;
+};
+
 struct GemvArgs {
   const void* x;
   const void* codes;
@@ -29,6 +40,7 @@ struct GemvArgs {
   // codes2/scales2 the up weight (n2 == n); every workgroup takes the same
   // rows of both and stores bf16(silu(G) * U) into y
   bool glu = false;
+  LoraTail lora = {};  // single-token route (eight waves)
 };
 
 // The second plane of a LinearPair as the kernels see it: the workgroups from
@@ -190,6 +202,7 @@ struct FmtArgs {
   void* y2 = nullptr;
   int64_t n2 = 0;
   bool glu = false;
+  LoraTail lora = {};  // up to 16 tokens
 };
 struct FmtPlan {
   int bn;      // rows per workgroup
@@ -214,8 +227,12 @@ struct LoraArgs {
   void* y;
   int64_t n, k, t, adapters, rank;
 };
-// bytes of u, the tokens' rank values in parts of a K split
-size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank, int64_t adapters);
+// bytes of u, the tokens' rank values [t][rank] (in parts of a K split)
+size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank);
+// few tokens: u by the tokens' own products, for a base product that takes a
+// LoraTail
+bool lora_few(int64_t t, int64_t rank);
+hipError_t launch_lora_dots(const LoraArgs& a, float* u, hipStream_t stream);
 hipError_t launch_lora_shrink(const LoraArgs& a, float* u, hipStream_t stream);
 // y = bf16(base + s B u)
 hipError_t launch_lora_finish(const LoraArgs& a, const float* u, const SumSource& base, hipStream_t stream);

@@ -8,17 +8,22 @@
 // and no second term where ids[t] names no adapter.  Two launches beside the
 // base product:
 //
-//   shrink   u, in binary32.  A workgroup takes 16 tokens, one of the
-//            distinct adapters among them (slot) and 16 ranks; its eight
-//            waves and KS workgroups split K.  Bound: reading A_a once per
-//            16 tokens that share it; the K split is there because one
-//            workgroup streams a whole 16 x K slab of A no faster than about
-//            50 GB/s.
+//   shrink   u, in binary32.  A workgroup takes 16 tokens, the distinct
+//            adapters among them one after the other (few tiles: each in a
+//            workgroup of its own) and 16 or 32 ranks; its eight waves and KS
+//            workgroups split K.  Bound: reading x once and A_a once per 16
+//            tokens that share it.  1024 tokens of runs, rank 32, K = 5120
+//            (13 MB): 8.2 us.
 //   finish   sums the KS parts of u, scales, multiplies with B_a and adds S:
 //            one read of S and B_a, one write of y, one rounding.  A wave
-//            takes 16 tokens and 16 NB rows and goes through the distinct
-//            adapters of its tokens: one pass over B for a run of tokens of
-//            one adapter, 16 for 16 tokens of 16.
+//            takes 16 tokens and 16 NB rows of a block and goes through the
+//            distinct adapters of its tokens: one pass over B for a run of
+//            tokens of one adapter, 16 for 16 tokens of 16.  1024 tokens on
+//            6144 rows (38 MB): 15 us.
+//
+// Up to 4096 rank values (T R) each token's own products make them
+// (lora_dots_kernel), and up to 16 tokens the base product's kernel adds the
+// adapters' term as its last step (LoraTail): two launches in all.
 //
 // u is binary32 from end to end; the matrix cores take s_a u as two bf16
 // parts (split_bf16), so the adapters' term is as exact as the base sum.
@@ -26,11 +31,17 @@
 #include "q4lin_mfma16.h"
 
 namespace q4lin {
+
+// up to this many rank values the tokens' own products make them
+bool lora_few(int64_t t, int64_t rank) { return t * rank <= 4096; }
+
 namespace {
 
 using namespace mfma16;
 
 constexpr int kWaves = 8;
+constexpr int kMaxSplit = 4;          // of the shrink's K
+
 constexpr int kThreads = 64 * kWaves;
 
 // The adapter of token t0 + i in lane 16 q + i (-1: none), and in `first` a
@@ -46,7 +57,8 @@ __device__ __forceinline__ int tile_adapters(const int* __restrict__ ids, int t0
   return id;
 }
 
-// u parts [KS][T][R].  grid: (rank tiles of 16 RT) * KS, slots, token tiles.
+// u parts [KS][T][R].  grid: rank tiles of 16 RT times KS, slots, token tiles; a
+// workgroup takes every gridDim.y-th of its tile's distinct adapters.
 template <int RT>
 __global__ void __launch_bounds__(kThreads)
 lora_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const int* __restrict__ ids,
@@ -54,196 +66,304 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ 
   __shared__ float red[kWaves][RT][16][20];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int t0 = blockIdx.z * 16;
-  uint32_t first;
-  const int id = tile_adapters(ids, t0, T, L, li, first);
-  if ((int)blockIdx.y >= __builtin_popcount(first)) return;
-  for (uint32_t s = blockIdx.y; s > 0; --s) first &= first - 1;
-  const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(first));
-  const int ks = blockIdx.x % KS, r0 = (blockIdx.x / KS) * (16 * RT);
+  const int ks = blockIdx.x % KS, t0 = blockIdx.z * 16, r0 = blockIdx.x / KS * (16 * RT);
+  uint32_t todo;
+  const int id = tile_adapters(ids, t0, T, L, li, todo);
 
   // this wave's run of 32-k steps
   const int steps = K >> 5, parts = KS * kWaves, part = ks * kWaves + wave;
   const int sb = (int)((int64_t)steps * part / parts), se = (int)((int64_t)steps * (part + 1) / parts);
-  const uint16_t* xp = x + (size_t)min(t0 + li, T - 1) * K + 8 * lq;  // rows past the last repeat it
-  const uint16_t* ap[RT];
+  // four lanes load 64 bytes of one row (neighbouring lanes on different rows
+  // occupy the address unit several times as long); a lane exchange hands
+  // lane (li, lq) its piece.  Rows past the last repeat it.
+  const int lr = lane >> 2, lp = 8 * (lane & 3), src4 = (4 * li + lq) * 4;
+  const uint16_t* xp = x + (size_t)min(t0 + lr, T - 1) * K + lp;
+  for (int slot = 0; todo != 0; ++slot) {
+    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+    todo &= todo - 1;
+    if (slot % gridDim.y != blockIdx.y) continue;
+    const uint16_t* ap[RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) ap[r] = a + ((size_t)ad * R + min(r0 + 16 * r + li, R - 1)) * K + 8 * lq;
-  f32x4_t acc[RT];
+    for (int r = 0; r < RT; ++r) ap[r] = a + ((size_t)ad * R + min(r0 + 16 * r + lr, R - 1)) * K + lp;
+    f32x4_t acc[RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  int s = sb;
-  for (; s + 4 <= se; s += 4) {  // four steps' loads in flight
-    u32x4_t xv[4], av[RT][4];
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int s = sb; s < se; s += 4) {
+      // four steps' loads in flight (steps past the run repeat the last and
+      // are not used)
+      u32x4_t xv[4], av[RT][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      xv[j] = *reinterpret_cast<const u32x4_t*>(xp + 32 * (size_t)(s + j));
+      for (int j = 0; j < 4; ++j) {
+        const size_t k = 32 * (size_t)min(s + j, se - 1);
+        xv[j] = *reinterpret_cast<const u32x4_t*>(xp + k);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) av[r][j] = *reinterpret_cast<const u32x4_t*>(ap[r] + 32 * (size_t)(s + j));
+        for (int r = 0; r < RT; ++r) av[r][j] = *reinterpret_cast<const u32x4_t*>(ap[r] + k);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (s + j >= se) break;
+        const u32x4_t xo = lane_piece(xv[j], src4);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r] = mfma(xo, lane_piece(av[r][j], src4), acc[r]);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = mfma(xv[j], av[r][j], acc[r]);
-  }
-  for (; s < se; ++s) {
-    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xp + 32 * (size_t)s);
+    __syncthreads();  // (the adapter before is summed)
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-      acc[r] = mfma(xv, *reinterpret_cast<const u32x4_t*>(ap[r] + 32 * (size_t)s), acc[r]);
-  }
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+      for (int i = 0; i < 4; ++i) red[wave][r][4 * lq + i][li] = acc[r][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < RT * 256; o += kThreads) {
+      const int r = o >> 8, t = (o >> 4) & 15, c = o & 15;
+      const int rank = r0 + 16 * r + c;
+      if (t0 + t >= T || rank >= R || ids[t0 + t] != ad) continue;
+      float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][r][4 * lq + i][li] = acc[r][i];
-  __syncthreads();
-  for (int o = threadIdx.x; o < RT * 256; o += kThreads) {
-    const int r = o >> 8, t = (o >> 4) & 15, c = o & 15;
-    const int rank = r0 + 16 * r + c;
-    if (t0 + t >= T || rank >= R || ids[t0 + t] != ad) continue;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += red[w][r][t][c];
-    u[((size_t)ks * T + t0 + t) * R + rank] = v;
+      for (int w = 0; w < kWaves; ++w) v += red[w][r][t][c];
+      u[((size_t)ks * T + t0 + t) * R + rank] = v;
+    }
   }
 }
 
-// grid: row blocks of 4 waves * 16 NB rows, token tiles.  RS: 32-rank steps
-// that cover R.
+// The same for few tokens: a workgroup makes RPW rank values of one token with
+// its own adapter (no tile, so tokens that share one read it again, from the
+// caches), its four waves sharing K: 2.6 us where the tiles take 4 at one
+// token and rank 16.  u: float [T][R].  grid: R / RPW, T.
+template <int RPW>
+__global__ void __launch_bounds__(256)
+lora_dots_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const int* __restrict__ ids,
+                 float* __restrict__ u, int K, int R, int L) {
+  __shared__ float part[4][RPW];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.y, r0 = blockIdx.x * RPW;
+  const int id = ids[t];
+  if ((uint32_t)id >= (uint32_t)L) return;
+  const uint16_t* xr = x + (size_t)t * K;
+  const uint16_t* ar = a + ((size_t)id * R + r0) * K;
+  float sum[RPW];
+#pragma unroll
+  for (int i = 0; i < RPW; ++i) sum[i] = 0.f;
+#pragma unroll 4
+  for (int k = 8 * (64 * wave + lane); k < K; k += 2048) {
+    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xr + k);
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      const u32x4_t av = *reinterpret_cast<const u32x4_t*>(ar + (size_t)i * K + k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t aw = av[j], xw = xv[j];
+        sum[i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, aw), __builtin_bit_cast(bf16x2_t, xw), sum[i], false);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RPW; ++i) {
+    const float v = (float)sum64_lanes((double)sum[i]);
+    if (lane == 0) part[wave][i] = v;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < RPW) {
+    const int i = threadIdx.x;
+    u[(size_t)t * R + r0 + i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+  }
+}
+
+// A workgroup takes 16 tokens and every gridDim.x-th block of 64 NB rows; a
+// wave 16 NB of a block's rows.  RS: 32-rank steps that cover R.  The base
+// sums come in, and y goes out, in runs of 256 NB bytes of a token's row (a
+// wave takes four tokens), the next block's sums asked for before the
+// current one is written; the adapters' term crosses over to that order
+// through LDS (two buffers, a barrier per block).
 template <int RS, int NB>
 __global__ void __launch_bounds__(256)
 lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ scale, const int* __restrict__ ids,
                    const float* __restrict__ u, SumSource base, uint16_t* __restrict__ y, int N, int T, int R, int L,
                    int KS, int vec) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int ROWS = 64 * NB;  // of a block
+  __shared__ __attribute__((aligned(16))) float term[2][16][ROWS + 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int t0 = blockIdx.y * 16;
-  const int n0 = (blockIdx.x * 4 + wave) * (16 * NB);
-  if (n0 >= N) return;
-  const int t = t0 + li;
-  uint32_t todo;
-  const int id = tile_adapters(ids, t0, T, L, li, todo);
 
+  // This lane's base sums of a block: tokens t0 + 4 wave + i, rows nl .. nl + NB - 1
+  typedef float fv_t __attribute__((ext_vector_type(NB)));
+  struct Sums {
+    fv_t v[4];
+  };
+  auto load_sums = [&](int nb0) __device__ {
+    Sums s;
+    const int nl = nb0 + NB * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = min(t0 + 4 * wave + i, T - 1);
+      const float* p = base.part + (size_t)t * N + nl;
+      s.v[i] = fv_t{};
+      if (vec) {
+        if (nl < N) s.v[i] = *reinterpret_cast<const fv_t*>(p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          if (nl + j < N) s.v[i][j] = p[j];
+      }
+    }
+    for (int k = 1; k < base.ks; ++k) {  // the other slices of a K split, in order
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* p = base.part + (size_t)k * base.stride + (size_t)min(t0 + 4 * wave + i, T - 1) * N + nl;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          if (nl + j < N) s.v[i][j] += p[j];
+      }
+    }
+    return s;
+  };
+  Sums cur = load_sums(blockIdx.x * ROWS);
+
+  uint32_t first;
+  const int id = tile_adapters(ids, t0, T, L, li, first);
   // token li's s_a u as two bf16 parts, ranks 32 s + 8 lq .. + 7 of step s
   u32x4_t uh[RS], ul[RS];
   const float sc = id >= 0 && scale != nullptr ? scale[id] : 1.0f;
 #pragma unroll
-  for (int s = 0; s < RS; ++s) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (id >= 0 && 32 * s + 8 * lq < R) {
-      for (int k = 0; k < KS; ++k) {  // parts in order
-        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(u + ((size_t)k * T + t) * R + 32 * s + 8 * lq);
-        const f32x4_t p0 = p[0], p1 = p[1];
+  for (int r = 0; r < RS; ++r) {
+    f32x4_t v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+    if (id >= 0 && 32 * r + 8 * lq < R) {
+      f32x4_t p0[kMaxSplit], p1[kMaxSplit];  // (all parts in flight; past the last, the last again)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] += p0[j];
-          v[4 + j] += p1[j];
-        }
+      for (int k = 0; k < kMaxSplit; ++k) {
+        const f32x4_t* p =
+            reinterpret_cast<const f32x4_t*>(u + ((size_t)min(k, KS - 1) * T + t0 + li) * R + 32 * r + 8 * lq);
+        p0[k] = p[0];
+        p1[k] = p[1];
       }
+#pragma unroll
+      for (int k = 0; k < kMaxSplit; ++k)
+        if (k < KS) {
+          v0 += p0[k];
+          v1 += p1[k];
+        }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t h0, l0, h1, l1;
-      split_bf16(sc * v[2 * j], h0, l0);
-      split_bf16(sc * v[2 * j + 1], h1, l1);
-      uh[s][j] = h0 | (h1 << 16);
-      ul[s][j] = l0 | (l1 << 16);
+      const f32x4_t v = j < 2 ? v0 : v1;
+      split_bf16(sc * v[2 * (j & 1)], h0, l0);
+      split_bf16(sc * v[2 * (j & 1) + 1], h1, l1);
+      uh[r][j] = h0 | (h1 << 16);
+      ul[r][j] = l0 | (l1 << 16);
     }
   }
+  int te[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) te[i] = base.texp != nullptr ? base.texp[min(t0 + 4 * wave + i, T - 1)] : 0;
 
-  f32x4_t acc[NB];
+  int buf = 0;
+  for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS, buf ^= 1) {
+    const int n0 = nb0 + wave * (16 * NB), nl = nb0 + NB * lane;
+    int re[NB];
 #pragma unroll
-  for (int c = 0; c < NB; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  while (todo != 0) {
-    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    todo &= todo - 1;
-    const uint16_t* bp = b + ((size_t)ad * N + n0) * R + 8 * lq;
-    f32x4_t d[NB];
+    for (int j = 0; j < NB; ++j) re[j] = base.texp != nullptr && nl + j < N ? base.rexp[nl + j] : 0;
+    f32x4_t acc[NB];
 #pragma unroll
-    for (int c = 0; c < NB; ++c) d[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < NB; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int last = max(N - 1 - n0, 0);  // rows past the last repeat it and are not stored
+    uint32_t todo = n0 < N ? first : 0u;
+    while (todo != 0) {
+      const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+      todo &= todo - 1;
+      const uint16_t* bp = b + ((size_t)ad * N + n0) * R + 8 * lq;
+      u32x4_t bv[RS][NB];
 #pragma unroll
-    for (int s = 0; s < RS; ++s) {
-      const bool in = 32 * s + 8 * lq < R;
+      for (int r = 0; r < RS; ++r)
 #pragma unroll
-      for (int c = 0; c < NB; ++c) {
-        u32x4_t bv = {0u, 0u, 0u, 0u};
-        const int row = min(16 * c + li, N - 1 - n0);  // rows past the last repeat it and are not stored
-        if (in) bv = *reinterpret_cast<const u32x4_t*>(bp + (size_t)row * R + 32 * s);
-        d[c] = mfma(bv, uh[s], d[c]);
-        d[c] = mfma(bv, ul[s], d[c]);
-      }
+        for (int c = 0; c < NB; ++c) {
+          bv[r][c] = u32x4_t{0u, 0u, 0u, 0u};
+          if (32 * r + 8 * lq < R)
+            bv[r][c] = *reinterpret_cast<const u32x4_t*>(bp + (size_t)min(16 * c + li, last) * R + 32 * r);
+        }
+      f32x4_t d[NB];
+#pragma unroll
+      for (int c = 0; c < NB; ++c) d[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < RS; ++r)
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+          d[c] = mfma(bv[r][c], uh[r], d[c]);
+          d[c] = mfma(bv[r][c], ul[r], d[c]);
+        }
+      // (a token keeps its own adapter's products only: taken, not added, so
+      // that an infinity in one request's adapter stays in its own rows)
+      const bool mine = id == ad;
+#pragma unroll
+      for (int c = 0; c < NB; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[c][i] = mine ? d[c][i] : acc[c][i];
     }
-    // (a token keeps its own adapter's products only: taken, not added, so
-    // that an infinity in one request's adapter stays in its own rows)
-    const bool mine = id == ad;
+    // rows 16 NB wave + 16 c + 4 lq .. + 3 of token li
 #pragma unroll
     for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[c][i] = mine ? d[c][i] : acc[c][i];
-  }
-  if (t >= T) return;
+      *reinterpret_cast<f32x4_t*>(&term[buf][li][16 * NB * wave + 16 * c + 4 * lq]) = acc[c];
+    Sums next = cur;
+    if (nb0 + gridDim.x * ROWS < N) next = load_sums(nb0 + gridDim.x * ROWS);
+    // (not __syncthreads, which would wait for those loads)
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 
-  // the base sum, the one rounding, the store: rows n0 + 16 c + 4 lq .. + 3 of token t
-  const int te = base.texp != nullptr ? base.texp[t] : 0;
-#pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    const int n = n0 + 16 * c + 4 * lq;
-    const size_t o = (size_t)t * N + n;
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < base.ks; ++k) {  // slices in order
-      const float* p = base.part + (size_t)k * base.stride + o;
-      if (vec) {
-        if (n < N) v += *reinterpret_cast<const f32x4_t*>(p);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < N) v[i] += p[i];
-      }
-    }
-    uint16_t h[4];
+    // the base sum, the one rounding, the store
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float f = v[i];
-      // the many-token route's sums carry a power of two per token and row
-      if (base.texp != nullptr && n + i < N) f = __builtin_ldexpf(f, te - base.rexp[n + i]);
-      h[i] = f32_to_bf16_rne(f + acc[c][i]);
-    }
-    if (vec) {
-      if (n < N)
-        *reinterpret_cast<u32x2_t*>(y + o) = u32x2_t{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
-    } else {
+      const int t = t0 + 4 * wave + i;
+      if (t >= T) break;
+      uint16_t h[NB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < N) y[o + i] = h[i];
+      for (int j = 0; j < NB; ++j) {
+        // (the many-token route's sums carry a power of two per token and row)
+        const float f = __builtin_ldexpf(cur.v[i][j], te[i] - re[j]);
+        h[j] = f32_to_bf16_rne(f + term[buf][4 * wave + i][NB * lane + j]);
+      }
+      uint16_t* o = y + (size_t)t * N + nl;
+      if (vec && NB == 4) {
+        if (nl < N)
+          *reinterpret_cast<u32x2_t*>(o) =
+              u32x2_t{h[0] | ((uint32_t)h[1 % NB] << 16), h[2 % NB] | ((uint32_t)h[3 % NB] << 16)};
+      } else {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          if (nl + j < N) o[j] = h[j];
+      }
     }
+    cur = next;
   }
 }
 
-// Workgroups that share K (so that at least about one per CU runs): each
-// still has 32 k steps for most of its waves.
-int shrink_split(int64_t k, int64_t t, int64_t r, int64_t adapters, int rt) {
-  const int64_t tiles = (t + 15) / 16 * ((r + 16 * rt - 1) / (16 * rt));
-  const int64_t slots = t < adapters ? t : adapters;  // an upper bound of the distinct adapters
-  const int64_t groups = tiles * (slots < 16 ? slots : 16);
-  int64_t ks = 256 / groups;
-  if (ks > 8) ks = 8;
+// The shrink's rank tiles per workgroup (two share the activations' loads) and
+// the workgroups that share K: about one per CU where the tokens of a tile
+// have one adapter.  (1024 tokens of rank 32 at K = 5120: 14 us without the
+// split, when 64 workgroups each read 480 KB.)
+struct ShrinkPlan {
+  int rt, ks;
+};
+ShrinkPlan shrink_plan(int64_t k, int64_t t, int64_t r) {
+  if (lora_few(t, r)) return ShrinkPlan{1, 1};
+  const int rt = r <= 16 ? 1 : 2;
+  int64_t ks = 256 / ((t + 15) / 16 * ((r + 16 * rt - 1) / (16 * rt)));
+  if (ks > kMaxSplit) ks = kMaxSplit;
   if (ks > k / (32 * kWaves)) ks = k / (32 * kWaves);
-  return ks < 1 ? 1 : (int)ks;
+  return ShrinkPlan{rt, ks < 1 ? 1 : (int)ks};
 }
 
-// rank tiles per workgroup: where there are many tokens, as many as share
-// the activations' loads; else one, for more workgroups
-int shrink_tiles(int64_t t, int64_t r) { return t < 256 || r <= 16 ? 1 : r <= 32 ? 2 : 4; }
-
 template <int RS>
-hipError_t launch_finish(const LoraArgs& a, const float* u, const SumSource& base, int ks, hipStream_t s) {
+hipError_t launch_finish(const LoraArgs& a, const float* u, const SumSource& base, hipStream_t s) {
+  const int ks = shrink_plan(a.k, a.t, a.rank).ks;
   const int64_t tiles = (a.t + 15) / 16;
   const int vec = (a.n & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
   // four 16-row tiles per wave share the token operand; one where that would
-  // leave CUs idle
+  // leave CUs idle.  About three workgroups per CU.
   const bool wide = tiles * ((a.n + 255) / 256) >= 256;
-  const int nb = wide ? 4 : 1;
-  const dim3 grid((unsigned)((a.n + 64 * nb - 1) / (64 * nb)), (unsigned)tiles);
+  const int64_t blocks = (a.n + (wide ? 255 : 63)) / (wide ? 256 : 64);
+  const int64_t most = 768 / tiles > 1 ? 768 / tiles : 1;
+  const dim3 grid((unsigned)(blocks < most ? blocks : most), (unsigned)tiles);
   auto go = [&](auto kern) {
     kern<<<grid, dim3(256), 0, s>>>(static_cast<const uint16_t*>(a.b), static_cast<const float*>(a.scale),
                                     static_cast<const int*>(a.ids), u, base, static_cast<uint16_t*>(a.y), (int)a.n,
@@ -256,33 +376,48 @@ hipError_t launch_finish(const LoraArgs& a, const float* u, const SumSource& bas
 
 }  // namespace
 
-size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank, int64_t adapters) {
-  const int ks = shrink_split(k, t, rank, adapters, shrink_tiles(t, rank));
-  return ((size_t)ks * (size_t)t * (size_t)rank * 4 + 255) & ~(size_t)255;
+hipError_t launch_lora_dots(const LoraArgs& a, float* u, hipStream_t s) {
+  // one rank value a workgroup while there are few
+  const int rpw = a.t * a.rank <= 256 ? 1 : 4;
+  auto go = [&](auto kern) {
+    kern<<<dim3((unsigned)(a.rank / rpw), (unsigned)a.t), dim3(256), 0, s>>>(
+        static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.a), static_cast<const int*>(a.ids), u,
+        (int)a.k, (int)a.rank, (int)a.adapters);
+  };
+  if (rpw == 1) go(lora_dots_kernel<1>);
+  else go(lora_dots_kernel<4>);
+  return hipGetLastError();
+}
+
+size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank) {
+  return ((size_t)shrink_plan(k, t, rank).ks * (size_t)t * (size_t)rank * 4 + 255) & ~(size_t)255;
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& a, float* u, hipStream_t s) {
-  const int rt = shrink_tiles(a.t, a.rank), ks = shrink_split(a.k, a.t, a.rank, a.adapters, rt);
-  const int64_t slots = a.t < a.adapters ? a.t : a.adapters;
-  const dim3 grid((unsigned)((a.rank + 16 * rt - 1) / (16 * rt) * ks), (unsigned)(slots < 16 ? slots : 16),
-                  (unsigned)((a.t + 15) / 16));
-  auto go = [&](auto kern) {
+  if (lora_few(a.t, a.rank)) return launch_lora_dots(a, u, s);
+  const auto [rt, ks] = shrink_plan(a.k, a.t, a.rank);
+  const int64_t tiles = (a.t + 15) / 16;
+  // A tile's adapters in workgroups of their own while there are few tiles (a
+  // workgroup without one costs its launch)
+  int64_t slots = a.t < a.adapters ? a.t : a.adapters;
+  if (slots > 16) slots = 16;
+  while (slots > 1 && slots * tiles > 64) slots >>= 1;
+  const dim3 grid((unsigned)((a.rank + 16 * rt - 1) / (16 * rt) * ks), (unsigned)slots, (unsigned)tiles);
+  auto go = [&, ks = ks](auto kern) {
     kern<<<grid, dim3(kThreads), 0, s>>>(static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.a),
                                          static_cast<const int*>(a.ids), u, (int)a.k, (int)a.t, (int)a.rank,
                                          (int)a.adapters, ks);
   };
   if (rt == 1) go(lora_shrink_kernel<1>);
-  else if (rt == 2) go(lora_shrink_kernel<2>);
-  else go(lora_shrink_kernel<4>);
+  else go(lora_shrink_kernel<2>);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_finish(const LoraArgs& a, const float* u, const SumSource& base, hipStream_t s) {
-  const int ks = shrink_split(a.k, a.t, a.rank, a.adapters, shrink_tiles(a.t, a.rank));
-  if (a.rank <= 32) return launch_finish<1>(a, u, base, ks, s);
-  if (a.rank <= 64) return launch_finish<2>(a, u, base, ks, s);
-  if (a.rank <= 128) return launch_finish<4>(a, u, base, ks, s);
-  return launch_finish<8>(a, u, base, ks, s);
+  if (a.rank <= 32) return launch_finish<1>(a, u, base, s);
+  if (a.rank <= 64) return launch_finish<2>(a, u, base, s);
+  if (a.rank <= 128) return launch_finish<4>(a, u, base, s);
+  return launch_finish<8>(a, u, base, s);
 }
 
 }  // namespace q4lin

@@ -253,6 +253,7 @@ hipError_t launch_sums(int route, const q4lin::GemvArgs& a, hipStream_t s) {
 constexpr int64_t kMaxLoraT = int64_t(1) << 19;
 constexpr int64_t kMaxRank = 256;
 constexpr int64_t kMaxAdapters = int64_t(1) << 20;
+constexpr int64_t kLoraTailT = 32;  // tokens up to which the base product's kernel adds the adapters' term
 struct LoraPlan {
   int route;       // Q4: the base product's route
   size_t u_bytes;  // the rank values, before the base product's part
@@ -277,7 +278,7 @@ int lora_plan(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_
     q4lin::FmtPlan fp;
     if (!q4lin::fmt_plan(fmt, n, k, t, &fp)) return Q4LIN_E_SHAPE;
   }
-  if (t <= 16 && q4lin::lora_few(t, rank)) {
+  if (t <= kLoraTailT && q4lin::lora_few(t, rank)) {
     q4lin::DecodePlan dp;
     p->tail = fmt != Q4LIN_FMT_Q4G64_F16S || (p->route == Q4LIN_ROUTE_SKINNY && small_uses_fmt(n, k, t)) ||
               (p->route == Q4LIN_ROUTE_DECODE && q4lin::decode_plan(n, k, t, &dp) && dp.waves == 8);

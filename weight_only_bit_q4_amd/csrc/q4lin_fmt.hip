@@ -870,11 +870,11 @@ constexpr int tok_pairs() {
   return TT >= 8 ? m - 2 : m;
 }
 
-template <int F, int CT, int TT, bool GLU>
+template <int F, int CT, int TT, bool GLU, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
 fmt_tok_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, const uint8_t* __restrict__ hi,
                const uint8_t* __restrict__ sc, uint16_t* __restrict__ y, const uint16_t* __restrict__ res,
-               int f32out, int N, int K, int T, int BN, int TS, Plane2 p2) {
+               int f32out, int N, int K, int T, int BN, int TS, Plane2 p2, LoraTail lora) {
   using U = Unit<F>;
   using S = TokShape<F, TT>;
   constexpr int XH = Fmt<F>::XH, HB = Fmt<F>::HB;
@@ -1071,7 +1071,8 @@ fmt_tok_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, c
   }
   wait_vm<0>();  // every copy into the rings has landed before the space is reused
   __syncthreads();
-  final_sum<F, CT, TT, GLU>(acc, lds, wave, li, lq, tid, x, lo, hi, sc, y, res, f32out, N, K, T, BN, n0, rows);
+  final_sum<F, CT, TT, GLU, LORA>(acc, lds, wave, li, lq, tid, x, lo, hi, sc, y, res, f32out, N, K, T, BN, n0, rows,
+                                  lora);
 }
 
 // ---------------------------------------------------------------------------
@@ -1455,7 +1456,11 @@ struct Chunk {
 
 template <int F, int CT, int TT, bool GLU>
 hipError_t launch_tok(const FmtArgs& a, const TokLaunch& L, const Chunk& c, hipStream_t s) {
-  auto kern = fmt_tok_kernel<F, CT, TT, GLU>;
+  auto kern = fmt_tok_kernel<F, CT, TT, GLU, false>;
+  if (a.lora.b != nullptr) {
+    if (TT != 2 || GLU) return hipErrorInvalidValue;
+    kern = fmt_tok_kernel<F, CT, TT, GLU, TT == 2 && !GLU>;
+  }
   hipError_t e = allow_full_lds(reinterpret_cast<const void*>(kern));
   if (e != hipSuccess) return e;
   const size_t lds = fmt_lds(TokShape<F, TT>::PPT, TT, L.bn, (a.k / Unit<F>::K) * Unit<F>::SB, GLU ? 2 : 1);
@@ -1463,7 +1468,7 @@ hipError_t launch_tok(const FmtArgs& a, const TokLaunch& L, const Chunk& c, hipS
   p2.first = (int)L.first;
   kern<<<dim3((unsigned)L.grid), dim3(kThreads), lds, s>>>(
       c.x, static_cast<const uint8_t*>(a.lo), static_cast<const uint8_t*>(a.hi), static_cast<const uint8_t*>(a.sc),
-      c.y, c.res, a.f32 ? 1 : 0, (int)a.n, (int)a.k, c.t, (int)L.bn, L.ts, p2);
+      c.y, c.res, a.f32 ? 1 : 0, (int)a.n, (int)a.k, c.t, (int)L.bn, L.ts, p2, a.lora);
   return hipGetLastError();
 }
 

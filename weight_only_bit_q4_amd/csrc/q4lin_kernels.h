@@ -202,7 +202,7 @@ struct FmtArgs {
   void* y2 = nullptr;
   int64_t n2 = 0;
   bool glu = false;
-  LoraTail lora = {};  // up to 16 tokens
+  LoraTail lora = {};  // up to 32 tokens
 };
 struct FmtPlan {
   int bn;      // rows per workgroup

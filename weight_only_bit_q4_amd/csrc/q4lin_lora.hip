@@ -22,7 +22,7 @@
 //            6144 rows (38 MB): 15 us.
 //
 // Up to 4096 rank values (T R) each token's own products make them
-// (lora_dots_kernel), and up to 16 tokens the base product's kernel adds the
+// (lora_dots_kernel), and up to 32 tokens the base product's kernel adds the
 // adapters' term as its last step (LoraTail): two launches in all.
 //
 // u is binary32 from end to end; the matrix cores take s_a u as two bf16
@@ -40,8 +40,7 @@ namespace {
 using namespace mfma16;
 
 constexpr int kWaves = 8;
-constexpr int kMaxSplit = 4;          // of the shrink's K
-
+constexpr int kMaxSplit = 4;  // of the shrink's K
 constexpr int kThreads = 64 * kWaves;
 
 // The adapter of token t0 + i in lane 16 q + i (-1: none), and in `first` a
@@ -228,20 +227,24 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   for (int r = 0; r < RS; ++r) {
     f32x4_t v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
     if (id >= 0 && 32 * r + 8 * lq < R) {
-      f32x4_t p0[kMaxSplit], p1[kMaxSplit];  // (all parts in flight; past the last, the last again)
+      const f32x4_t* p = reinterpret_cast<const f32x4_t*>(u + (size_t)(t0 + li) * R + 32 * r + 8 * lq);
+      v0 = p[0];
+      v1 = p[1];
+      if (KS > 1) {
+        f32x4_t p0[kMaxSplit], p1[kMaxSplit];  // (all parts in flight; past the last, the last again)
 #pragma unroll
-      for (int k = 0; k < kMaxSplit; ++k) {
-        const f32x4_t* p =
-            reinterpret_cast<const f32x4_t*>(u + ((size_t)min(k, KS - 1) * T + t0 + li) * R + 32 * r + 8 * lq);
-        p0[k] = p[0];
-        p1[k] = p[1];
-      }
-#pragma unroll
-      for (int k = 0; k < kMaxSplit; ++k)
-        if (k < KS) {
-          v0 += p0[k];
-          v1 += p1[k];
+        for (int k = 1; k < kMaxSplit; ++k) {
+          const f32x4_t* q = p + (size_t)min(k, KS - 1) * T * (R >> 2);
+          p0[k] = q[0];
+          p1[k] = q[1];
         }
+#pragma unroll
+        for (int k = 1; k < kMaxSplit; ++k)
+          if (k < KS) {
+            v0 += p0[k];
+            v1 += p1[k];
+          }
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

@@ -231,8 +231,6 @@ moe_choose_kernel(const double* __restrict__ lg, int* __restrict__ ids, float* _
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-// up to this many pairs the grid has a row of workgroups per pair (that of
-// an expert's first pair works), beyond it one per expert
 constexpr int kPairGrid = 64;
 
 // Code dword w (k0..k7) -> exact bf16 128 + q in natural order: byte b gives
@@ -289,6 +287,16 @@ __device__ __forceinline__ u32x4_t to_paired(u32x4_t v) {
 //     that the scales (lane l: row l % 16, the group of its accumulator
 //     rows) cost one multiplication for GP groups.
 constexpr int kTileStage = 16 * 128;  // code bytes of a row tile in a stage
+
+// where this lane copies codes from (rows lane / 8 of a tile's upper or lower
+// half), and where it reads its 8 code bytes of group g in a slot: row li,
+// byte 32 g + 8 lq
+__device__ __forceinline__ uint32_t code_offset(uint32_t crow, int lane) {
+  return (uint32_t)(lane >> 3) * crow + 16u * ((lane & 7) ^ (lane >> 3));
+}
+__device__ __forceinline__ int code_read(int li, int lq, int g) {
+  return li * 128 + 16 * ((2 * g + (lq >> 1)) ^ (li & 7)) + 8 * (lq & 1);
+}
 
 template <int NT, int GP>
 struct Acts {
@@ -381,6 +389,18 @@ __device__ __forceinline__ int list_pairs(const int* __restrict__ ids, int P, in
   return m;
 }
 
+// The expert of this workgroup (its blockIdx.y), or -1: nothing to do.  Up to
+// kPairGrid pairs the grid has a row of workgroups per pair (that of an
+// expert's first pair works), beyond it one per expert.
+__device__ __forceinline__ int block_expert(const int* __restrict__ ids, int P, int E, int lane) {
+  if (P > kPairGrid) return blockIdx.y;
+  const int id = lane < P ? ids[lane] : -1;
+  const int e = __builtin_amdgcn_readlane(id, blockIdx.y);
+  if ((uint32_t)e >= (uint32_t)E) return -1;
+  const uint64_t mask = __builtin_amdgcn_ballot_w64(id == e);
+  return (mask & ((1ull << blockIdx.y) - 1)) != 0 ? -1 : e;
+}
+
 // h = silu(g) u of pair p and row n in two bf16 parts
 __device__ __forceinline__ void store_gated(float g, float u, uint16_t* h, int p, int rows, int n) {
   uint32_t hi, lo;
@@ -412,10 +432,10 @@ __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScal
   constexpr bool PAIRED = DOWN || NT == 1;    // code order of the products (x is permuted into it up to one tile)
   const int li = lane & 15, lq = lane >> 4, G = K >> 6;
   const uint32_t crow = (uint32_t)K >> 1;
-  const uint32_t c_off = (uint32_t)(lane >> 3) * crow + 16u * ((lane & 7) ^ (lane >> 3));
-  int rd[4];  // this lane's 8 code bytes of group g in a slot: row li, byte 32 g + 8 lq of a tile
+  const uint32_t c_off = code_offset(crow, lane);
+  int rd[4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) rd[g] = li * 128 + 16 * ((2 * g + (lq >> 1)) ^ (li & 7)) + 8 * (lq & 1);
+  for (int g = 0; g < 4; ++g) rd[g] = code_read(li, lq, g);
   const int xsrc4 = (4 * li + lq) * 4;  // the lane holding this lane's activations after an exchange (byte address)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -564,20 +584,18 @@ struct OneToken {
   int renorm;
 };
 
-// Gate and up (DOWN false): act = x, codes[0]/[1] the gate and up weights,
-// out = h in two parts, [pair][part][rows] in the paired order.  Down: act =
-// h, codes0 the down weight, out float [pair][rows].  K: the inner dimension
-// of this product, rows: the rows of one expert, wk: waves that share K (the
-// other kWaves / wk share the workgroup's rows).
-template <int R, bool DOWN, bool ONE>
+// The gate and up products of experts with few rows each, and the gate: h in
+// two parts, [pair][part][rows] in the paired order.  K: of the products,
+// rows: of h, wk: waves that share K (the other kWaves / wk share the
+// workgroup's rows).
+template <int R, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2)
-moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
-                  const uint16_t* scales1, const int* __restrict__ ids, void* out, int K, int rows, int E, int P,
-                  int top_k, uint32_t act_bytes, int wk, OneToken one) {
-  constexpr int RP = DOWN ? 2 : 1;       // activation rows per pair
-  constexpr int BT = 32 / RP;            // pairs per pass, at most
-  constexpr int RT = DOWN ? R : R / 2;   // row tiles of the output per wave
-  constexpr int SLOT = R * kTileStage;   // bytes of one stage's codes
+moe_gated_kernel(const uint16_t* x, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
+                 const uint16_t* scales1, const int* __restrict__ ids, uint16_t* h, int K, int rows, int E, int P,
+                 int top_k, uint32_t x_bytes, int wk, OneToken one) {
+  constexpr int BT = 32;                // pairs per pass, at most
+  constexpr int RT = R / 2;             // row tiles of h per wave
+  constexpr int SLOT = R * kTileStage;  // bytes of one stage's codes
   typedef float Red[R][16][20];
   static_assert(sizeof(Red) <= (size_t)SLOT, "the waves' sums reuse a ring slot");
   // the rings' two slots (two objects, so that a read of one is known not to
@@ -598,12 +616,9 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
       return;
     }
     e = choose_one<kOneExperts / 64>(one.lg, E, e + 1, lane, 0, nullptr, nullptr, nullptr);
-  } else if (P <= kPairGrid) {
-    const int id = lane < P ? ids[lane] : -1;
-    e = __builtin_amdgcn_readlane(id, blockIdx.y);
-    if ((uint32_t)e >= (uint32_t)E) return;
-    const uint64_t mask = __builtin_amdgcn_ballot_w64(id == e);
-    if ((mask & ((1ull << blockIdx.y) - 1)) != 0) return;  // an earlier pair's workgroups serve it
+  } else {
+    e = block_expert(ids, P, E, lane);
+    if (e < 0) return;
   }
 
   const int n0 = (blockIdx.x * wr + rp) * (16 * RT);  // this wave's first output row
@@ -617,8 +632,8 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
     // (rows are multiples of 16: a tile is whole or absent)
     rc[r] = make_rsrc((r < RT ? codes0 : codes1) + ((size_t)e * rows + t0) * crow, t0 < rows ? 16u * crow : 0u);
   }
-  const rsrc_t rx = make_rsrc(act, act_bytes);
-  RowScales<R, DOWN> rs(scales0, scales1, ((size_t)e * rows + n0) * G, min(16 * RT, rows - n0), G, lane);
+  const rsrc_t rx = make_rsrc(x, x_bytes);
+  RowScales<R, false> rs(scales0, scales1, ((size_t)e * rows + n0) * G, min(16 * RT, rows - n0), G, lane);
 
   // One pass over the wave's share of K for the mr activation rows of the
   // list, then the workgroup's sums
@@ -629,13 +644,11 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int a = GP == 1 ? 16 * nt + (lane >> 2) : li % MT;
-      const int p = list[wave][min(a, mr - 1) / RP];
-      const uint32_t row = DOWN ? 2u * p + (a & 1) : (uint32_t)(p / top_k);
       // (rows past the last read as zeros)
-      x_off[nt] = a < mr ? act_offset<GP>(row, K, lane) : kNowhere;
+      x_off[nt] = a < mr ? act_offset<GP>((uint32_t)(list[wave][min(a, mr - 1)] / top_k), K, lane) : kNowhere;
     }
     f32x4_t acc[NT][R];
-    stream_sums<NT, GP, R, DOWN>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
+    stream_sums<NT, GP, R, false>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
 
     // the sums of the waves that share K (and of a tile's groups)
 #pragma unroll
@@ -649,12 +662,12 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
 #pragma unroll
           for (int i = 0; i < 4; ++i) red[r][4 * lq + i][li] = acc[nt][r][i];
       __syncthreads();
-      const int tiles = wr * RT, pairs = min(MT, mr - MT * nt) / RP;
+      const int tiles = wr * RT, pairs = min(MT, mr - MT * nt);
       for (int o = tid; o < 16 * tiles * pairs; o += kThreads) {
         const int c = o & 15, tile = (o >> 4) % tiles, t = (o >> 4) / tiles;
         const int w0 = tile / RT * wk, r = tile % RT, n = (blockIdx.x * tiles + tile) * 16 + c;
         if (n >= rows) continue;
-        const int p = list[wave][MT / RP * nt + t];
+        const int p = list[wave][MT * nt + t];
         auto sum = [&](int rr, int tt) __device__ {
           double v = 0.0;
           for (int w = 0; w < wk; ++w)
@@ -663,11 +676,7 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
               v += (double)(*reinterpret_cast<const Red*>(ring0 + (w0 + w) * SLOT))[rr][MT * j + tt][c];
           return v;
         };
-        if constexpr (DOWN) {
-          static_cast<float*>(out)[(size_t)p * rows + n] = (float)(sum(r, 2 * t) + sum(r, 2 * t + 1));
-        } else {
-          store_gated((float)sum(r, t), (float)sum(RT + r, t), static_cast<uint16_t*>(out), p, rows, n);
-        }
+        store_gated((float)sum(r, t), (float)sum(RT + r, t), h, p, rows, n);
       }
     }
   };
@@ -681,7 +690,7 @@ moe_expert_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* sc
     }
     m = list_pairs<BT>(ids, P, e, b0, lane, list[wave]);
     if (m == 0) return;
-    const int mr = min(BT, m - b0) * RP;
+    const int mr = min(BT, m - b0);
     // the smallest tiles that hold the rows
     if (mr <= 4) pass(Slot<1>{}, Slot<4>{}, mr);
     else if (mr <= 8) pass(Slot<1>{}, Slot<2>{}, mr);
@@ -750,35 +759,42 @@ moe_down_one_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* sca
 }
 
 // ---------------------------------------------------------------------------
-// Experts with many rows each: the four waves of a workgroup take different
-// rows of the weight over the same K and share the activations, which go
-// through LDS once per workgroup (two slots of one stage, a barrier per
-// stage), up to 64 activation rows a pass.  The codes go straight to
-// registers, lane (li, lq) 16 bytes of row li; lanes l and l + 32 swap half
-// of them, so that every lane holds 8 code bytes of each of two groups.
+// The same for workgroups whose eight waves take different rows of the weight
+// over the same K and share the activations, up to 32 activation rows a pass,
+// in stages of 128 k.  Codes go through a ring of each wave (two slots),
+// activations through one of the workgroup (three slots, a barrier per
+// stage); both are asked for two stages before their use.  Registers and LDS
+// for four waves per SIMD, as far as the conversion of the codes and the
+// scaling of the sums, not the weight stream, bound it: from about 16 rows.
 // blockIdx.z shares K (down only: parts of the sums, added by the combine).
-// Bound: the weight stream up to about 16 rows; above it the conversion of
-// the codes and the scaling of the sums, for which a row tile's codes are
-// converted once for all activation rows.
 // ---------------------------------------------------------------------------
+constexpr int kWideWaves = 8;
 template <int R, bool DOWN>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(64 * kWideWaves, 4)
 moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
-                const uint16_t* scales1, const int* __restrict__ ids, void* out, int K, int rows, int P, int top_k,
-                uint32_t act_bytes) {
+                const uint16_t* scales1, const int* __restrict__ ids, void* out, int K, int rows, int E, int P,
+                int top_k, uint32_t act_bytes) {
   constexpr int RP = DOWN ? 2 : 1;      // activation rows per pair
-  constexpr int BT = 64 / RP;           // pairs per pass, at most
+  constexpr int BT = 32 / RP;           // pairs per pass, at most
   constexpr int RT = DOWN ? R : R / 2;  // row tiles of the output per wave
-  constexpr int XROW = 512;             // bytes of an activation row in a stage
-  __shared__ __attribute__((aligned(16))) uint8_t xs0[64 * XROW];
-  __shared__ __attribute__((aligned(16))) uint8_t xs1[64 * XROW];
-  __shared__ int list[kWaves][BT];
+  constexpr int XROW = 256;             // bytes of an activation row in a stage (128 k here)
+  constexpr int TILE = 16 * 64;         // code bytes of a row tile in a stage
+  constexpr int SLOT = R * TILE;
+  __shared__ __attribute__((aligned(16))) uint8_t ring0[kWideWaves * SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t ring1[kWideWaves * SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t xs0[32 * XROW];
+  __shared__ __attribute__((aligned(16))) uint8_t xs1[32 * XROW];
+  __shared__ __attribute__((aligned(16))) uint8_t xs2[32 * XROW];
+  __shared__ int list[kWideWaves][BT];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int e = blockIdx.y;
-  const int n0 = (blockIdx.x * kWaves + wave) * (16 * RT);  // this wave's first output row
-  const int G = K >> 6, stages = (G + 3) >> 2;
-  const int sb = stages * blockIdx.z / gridDim.z, se = stages * (blockIdx.z + 1) / gridDim.z;
+  const int e = block_expert(ids, P, E, lane);
+  if (e < 0) return;
+  const int n0 = (blockIdx.x * kWideWaves + wave) * (16 * RT);  // this wave's first output row
+  const int G = K >> 6, stages = (G + 1) >> 1;
+  // (shares of whole quads of stages, as the scales come)
+  const int quads = (stages + 3) >> 2;
+  const int sb = 4 * (int)(quads * blockIdx.z / gridDim.z), se = min(4 * (int)(quads * (blockIdx.z + 1) / gridDim.z), stages);
   const uint32_t crow = (uint32_t)K >> 1;
   rsrc_t rc[R];
 #pragma unroll
@@ -787,8 +803,18 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
     rc[r] = make_rsrc((r < RT ? codes0 : codes1) + ((size_t)e * rows + t0) * crow, t0 < rows ? 16u * crow : 0u);
   }
   const rsrc_t rx = make_rsrc(act, act_bytes);
-  const uint32_t c_off = (uint32_t)li * crow + 16u * lq;
-  RowScales<R, DOWN> rs(scales0, scales1, ((size_t)e * rows + n0) * G, min(16 * RT, rows - n0), G, lane);
+  // four lanes copy 64 bytes of a row; piece p of row i lies at position 4 i + (p ^ (i / 2 & 3))
+  const uint32_t c_off = (uint32_t)(lane >> 2) * crow + 16u * ((lane & 3) ^ ((lane >> 3) & 3));
+  const RowScales<R, DOWN> rs(scales0, scales1, ((size_t)e * rows + n0) * G, min(16 * RT, rows - n0), G, lane);
+  // operand reads: codes as in stream_sums; activations of group g: pieces
+  // 8 g + 2 lq + h of row li
+  int rd[2], xd[4];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    rd[g] = wave * SLOT + li * 64 + 16 * ((2 * g + (lq >> 1)) ^ ((li >> 1) & 3)) + 8 * (lq & 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) xd[2 * g + h] = li * XROW + 16 * ((8 * g + 2 * lq + h) ^ li);
+  }
 
   int m = 1;
   for (int b0 = 0; b0 < m; b0 += BT) {
@@ -798,124 +824,127 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
       constexpr int NT = decltype(ntc)::value;
       // code order of the products (x is permuted into the paired one for a single tile)
       constexpr bool PAIRED = DOWN || NT == 1;
-      // activation rows: copy j of a wave moves two rows, lane l the piece of
-      // 16 bytes that lies at position l % 32 of row l / 32; piece p of row a
+      constexpr int LOADS = R + 1;  // of a stage, the scales not counted
+      // activation rows: a wave copies four rows, lane l the piece of
+      // 16 bytes that lies at position l % 16 of row l / 16; piece p of row a
       // at position p ^ (a % 16), so that sixteen rows' reads of one piece
       // spread over the banks
-      uint32_t x_off[2 * NT];
-#pragma unroll
-      for (int j = 0; j < 2 * NT; ++j) {
-        const int a = 4 * NT * wave + 2 * j + (lane >> 5);
+      uint32_t x_off;
+      {
+        const int a = 4 * wave + (lane >> 4);
         const int p = list[wave][min(a, mr - 1) / RP];
         const uint32_t row = DOWN ? 2u * p + (a & 1) : (uint32_t)(p / top_k);
-        x_off[j] = a < mr ? row * (uint32_t)K * 2u + 16u * ((lane & 31) ^ (a & 15)) : kNowhere;
+        x_off = a < mr ? row * (uint32_t)K * 2u + 16u * ((lane & 15) ^ (a & 15)) : kNowhere;
       }
       f32x4_t acc[NT][R];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[nt][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      int rd[2];  // piece 4 (lq & 1) + 2 (lq >> 1) + h of the first group, row li
-#pragma unroll
-      for (int h = 0; h < 2; ++h) rd[h] = 4 * (lq & 1) + 2 * (lq >> 1) + h;
 
       auto load_x = [&](uint8_t* xs, int s) __device__ {
-        const uint32_t away = s < se ? 0u : kNowhere;
-#pragma unroll
-        for (int j = 0; j < 2 * NT; ++j)
-          dma16(rx, (x_off[j] + 512u * (uint32_t)s) | away, 0, xs + (4 * NT * wave + 2 * j) * XROW);
+        // (groups past K and rows past the last land as zeros)
+        const bool in = ((lane & 15) ^ ((4 * wave + (lane >> 4)) & 15)) < (s < se ? 8 * (G - 2 * s) : 0);
+        dma16(rx, in ? x_off + 256u * (uint32_t)s : kNowhere, 0, xs + 4 * wave * XROW);
         in_order();
       };
-      auto load_c = [&](u32x4_t (&c)[R][2], int s) __device__ {
-        const uint32_t o = (c_off + 128u * (uint32_t)s) | (s < se ? 0u : kNowhere);
+      auto load_c = [&](uint8_t* ring, int s) __device__ {
+        const uint32_t o = (c_off + 64u * (uint32_t)s) | (s < se ? 0u : kNowhere);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int v = 0; v < 2; ++v) c[r][v] = __builtin_amdgcn_raw_buffer_load_b128(rc[r], o + 64 * v, 0, 0);
+        for (int r = 0; r < R; ++r) dma16(rc[r], o, 0, ring + wave * SLOT + r * TILE);
         in_order();
       };
-      auto compute = [&](const u32x4_t (&c)[R][2], const uint8_t* xs, uint32_t d0, uint32_t d1, int s) __device__ {
+      auto compute = [&](const uint8_t* ring, const uint8_t* xs, uint32_t d0) __device__ {
         const u32x4_t eights = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
         const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+        uint32_t sc[R];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          if (v == 1 && 4 * s + 2 >= G) break;
-          uint32_t cx[R][2], cy[R][2], sc[R];
+        for (int r = 0; r < R; ++r) sc[r] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d0);
+        // Tile by tile (r of group g): a tile's sums are scaled when the next
+        // tile's codes are converted and its products under way, and a
+        // group's LDS reads are issued a group ahead
+        u32x4_t x[2][NT][2];
+        u32x2_t cw[2][R];
+        f32x4_t cr[2][NT], p[2][NT];
+        auto fetch = [&](auto gc) __device__ {
+          constexpr int g = decltype(gc)::value;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const auto sx = __builtin_amdgcn_permlane32_swap(c[r][v].x, c[r][v].z, false, false);
-            const auto sy = __builtin_amdgcn_permlane32_swap(c[r][v].y, c[r][v].w, false, false);
-            cx[r][0] = sx[0], cx[r][1] = sx[1], cy[r][0] = sy[0], cy[r][1] = sy[1];
-            sc[r] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)(v ? d1 : d0));
-          }
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (g == 1 && 4 * s + 2 * v + 1 >= G) break;
-            u32x4_t x[NT][2];
-            f32x4_t cr[NT];
+            for (int h = 0; h < 2; ++h)
+              x[g & 1][nt][h] = *reinterpret_cast<const u32x4_t*>(xs + xd[2 * g + h] + 16 * nt * XROW);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            cw[g & 1][r] = *reinterpret_cast<const u32x2_t*>(ring + rd[g] + r * TILE);
+        };
+        auto scale = [&](auto qc) __device__ {
+          constexpr int q = decltype(qc)::value, g = q / R, r = q % R;
+          const float sv = f16_bits_to_f32((uint16_t)(g ? sc[r] >> 16 : sc[r] & 0xFFFFu));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[nt][r][i] = __builtin_fmaf(sv, p[q & 1][nt][i] - cr[g & 1][nt][i], acc[nt][r][i]);
+        };
+        fetch(Slot<0>{});
+        static_for<2 * R>([&](auto qc) __device__ {
+          constexpr int q = decltype(qc)::value, g = q / R, r = q % R;
+          if constexpr (r == 0) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                x[nt][h] = *reinterpret_cast<const u32x4_t*>(xs + (16 * nt + li) * XROW +
-                                                             16 * ((8 * (2 * v + g) + rd[h]) ^ li));
-                if constexpr (PAIRED && !DOWN) x[nt][h] = to_paired(x[nt][h]);
+              if constexpr (PAIRED && !DOWN) {
+                x[g & 1][nt][0] = to_paired(x[g & 1][nt][0]);
+                x[g & 1][nt][1] = to_paired(x[g & 1][nt][1]);
               }
-              cr[nt] = mfma(x[nt][0], eights, zero);
-              cr[nt] = mfma(x[nt][1], eights, cr[nt]);
+              cr[g & 1][nt] = mfma(x[g & 1][nt][0], eights, zero);
             }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const u32x4_t w0 = PAIRED ? q4_paired(cx[r][g]) : q4_natural(cx[r][g]);
-              const u32x4_t w1 = PAIRED ? q4_paired(cy[r][g]) : q4_natural(cy[r][g]);
-              const float sv = f16_bits_to_f32((uint16_t)(g ? sc[r] >> 16 : sc[r] & 0xFFFFu));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                f32x4_t p = mfma(x[nt][0], w0, zero);
-                p = mfma(x[nt][1], w1, p);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[nt][r][i] = __builtin_fmaf(sv, p[i] - cr[nt][i], acc[nt][r][i]);
-              }
-            }
+            for (int nt = 0; nt < NT; ++nt) cr[g & 1][nt] = mfma(x[g & 1][nt][1], eights, cr[g & 1][nt]);
           }
-        }
+          const u32x4_t w0 = PAIRED ? q4_paired(cw[g & 1][r].x) : q4_natural(cw[g & 1][r].x);
+          const u32x4_t w1 = PAIRED ? q4_paired(cw[g & 1][r].y) : q4_natural(cw[g & 1][r].y);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) p[q & 1][nt] = mfma(x[g & 1][nt][0], w0, zero);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) p[q & 1][nt] = mfma(x[g & 1][nt][1], w1, p[q & 1][nt]);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (q > 0) scale(Slot<(q > 0 ? q - 1 : 0)>{});
+          if constexpr (r == 0 && g < 1) fetch(Slot<1>{});
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        scale(Slot<2 * R - 1>{});
       };
-      // Per stage: the next stage's activations are asked for when every
-      // wave has left their slot (the barrier), the codes of the stage after
-      // it when their registers are free; before the next barrier the
-      // activations have landed (only loads issued after them outstanding).
-      u32x4_t c0[R][2], c1[R][2];
       typename RowScales<R, DOWN>::Regs S;
-      rs.load(S, sb, se);
+      uint32_t d[4];
+      rs.load(S, sb >> 1, (se + 1) >> 1);
       load_x(xs0, sb);
-      load_c(c0, sb);
-      load_c(c1, sb + 1);
-      wait_vm<4 * R>();
-      in_order();
-      __builtin_amdgcn_s_barrier();
-      in_order();
-      for (int s = sb; s < se; s += 2) {
-        uint32_t d[4];
-        rs.rows(S, s, d);
-        load_x(xs1, s + 1);
-        compute(c0, xs0, d[0], d[1], s);
-        wait_lgkm0();
-        in_order();
-        load_c(c0, s + 2);
-        rs.load(S, s + 2, se);
-        wait_vm<2 * R + RowScales<R, DOWN>::LOADS>();
-        in_order();
-        __builtin_amdgcn_s_barrier();
-        in_order();
-        load_x(xs0, s + 2);
-        if (s + 1 < se) compute(c1, xs1, d[2], d[3], s + 1);
-        wait_lgkm0();
-        in_order();
-        load_c(c1, s + 3);
-        wait_vm<2 * R>();
-        in_order();
-        __builtin_amdgcn_s_barrier();
-        in_order();
+      load_c(ring0, sb);
+      load_x(xs1, sb + 1);
+      load_c(ring1, sb + 1);
+      // Per stage: it has landed when only loads issued after its codes are
+      // outstanding; behind the barrier every wave's part of its activations
+      // has, and every wave has left the slot of the stage before, which
+      // takes the activations of the stage after the next
+      for (int s0 = sb; s0 < se; s0 += 12) {
+        static_for<12>([&](auto ic) __device__ {
+          constexpr int i = decltype(ic)::value;
+          const int s = s0 + i;
+          if (s < se) {  // (the same for all waves)
+            wait_vm<LOADS + (i % 4 == 1 ? RowScales<R, DOWN>::LOADS : 0)>();
+            in_order();
+            __builtin_amdgcn_s_barrier();
+            in_order();
+            if constexpr (i % 4 == 0) {
+              rs.rows(S, s >> 1, d);
+              rs.load(S, (s >> 1) + 2, (se + 1) >> 1);
+            }
+            load_x((i + 2) % 3 == 0 ? xs0 : (i + 2) % 3 == 1 ? xs1 : xs2, s + 2);
+            compute((i & 1) ? ring1 : ring0, i % 3 == 0 ? xs0 : i % 3 == 1 ? xs1 : xs2, d[i % 4]);
+            wait_lgkm0();
+            in_order();
+            load_c((i & 1) ? ring1 : ring0, s + 2);
+          }
+        });
       }
       wait_vm<0>();  // (nothing lands in the slots any more)
       in_order();
@@ -941,9 +970,7 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
     };
     const int mr = min(BT, m - b0) * RP;
     if (mr <= 16) pass(Slot<1>{}, mr);
-    else if (mr <= 32) pass(Slot<2>{}, mr);
-    else if (mr <= 48) pass(Slot<3>{}, mr);
-    else pass(Slot<4>{}, mr);
+    else pass(Slot<2>{}, mr);
     __syncthreads();
   }
 }
@@ -981,71 +1008,83 @@ moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids,
 
 size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-constexpr int kRowTiles = 4;  // per wave
-constexpr int64_t kWideFrom = 40;  // activation rows per expert
-constexpr int kOneRowTiles = 2;  // of a single token's down products
+constexpr int kRowTiles = 4;      // per wave (gate and up of few rows)
+constexpr int kWideRowTiles = 2;  // per wave (workgroups that share the activations)
+constexpr int kOneRowTiles = 2;   // of a single token's down products
+// Pairs per expert in use from which the gate and up products share the
+// activations in workgroups (24 of them on eight experts of 2 x 14336 x 5120:
+// 194 us against 222; 4 on 128 of 2 x 768 x 2048 58 either way; 4 on 16 of
+// 2 x 1536 x 5120 45 against 41).
+constexpr int64_t kWideGate = 20;
+// workgroups that the chip holds at a time (two per CU, by LDS and registers)
+constexpr int64_t kResident = 512;
 
-// How the expert products run.  P pairs on `hit` experts in use (at most;
-// the routing is not known here).  Up to kWideFrom activation rows per expert
-// the waves of a workgroup share K, so many that about six waves per CU run
-// (at 32 rows a pass both kinds take the same time, 220 us for eight experts
-// of 2 x 14336 x 5120; with 8 of them used the first takes 27 us where the
-// second takes 35 on 16 experts of 5120 x 1536); above, they share the
-// activations, and workgroups share K where there are few (48 rows on eight
-// experts of 5120 x 14336: 166 us against 214).
-struct ExpertPlan {
-  bool wide;
-  int split;  // of K
-};
-template <bool DOWN>
-ExpertPlan expert_plan(int64_t rows, int64_t inner_dim, int64_t P, int64_t experts) {
-  constexpr int RT = DOWN ? kRowTiles : kRowTiles / 2;
-  const int64_t hit = P < experts ? P : experts;
-  const int64_t waves = (rows + 16 * RT - 1) / (16 * RT) * hit, stages = (inner_dim + 255) / 256;
-  int split = waves >= 1400 ? 1 : waves >= 700 ? 2 : 4;
-  if (P * (DOWN ? 2 : 1) / hit < kWideFrom) return ExpertPlan{false, split};
-  if (!DOWN) split = 1;
-  if (split > stages) split = (int)stages;
-  return ExpertPlan{true, split};
+// Into how many shares (of those below) to split `stages` stages of K, when
+// `groups` workgroups take a whole K each: the rounds of resident workgroups
+// times a share's stages and the `extra` that a workgroup's start and end cost.
+int k_split(int64_t groups, int64_t stages, int64_t extra, int64_t most, bool powers) {
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int64_t s = 1; s <= most && s <= stages; s = powers ? 2 * s : s + 1) {
+    const int64_t c = (groups * s + kResident - 1) / kResident * ((stages + s - 1) / s + extra);
+    if (c < cost) {
+      cost = c;
+      best = (int)s;
+    }
+  }
+  return best;
+}
+// experts in use, at most (the routing is not known here)
+int64_t experts_hit(const MoeArgs& a) {
+  const int64_t pairs = a.t * a.top_k;
+  return pairs < a.experts ? pairs : a.experts;
+}
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// parts of the down products' sums
+int down_parts(const MoeArgs& a) {
+  return k_split(ceil_div(a.k, kWideWaves * 16 * kWideRowTiles) * experts_hit(a), ceil_div(a.inner, 128), 4, 8, false);
 }
 
-template <bool DOWN>
-hipError_t launch_experts(const MoeArgs& a, void* h, float* parts, const double* lg, hipStream_t s) {
-  constexpr int R = kRowTiles, RT = DOWN ? R : R / 2;
+hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t s) {
   const int P = (int)(a.t * a.top_k);
-  const int* ids = static_cast<const int*>(a.ids);
+  const unsigned slots = (unsigned)(P <= kPairGrid ? P : a.experts);
   auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
-  const int64_t rows = DOWN ? a.k : a.inner, K = DOWN ? a.inner : a.k;
-  const ExpertPlan plan = expert_plan<DOWN>(rows, K, P, a.experts);
-  const uint16_t* act = DOWN ? u16(h) : u16(a.x);
-  const uint32_t act_bytes = (uint32_t)(DOWN ? (int64_t)P * a.inner * 4 : a.t * a.k * 2);
-  const uint8_t* c0 = u8(DOWN ? a.codes_down : a.codes_gate);
-  const uint16_t* s0 = u16(DOWN ? a.scales_down : a.scales_gate);
-  void* out = DOWN ? static_cast<void*>(parts) : h;
-  if (plan.wide) {
-    const int64_t per = kWaves * 16 * RT;
-    moe_wide_kernel<R, DOWN><<<dim3((unsigned)((rows + per - 1) / per), (unsigned)a.experts, (unsigned)plan.split),
-                               dim3(kThreads), 0, s>>>(act, c0, s0, u8(a.codes_up), u16(a.scales_up), ids, out, (int)K,
-                                                       (int)rows, P, (int)a.top_k, act_bytes);
-  } else {
-    const int64_t per = kWaves / plan.split * 16 * RT;
-    const unsigned blocks = (unsigned)((rows + per - 1) / per);
-    auto go = [&](auto kern, unsigned slots) {
-      kern<<<dim3(blocks, slots), dim3(kThreads), 0, s>>>(
-          act, c0, s0, u8(a.codes_up), u16(a.scales_up), ids, out, (int)K, (int)rows, (int)a.experts, P, (int)a.top_k,
-          act_bytes, plan.split, OneToken{lg, static_cast<int*>(a.ids), static_cast<float*>(a.weights), a.renorm});
-    };
-    if (!DOWN && lg != nullptr) go(moe_expert_kernel<R, DOWN, !DOWN>, (unsigned)P + 1);
-    else go(moe_expert_kernel<R, DOWN, false>, (unsigned)(P <= kPairGrid ? P : a.experts));
+  const uint32_t x_bytes = (uint32_t)(a.t * a.k * 2);
+  if (P / experts_hit(a) >= kWideGate) {
+    constexpr int R = kWideRowTiles;
+    const dim3 grid((unsigned)ceil_div(a.inner, kWideWaves * 8 * R), slots);
+    moe_wide_kernel<R, false><<<grid, dim3(64 * kWideWaves), 0, s>>>(
+        u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up),
+        static_cast<const int*>(a.ids), h, (int)a.k, (int)a.inner, (int)a.experts, P, (int)a.top_k, x_bytes);
+    return hipGetLastError();
   }
+  constexpr int R = kRowTiles;
+  const int wk = k_split(ceil_div(a.inner, kWaves * 8 * R) * experts_hit(a), ceil_div(a.k, 256), 2, kWaves, true);
+  const unsigned blocks = (unsigned)ceil_div(a.inner, kWaves / wk * 8 * R);
+  auto go = [&](auto kern, unsigned rows) {
+    kern<<<dim3(blocks, rows), dim3(kThreads), 0, s>>>(
+        u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up),
+        static_cast<const int*>(a.ids), static_cast<uint16_t*>(h), (int)a.k, (int)a.inner, (int)a.experts, P,
+        (int)a.top_k, x_bytes, wk, OneToken{lg, static_cast<int*>(a.ids), static_cast<float*>(a.weights), a.renorm});
+  };
+  if (lg != nullptr) go(moe_gated_kernel<R, true>, slots + 1);
+  else go(moe_gated_kernel<R, false>, slots);
   return hipGetLastError();
 }
 
-// parts of the down products' sums
-int down_parts(int64_t inner, int64_t k, int64_t experts, int64_t pairs) {
-  const ExpertPlan plan = expert_plan<true>(k, inner, pairs, experts);
-  return plan.wide ? plan.split : 1;
+hipError_t launch_down(const MoeArgs& a, const void* h, float* parts, hipStream_t s) {
+  constexpr int R = kWideRowTiles;
+  const int P = (int)(a.t * a.top_k);
+  const dim3 grid((unsigned)ceil_div(a.k, kWideWaves * 16 * R), (unsigned)(P <= kPairGrid ? P : a.experts),
+                  (unsigned)down_parts(a));
+  const auto codes = static_cast<const uint8_t*>(a.codes_down);
+  const auto scales = static_cast<const uint16_t*>(a.scales_down);
+  moe_wide_kernel<R, true><<<grid, dim3(64 * kWideWaves), 0, s>>>(
+      static_cast<const uint16_t*>(h), codes, scales, codes, scales, static_cast<const int*>(a.ids), parts,
+      (int)a.inner, (int)a.k, (int)a.experts, P, (int)a.top_k, (uint32_t)((int64_t)P * a.inner * 4));
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -1081,7 +1120,9 @@ hipError_t launch_moe_route(const MoeArgs& a, void* workspace, hipStream_t s) {
 // router's logits lie where h comes to lie)
 size_t moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t) {
   const size_t route = moe_route_workspace_bytes(k, experts, t);
-  const size_t sums = (size_t)down_parts(inner, k, experts, t * top_k) * (size_t)(t * top_k * k * 4);
+  MoeArgs a{};
+  a.inner = inner, a.k = k, a.experts = experts, a.top_k = top_k, a.t = t;
+  const size_t sums = t == 1 ? 0 : (size_t)down_parts(a) * (size_t)(t * top_k * k * 4);
   // (a single token's logits lie where the sums would)
   const size_t one = t == 1 ? (size_t)experts * 8 : 0;
   const size_t all = al256((size_t)(t * top_k * inner * 4)) + al256(sums > one ? sums : one);
@@ -1092,7 +1133,7 @@ hipError_t launch_moe_experts(const MoeArgs& a, const double* lg, void* workspac
   void* h = workspace;
   const int64_t h_bytes = a.t * a.top_k * a.inner * 4;
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + al256((size_t)h_bytes));
-  hipError_t e = launch_experts<false>(a, h, parts, lg, s);
+  hipError_t e = launch_gated(a, h, lg, s);
   if (e != hipSuccess) return e;
   const int* ids = static_cast<const int*>(a.ids);
   const float* weights = static_cast<const float*>(a.weights);
@@ -1105,13 +1146,13 @@ hipError_t launch_moe_experts(const MoeArgs& a, const double* lg, void* workspac
         (int)a.top_k, (uint32_t)h_bytes);
     return hipGetLastError();
   }
-  e = launch_experts<true>(a, h, parts, nullptr, s);
+  e = launch_down(a, h, parts, s);
   if (e != hipSuccess) return e;
   const int64_t quads = a.t * (a.k / 4);
   const int vec = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
   moe_combine_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s>>>(
       parts, ids, weights, y, (int)a.k, (int)a.experts, (int)a.top_k, (int)a.t,
-      down_parts(a.inner, a.k, a.experts, a.t * a.top_k), vec);
+      down_parts(a), vec);
   return hipGetLastError();
 }
 

@@ -75,11 +75,9 @@ __device__ __forceinline__ void logit_sums(const uint16_t* const (&r)[EPW], cons
     for (int i = 0; i < EPW; ++i) sum[t][i] = sum64_lanes(sum[t][i]);
 }
 
-// One token's choice by a single wave, from its E logits.  An expert's key is
-// its logit's bits in an order-preserving form, the lowest eleven bits of the
-// fraction giving way to the expert's number (equals: the lowest first; a NaN
-// lowest).  Returns the expert of rank n - 1; with `chosen`, n numbers of LDS,
-// the whole choice of n experts is written to ids and weights.  E <= 64 B.
+// A token's choice by a single wave.  An expert's key is its logit's bits in
+// an order-preserving form, the lowest eleven bits of the fraction giving way
+// to the expert's number (equals: the lowest first; a NaN lowest).
 __device__ __forceinline__ uint64_t max64_lanes(uint64_t v) {
   auto step = [&](uint64_t o) __device__ { v = o > v ? o : v; };
   auto dpp = [&](auto c) __device__ {
@@ -102,43 +100,51 @@ __device__ __forceinline__ uint64_t max64_lanes(uint64_t v) {
        __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false));
   return v;
 }
+__device__ __forceinline__ uint64_t route_key(double l, int e) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, l);
+  const uint64_t o = l != l ? 0 : (u >> 63) ? ~u : u | 0x8000000000000000ull;
+  return (o & ~2047ull) | (uint64_t)(kMaxExperts - e);
+}
+// the expert of rank n - 1 by its key (keys of experts lane, lane + 64, ...);
+// with `chosen`, all n
 template <int B>
-__device__ __forceinline__ int choose_one(const double* lg, int E, int n, int lane, int renorm, int* chosen,
-                                          int* __restrict__ ids, float* __restrict__ weights) {
-  uint64_t key[B];  // of experts lane, lane + 64, ...
-#pragma unroll
-  for (int b = 0; b < B; ++b) {
-    const int i = 64 * b + lane;
-    const double l = lg[min(i, E - 1)];
-    const uint64_t u = __builtin_bit_cast(uint64_t, l);
-    const uint64_t o = l != l ? 0 : (u >> 63) ? ~u : u | 0x8000000000000000ull;
-    key[b] = i < E ? (o & ~2047ull) | (uint64_t)(64 * B - i) : 0;
-  }
+__device__ __forceinline__ int choose_rank(uint64_t (&key)[B], int n, int lane, int* chosen) {
   int e = 0;
   for (int j = 0; j < n; ++j) {
     uint64_t best = key[0];
 #pragma unroll
     for (int b = 1; b < B; ++b) best = key[b] > best ? key[b] : best;
     best = max64_lanes(best);
-    e = 64 * B - (int)((uint32_t)best & 2047u);
+    e = kMaxExperts - (int)((uint32_t)best & 2047u);
 #pragma unroll
     for (int b = 0; b < B; ++b) key[b] = key[b] == best ? 0 : key[b];
     if (chosen != nullptr && lane == 0) chosen[j] = e;
   }
-  if (chosen != nullptr) {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    // the softmax runs over the chosen experts, or over all
-    const double top = lg[chosen[0]];
-    double sum = 0.0;
-    for (int i = lane; i < (renorm ? n : E); i += 64) sum += exp(lg[renorm ? chosen[i] : i] - top);
-    sum = sum64_lanes(sum);
-    for (int j = lane; j < n; j += 64) {
-      ids[j] = chosen[j];
-      weights[j] = (float)(exp(lg[chosen[j]] - top) / sum);
-    }
-  }
   return e;
+}
+// a token's choice of n experts, from its E <= 64 B logits; chosen: n numbers of LDS
+template <int B>
+__device__ __forceinline__ void choose_one(const double* lg, int E, int n, int lane, int renorm, int* chosen,
+                                           int* __restrict__ ids, float* __restrict__ weights) {
+  uint64_t key[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const int i = 64 * b + lane;
+    const uint64_t k = route_key(lg[min(i, E - 1)], i);
+    key[b] = i < E ? k : 0;
+  }
+  choose_rank<B>(key, n, lane, chosen);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  // the softmax runs over the chosen experts, or over all
+  const double top = lg[chosen[0]];
+  double sum = 0.0;
+  for (int i = lane; i < (renorm ? n : E); i += 64) sum += exp(lg[renorm ? chosen[i] : i] - top);
+  sum = sum64_lanes(sum);
+  for (int j = lane; j < n; j += 64) {
+    ids[j] = chosen[j];
+    weights[j] = (float)(exp(lg[chosen[j]] - top) / sum);
+  }
 }
 
 // Small routers: one workgroup per token makes the logits and the choice
@@ -278,8 +284,8 @@ __device__ __forceinline__ u32x4_t to_paired(u32x4_t v) {
 //   * Scales: every second stage lane r loads the eight of the wave's row r,
 //     16 bytes from the dword that holds the first, and the dword behind
 //     them where rows of an odd number of groups start in the middle of one.
-//   * Activations, GP = 1 (NT tiles of 16 activation rows): four lanes load
-//     from one row; a lane exchange hands them over.
+//   * Activations, GP = 1 (up to 16 activation rows): four lanes load from
+//     one row; a lane exchange hands them over.
 //   * Activations, GP = 2 or 4 (at most 8 or 4 activation rows): a tile's 16
 //     rows are those rows times GP scale groups, zero but for the products
 //     of the own group.  A product of GP groups' codes with such operands
@@ -298,9 +304,9 @@ __device__ __forceinline__ int code_read(int li, int lq, int g) {
   return li * 128 + 16 * ((2 * g + (lq >> 1)) ^ (li & 7)) + 8 * (lq & 1);
 }
 
-template <int NT, int GP>
+template <int GP>
 struct Acts {
-  u32x4_t v[NT][8 / GP];
+  u32x4_t v[8 / GP];
 };
 
 // The scales of a wave's rows: 16 RT rows of one plane (and, gate and up, of
@@ -418,18 +424,15 @@ __device__ __forceinline__ uint32_t act_offset(uint32_t row, int K, int lane) {
   return row * (uint32_t)K * 2u + (GP == 1 ? 32u * (lane & 3) : 32u * lq + 128u * (li / (16 / GP)));
 }
 
-// acc[nt][r][i] = the sums over stages sb .. se - 1 of activation row
-// 16 nt + 4 lq + i (GP > 1: of group (4 lq + i) / MT of row (4 lq + i) % MT)
-// and weight row li of row tile r.  rc: the row tiles' codes, slot0 and
-// slot1: the wave's ring.
-template <int NT, int GP, int R, bool DOWN>
+// acc[r][i] = the sums over stages sb .. se - 1 of activation row 4 lq + i
+// (GP > 1: of group (4 lq + i) / MT of row (4 lq + i) % MT) and weight row li
+// of row tile r.  rc: the row tiles' codes, slot0 and slot1: the wave's ring.
+template <int GP, int R, bool DOWN>
 __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScales<R, DOWN>& rs, rsrc_t rx,
-                                            const uint32_t (&x_off)[NT], uint8_t* slot0, uint8_t* slot1, int K, int sb,
-                                            int se, int lane, f32x4_t (&acc)[NT][R]) {
-  static_assert(GP == 1 || NT == 1, "packed groups take one tile");
-  constexpr int MT = 16 / GP;                 // activation rows of a tile
-  constexpr int LOADS = 2 * R + NT * 8 / GP;  // of one stage, the scales not counted
-  constexpr bool PAIRED = DOWN || NT == 1;    // code order of the products (x is permuted into it up to one tile)
+                                            uint32_t x_off, uint8_t* slot0, uint8_t* slot1, int K, int sb,
+                                            int se, int lane, f32x4_t (&acc)[R]) {
+  constexpr int MT = 16 / GP;            // activation rows of a tile
+  constexpr int LOADS = 2 * R + 8 / GP;  // of one stage, the scales not counted
   const int li = lane & 15, lq = lane >> 4, G = K >> 6;
   const uint32_t crow = (uint32_t)K >> 1;
   const uint32_t c_off = code_offset(crow, lane);
@@ -438,13 +441,11 @@ __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScal
   for (int g = 0; g < 4; ++g) rd[g] = code_read(li, lq, g);
   const int xsrc4 = (4 * li + lq) * 4;  // the lane holding this lane's activations after an exchange (byte address)
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int r = 0; r < R; ++r) acc[nt][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   // (a stage past the wave's share and groups past K: offsets past every
   // range, which read as zeros)
-  auto load = [&](Acts<NT, GP>& L, uint8_t* ring, int s) __device__ {
+  auto load = [&](Acts<GP>& L, uint8_t* ring, int s) __device__ {
     const uint32_t away = s < se ? 0u : kNowhere;
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -456,16 +457,13 @@ __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScal
 #pragma unroll
     for (int g = 0; g < 4 / GP; ++g) {
       const uint32_t away_g = s < se && 4 * s + GP * g + (GP == 1 ? 0 : li / MT) < G ? 0u : kNowhere;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t o = (x_off[nt] + 512u * (uint32_t)s) | away_g;
-        L.v[nt][2 * g] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g, 0, 0);
-        L.v[nt][2 * g + 1] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g + 16, 0, 0);
-      }
+      const uint32_t o = (x_off + 512u * (uint32_t)s) | away_g;
+      L.v[2 * g] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g, 0, 0);
+      L.v[2 * g + 1] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 128 * GP * g + 16, 0, 0);
     }
     in_order();
   };
-  auto compute = [&](const Acts<NT, GP>& L, const uint8_t* ring, uint32_t d0, uint32_t d1, int s) __device__ {
+  auto compute = [&](const Acts<GP>& L, const uint8_t* ring, uint32_t d0, uint32_t d1, int s) __device__ {
     const u32x4_t eights = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     uint32_t sc[R][2];
@@ -476,38 +474,31 @@ __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScal
     }
     auto codes = [&](int r, int g, u32x4_t (&w)[2]) __device__ {
       const u32x2_t cw = *reinterpret_cast<const u32x2_t*>(ring + rd[g] + r * kTileStage);
-      w[0] = PAIRED ? q4_paired(cw.x) : q4_natural(cw.x);
-      w[1] = PAIRED ? q4_paired(cw.y) : q4_natural(cw.y);
+      w[0] = q4_paired(cw.x);
+      w[1] = q4_paired(cw.y);
     };
     if constexpr (GP == 1) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         if (g > 0 && 4 * s + g >= G) break;
-        u32x4_t x[NT][2];
-        f32x4_t cr[NT];
+        u32x4_t x[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            x[nt][h] = lane_piece(L.v[nt][2 * g + h], xsrc4);
-            if constexpr (PAIRED && !DOWN) x[nt][h] = to_paired(x[nt][h]);
-          }
-          cr[nt] = mfma(x[nt][0], eights, zero);
-          cr[nt] = mfma(x[nt][1], eights, cr[nt]);
+        for (int h = 0; h < 2; ++h) {
+          x[h] = lane_piece(L.v[2 * g + h], xsrc4);
+          if constexpr (!DOWN) x[h] = to_paired(x[h]);
         }
+        f32x4_t cr = mfma(x[0], eights, zero);
+        cr = mfma(x[1], eights, cr);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           u32x4_t w[2];
           codes(r, g, w);
           const uint32_t sb16 = (g & 1) ? sc[r][g >> 1] >> 16 : sc[r][g >> 1] & 0xFFFFu;
           const float sv = f16_bits_to_f32((uint16_t)sb16);
+          f32x4_t p = mfma(x[0], w[0], zero);
+          p = mfma(x[1], w[1], p);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            f32x4_t p = mfma(x[nt][0], w[0], zero);
-            p = mfma(x[nt][1], w[1], p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][r][i] = __builtin_fmaf(sv, p[i] - cr[nt][i], acc[nt][r][i]);
-          }
+          for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(sv, p[i] - cr[i], acc[r][i]);
         }
       }
     } else {
@@ -517,7 +508,7 @@ __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScal
         f32x4_t cr = zero;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x4_t v = DOWN ? L.v[0][2 * g + h] : to_paired(L.v[0][2 * g + h]);
+          const u32x4_t v = DOWN ? L.v[2 * g + h] : to_paired(L.v[2 * g + h]);
 #pragma unroll
           for (int j = 0; j < GP; ++j)
 #pragma unroll
@@ -542,12 +533,12 @@ __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScal
             p = mfma(x[j][1], w[1], p);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[0][r][i] = __builtin_fmaf(sv, p[i] - cr[i], acc[0][r][i]);
+          for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(sv, p[i] - cr[i], acc[r][i]);
         }
       }
     }
   };
-  Acts<NT, GP> L[2];
+  Acts<GP> L[2];
   typename RowScales<R, DOWN>::Regs S;
   rs.load(S, sb, se);
   load(L[0], slot0, sb);
@@ -575,25 +566,75 @@ __device__ __forceinline__ void stream_sums(const rsrc_t (&rc)[R], const RowScal
   in_order();
 }
 
-// The gate and up products of one token choose their expert themselves
-constexpr int kOneExperts = 256;  // at most
-struct OneToken {
+// A few tokens' choice, made where it is used: the logits [T][E], and where
+// the choice goes
+constexpr int kFewTokens = 8;         // at most,
+constexpr int kFewExperts = 256;      // of so many experts,
+struct Choice {
   const double* lg;
   int* ids;
   float* weights;
-  int renorm;
+  int T, renorm;
 };
+
+// The expert e of pair (blockIdx.y / top_k, blockIdx.y % top_k) and the pairs
+// that chose it, in order, into the wave's list; returns how many, 0 if an
+// earlier token chose it (whose workgroups serve it).
+template <int FT>
+__device__ __forceinline__ int choose_pairs(const Choice& c, int E, int top_k, int lane, int* list, int& e) {
+  constexpr int B = kFewExperts / 64;
+  uint64_t key[FT][B];  // (every token's loads in flight; tokens past T repeat the last)
+#pragma unroll
+  for (int t = 0; t < FT; ++t)
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = 64 * b + lane;
+      const uint64_t k = route_key(c.lg[(size_t)min(t, c.T - 1) * E + min(i, E - 1)], i);
+      key[t][b] = i < E ? k : 0;
+    }
+  const int mine = blockIdx.y / top_k;
+  uint64_t own[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    own[b] = key[0][b];
+#pragma unroll
+    for (int t = 1; t < FT; ++t) own[b] = t == mine ? key[t][b] : own[b];
+  }
+  e = choose_rank<B>(own, blockIdx.y - mine * top_k + 1, lane, nullptr);
+  int m = 0;
+  bool served = false;
+#pragma unroll
+  for (int t = 0; t < FT; ++t) {
+    uint64_t mk = key[t][0];
+#pragma unroll
+    for (int b = 1; b < B; ++b) mk = e >> 6 == b ? key[t][b] : mk;
+    const uint64_t ke = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mk, e & 63) |
+                        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(mk >> 32), e & 63) << 32);
+    int rank = 0;
+#pragma unroll
+    for (int b = 0; b < B; ++b) rank += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[t][b] > ke));
+    if (t < c.T && rank < top_k) {
+      served |= t < mine;
+      if (lane == 0) list[m] = t * top_k + rank;
+      ++m;
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return served ? 0 : m;
+}
 
 // The gate and up products of experts with few rows each, and the gate: h in
 // two parts, [pair][part][rows] in the paired order.  K: of the products,
 // rows: of h, wk: waves that share K (the other kWaves / wk share the
-// workgroup's rows).
-template <int R, bool ONE>
+// workgroup's rows).  CHOOSE: tokens whose choice is made here, at most (0:
+// ids hold it).
+template <int R, int CHOOSE>
 __global__ void __launch_bounds__(kThreads, 2)
 moe_gated_kernel(const uint16_t* x, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
                  const uint16_t* scales1, const int* __restrict__ ids, uint16_t* h, int K, int rows, int E, int P,
-                 int top_k, uint32_t x_bytes, int wk, OneToken one) {
-  constexpr int BT = 32;                // pairs per pass, at most
+                 int top_k, uint32_t x_bytes, int wk, Choice choice) {
+  constexpr int BT = 16;                // pairs per pass, at most
   constexpr int RT = R / 2;             // row tiles of h per wave
   constexpr int SLOT = R * kTileStage;  // bytes of one stage's codes
   typedef float Red[R][16][20];
@@ -603,19 +644,23 @@ moe_gated_kernel(const uint16_t* x, const uint8_t* codes0, const uint16_t* scale
   __shared__ __attribute__((aligned(16))) uint8_t ring0[kWaves * SLOT];
   __shared__ __attribute__((aligned(16))) uint8_t ring1[kWaves * SLOT];
   __shared__ int list[kWaves][BT];
-  static_assert(!ONE || kWaves * BT >= kPairGrid, "the single token's choice fits the lists");
+  __shared__ int chosen[CHOOSE ? kWaves : 1][CHOOSE ? kPairGrid : 1];
+  static_assert(CHOOSE <= BT, "one pass");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int wr = kWaves / wk, kp = wave % wk, rp = wave / wk;
 
-  int e = blockIdx.y;
-  if constexpr (ONE) {
-    if (e == P) {  // (a workgroup of its own writes the choice)
-      if (blockIdx.x == 0 && wave == 0)
-        choose_one<kOneExperts / 64>(one.lg, E, P, lane, one.renorm, &list[0][0], one.ids, one.weights);
+  int e, m = 1;
+  if constexpr (CHOOSE > 0) {
+    if ((int)blockIdx.y == P) {  // (a workgroup of its own writes the choice)
+      if (blockIdx.x > 0) return;
+      for (int t = wave; t < choice.T; t += kWaves)
+        choose_one<kFewExperts / 64>(choice.lg + (size_t)t * E, E, top_k, lane, choice.renorm, chosen[wave],
+                                     choice.ids + (size_t)t * top_k, choice.weights + (size_t)t * top_k);
       return;
     }
-    e = choose_one<kOneExperts / 64>(one.lg, E, e + 1, lane, 0, nullptr, nullptr, nullptr);
+    m = choose_pairs<CHOOSE>(choice, E, top_k, lane, list[wave], e);
+    if (m == 0) return;
   } else {
     e = block_expert(ids, P, E, lane);
     if (e < 0) return;
@@ -637,94 +682,77 @@ moe_gated_kernel(const uint16_t* x, const uint8_t* codes0, const uint16_t* scale
 
   // One pass over the wave's share of K for the mr activation rows of the
   // list, then the workgroup's sums
-  auto pass = [&](auto ntc, auto gpc, int mr) __device__ {
-    constexpr int NT = decltype(ntc)::value, GP = decltype(gpc)::value;
-    constexpr int MT = 16 / GP;  // activation rows of a tile
-    uint32_t x_off[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int a = GP == 1 ? 16 * nt + (lane >> 2) : li % MT;
-      // (rows past the last read as zeros)
-      x_off[nt] = a < mr ? act_offset<GP>((uint32_t)(list[wave][min(a, mr - 1)] / top_k), K, lane) : kNowhere;
-    }
-    f32x4_t acc[NT][R];
-    stream_sums<NT, GP, R, false>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
+  auto pass = [&](auto gpc, int mr) __device__ {
+    constexpr int GP = decltype(gpc)::value, MT = 16 / GP;
+    const int a = GP == 1 ? lane >> 2 : li % MT;
+    // (rows past the last read as zeros)
+    const uint32_t x_off = a < mr ? act_offset<GP>((uint32_t)(list[wave][min(a, mr - 1)] / top_k), K, lane) : kNowhere;
+    f32x4_t acc[R];
+    stream_sums<GP, R, false>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
 
-    // the sums of the waves that share K (and of a tile's groups)
+    // the sums of the waves that share K and of a tile's groups
+    Red& red = *reinterpret_cast<Red*>(ring0 + wave * SLOT);
+    if (4 * lq % MT < mr)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (MT * nt >= mr) break;
-      if (nt > 0) __syncthreads();
-      Red& red = *reinterpret_cast<Red*>(ring0 + wave * SLOT);
-      if (MT * nt + 4 * lq % MT < mr)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int i = 0; i < 4; ++i) red[r][4 * lq + i][li] = acc[r][i];
+    __syncthreads();
+    const int tiles = wr * RT;
+    for (int o = tid; o < 16 * tiles * mr; o += kThreads) {
+      const int c = o & 15, tile = (o >> 4) % tiles, t = (o >> 4) / tiles;
+      const int w0 = tile / RT * wk, r = tile % RT, n = (blockIdx.x * tiles + tile) * 16 + c;
+      if (n >= rows) continue;
+      auto sum = [&](int rr) __device__ {
+        double v = 0.0;
+        for (int w = 0; w < wk; ++w)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) red[r][4 * lq + i][li] = acc[nt][r][i];
-      __syncthreads();
-      const int tiles = wr * RT, pairs = min(MT, mr - MT * nt);
-      for (int o = tid; o < 16 * tiles * pairs; o += kThreads) {
-        const int c = o & 15, tile = (o >> 4) % tiles, t = (o >> 4) / tiles;
-        const int w0 = tile / RT * wk, r = tile % RT, n = (blockIdx.x * tiles + tile) * 16 + c;
-        if (n >= rows) continue;
-        const int p = list[wave][MT * nt + t];
-        auto sum = [&](int rr, int tt) __device__ {
-          double v = 0.0;
-          for (int w = 0; w < wk; ++w)
-#pragma unroll
-            for (int j = 0; j < GP; ++j)
-              v += (double)(*reinterpret_cast<const Red*>(ring0 + (w0 + w) * SLOT))[rr][MT * j + tt][c];
-          return v;
-        };
-        store_gated((float)sum(r, t), (float)sum(RT + r, t), h, p, rows, n);
-      }
+          for (int j = 0; j < GP; ++j)
+            v += (double)(*reinterpret_cast<const Red*>(ring0 + (w0 + w) * SLOT))[rr][MT * j + t][c];
+        return v;
+      };
+      store_gated((float)sum(r), (float)sum(RT + r), h, list[wave][t], rows, n);
     }
   };
 
-  int m = 1;
   for (int b0 = 0; b0 < m; b0 += BT) {
-    if constexpr (ONE) {
-      list[wave][0] = blockIdx.y;
-      pass(Slot<1>{}, Slot<4>{}, 1);
-      return;
+    if constexpr (CHOOSE == 0) {
+      m = list_pairs<BT>(ids, P, e, b0, lane, list[wave]);
+      if (m == 0) return;
     }
-    m = list_pairs<BT>(ids, P, e, b0, lane, list[wave]);
-    if (m == 0) return;
     const int mr = min(BT, m - b0);
     // the smallest tiles that hold the rows
-    if (mr <= 4) pass(Slot<1>{}, Slot<4>{}, mr);
-    else if (mr <= 8) pass(Slot<1>{}, Slot<2>{}, mr);
-    else if (mr <= 16) pass(Slot<1>{}, Slot<1>{}, mr);
-    else pass(Slot<2>{}, Slot<1>{}, mr);
+    if (mr <= 4) pass(Slot<4>{}, mr);
+    else if (mr <= 8) pass(Slot<2>{}, mr);
+    else pass(Slot<1>{}, mr);
     __syncthreads();
   }
 }
 
-// The down products of a single token and their weighted sum in one launch: a
-// workgroup of 16 waves takes 16 R rows; its waves share the chosen experts
-// and, where there are fewer than waves, each expert's K.
-constexpr int kOneWaves = 16;
+// The down products of a few pairs and their weighted sums in one launch: a
+// workgroup of 16 waves takes 16 R rows of y; its waves share the pairs and,
+// where there are fewer than waves, each pair's K.  (An expert that several
+// tokens chose is read again for each, by the same workgroup.)
+constexpr int kFewWaves = 16;
 template <int R>
-__global__ void __launch_bounds__(64 * kOneWaves)
-moe_down_one_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* scales, const int* __restrict__ ids,
-                    const float* __restrict__ weights, uint16_t* y, int K, int rows, int E, int P,
-                    uint32_t act_bytes) {
+__global__ void __launch_bounds__(64 * kFewWaves)
+moe_down_few_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* scales, const int* __restrict__ ids,
+                    const float* __restrict__ weights, uint16_t* y, int K, int rows, int E, int T, int top_k,
+                    uint32_t h_bytes) {
   constexpr int SLOT = R * kTileStage;
-  __shared__ __attribute__((aligned(16))) uint8_t ring0[kOneWaves * SLOT];
-  __shared__ __attribute__((aligned(16))) uint8_t ring1[kOneWaves * SLOT];
-  __shared__ float red[kOneWaves][R][16];
+  __shared__ __attribute__((aligned(16))) uint8_t ring0[kFewWaves * SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t ring1[kFewWaves * SLOT];
+  __shared__ float sums[kFewWaves][kFewTokens][16 * R];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.x * (16 * R);
+  const int n0 = blockIdx.x * (16 * R), P = T * top_k;
   const int G = K >> 6, stages = (G + 3) >> 2;
-  const int wpp = P < kOneWaves ? kOneWaves / P : 1;  // waves per pair
+  const int wpp = P < kFewWaves ? kFewWaves / P : 1;  // waves per pair
   const uint32_t crow = (uint32_t)K >> 1;
-  const rsrc_t rx = make_rsrc(h, act_bytes);
-  float sum[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) sum[r] = 0.f;
+  const rsrc_t rx = make_rsrc(h, h_bytes);
+  for (int i = lane; i < kFewTokens * 16 * R; i += 64) (&sums[wave][0][0])[i] = 0.f;
   const int part = wave % wpp, sb = stages * part / wpp, se = stages * (part + 1) / wpp;
-  for (int p = wave / wpp; p < P; p += kOneWaves / wpp) {
+  for (int p = wave / wpp; p < P; p += kFewWaves / wpp) {
     const int e = __builtin_amdgcn_readfirstlane(ids[p]);
     if ((uint32_t)e >= (uint32_t)E || sb >= se) continue;
     const float wp = weights[p];
@@ -736,25 +764,25 @@ moe_down_one_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* sca
     }
     const RowScales<R, true> rs(scales, scales, ((size_t)e * rows + n0) * G, min(16 * R, rows - n0), G, lane);
     const int a = li % 4;  // the pair's two parts
-    const uint32_t x_off[1] = {a < 2 ? act_offset<4>(2u * p + a, K, lane) : kNowhere};
-    f32x4_t acc[1][R];
-    stream_sums<1, 4, R, true>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
+    const uint32_t x_off = a < 2 ? act_offset<4>(2u * p + a, K, lane) : kNowhere;
+    f32x4_t acc[R];
+    stream_sums<4, R, true>(rc, rs, rx, x_off, ring0 + wave * SLOT, ring1 + wave * SLOT, K, sb, se, lane, acc);
+    // this lane: row li, group lq of every stage
 #pragma unroll
-    for (int r = 0; r < R; ++r) sum[r] = __builtin_fmaf(wp, acc[0][r][0] + acc[0][r][1], sum[r]);
-  }
-  // this lane: row li, group lq of every stage
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float v = sum[r];
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    if (lq == 0) red[wave][r][li] = v;
+    for (int r = 0; r < R; ++r) {
+      float v = acc[r][0] + acc[r][1];
+      v += __shfl_xor(v, 16);
+      v += __shfl_xor(v, 32);
+      if (lq == 0) sums[wave][p / top_k][16 * r + li] = __builtin_fmaf(wp, v, sums[wave][p / top_k][16 * r + li]);
+    }
   }
   __syncthreads();
-  if (tid < 16 * R && n0 + tid < rows) {
+  for (int i = tid; i < T * 16 * R; i += 64 * kFewWaves) {
+    const int t = i / (16 * R), r = i % (16 * R);
+    if (n0 + r >= rows) continue;
     double v = 0.0;
-    for (int w = 0; w < kOneWaves; ++w) v += (double)red[w][tid >> 4][tid & 15];
-    y[n0 + tid] = f32_to_bf16_rne((float)v);
+    for (int w = 0; w < kFewWaves; ++w) v += (double)sums[w][t][r];
+    y[(size_t)t * rows + n0 + r] = f32_to_bf16_rne((float)v);
   }
 }
 
@@ -1010,12 +1038,11 @@ size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 constexpr int kRowTiles = 4;      // per wave (gate and up of few rows)
 constexpr int kWideRowTiles = 2;  // per wave (workgroups that share the activations)
-constexpr int kOneRowTiles = 2;   // of a single token's down products
 // Pairs per expert in use from which the gate and up products share the
 // activations in workgroups (24 of them on eight experts of 2 x 14336 x 5120:
 // 194 us against 222; 4 on 128 of 2 x 768 x 2048 58 either way; 4 on 16 of
 // 2 x 1536 x 5120 45 against 41).
-constexpr int64_t kWideGate = 20;
+constexpr int64_t kWideGate = 18;
 // workgroups that the chip holds at a time (two per CU, by LDS and registers)
 constexpr int64_t kResident = 512;
 
@@ -1041,18 +1068,25 @@ int64_t experts_hit(const MoeArgs& a) {
 }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Whether one launch makes the down products and their sums: a single token,
+// or a few that share few experts (16 waves for every 16 or 32 rows of y; two
+// launches fewer, but an expert is read again for every token that chose it)
+bool few_pairs(const MoeArgs& a) {
+  return a.t == 1 || (a.t <= kFewTokens && a.t * a.top_k <= kPairGrid && 2 * a.t * a.top_k <= a.experts);
+}
 // parts of the down products' sums
 int down_parts(const MoeArgs& a) {
   return k_split(ceil_div(a.k, kWideWaves * 16 * kWideRowTiles) * experts_hit(a), ceil_div(a.inner, 128), 4, 8, false);
 }
 
 hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t s) {
+  // (lg: the choice is made here)
   const int P = (int)(a.t * a.top_k);
   const unsigned slots = (unsigned)(P <= kPairGrid ? P : a.experts);
   auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
   const uint32_t x_bytes = (uint32_t)(a.t * a.k * 2);
-  if (P / experts_hit(a) >= kWideGate) {
+  if (lg == nullptr && P / experts_hit(a) >= kWideGate) {
     constexpr int R = kWideRowTiles;
     const dim3 grid((unsigned)ceil_div(a.inner, kWideWaves * 8 * R), slots);
     moe_wide_kernel<R, false><<<grid, dim3(64 * kWideWaves), 0, s>>>(
@@ -1067,10 +1101,12 @@ hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t
     kern<<<dim3(blocks, rows), dim3(kThreads), 0, s>>>(
         u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up),
         static_cast<const int*>(a.ids), static_cast<uint16_t*>(h), (int)a.k, (int)a.inner, (int)a.experts, P,
-        (int)a.top_k, x_bytes, wk, OneToken{lg, static_cast<int*>(a.ids), static_cast<float*>(a.weights), a.renorm});
+        (int)a.top_k, x_bytes, wk,
+        Choice{lg, static_cast<int*>(a.ids), static_cast<float*>(a.weights), (int)a.t, a.renorm});
   };
-  if (lg != nullptr) go(moe_gated_kernel<R, true>, slots + 1);
-  else go(moe_gated_kernel<R, false>, slots);
+  if (lg == nullptr) go(moe_gated_kernel<R, 0>, slots);
+  else if (a.t == 1) go(moe_gated_kernel<R, 1>, slots + 1);
+  else go(moe_gated_kernel<R, kFewTokens>, slots + 1);
   return hipGetLastError();
 }
 
@@ -1122,10 +1158,10 @@ size_t moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t to
   const size_t route = moe_route_workspace_bytes(k, experts, t);
   MoeArgs a{};
   a.inner = inner, a.k = k, a.experts = experts, a.top_k = top_k, a.t = t;
-  const size_t sums = t == 1 ? 0 : (size_t)down_parts(a) * (size_t)(t * top_k * k * 4);
-  // (a single token's logits lie where the sums would)
-  const size_t one = t == 1 ? (size_t)experts * 8 : 0;
-  const size_t all = al256((size_t)(t * top_k * inner * 4)) + al256(sums > one ? sums : one);
+  const size_t sums = few_pairs(a) ? 0 : (size_t)down_parts(a) * (size_t)(t * top_k * k * 4);
+  // (a few tokens' logits lie where the sums would)
+  const size_t lg = t <= kFewTokens ? (size_t)(t * experts * 8) : 0;
+  const size_t all = al256((size_t)(t * top_k * inner * 4)) + al256(sums > lg ? sums : lg);
   return route > all ? route : all;
 }
 
@@ -1138,12 +1174,17 @@ hipError_t launch_moe_experts(const MoeArgs& a, const double* lg, void* workspac
   const int* ids = static_cast<const int*>(a.ids);
   const float* weights = static_cast<const float*>(a.weights);
   uint16_t* y = static_cast<uint16_t*>(a.y);
-  if (a.t == 1) {
-    moe_down_one_kernel<kOneRowTiles><<<dim3((unsigned)((a.k + 16 * kOneRowTiles - 1) / (16 * kOneRowTiles))),
-                                        dim3(64 * kOneWaves), 0, s>>>(
-        static_cast<const uint16_t*>(h), static_cast<const uint8_t*>(a.codes_down),
-        static_cast<const uint16_t*>(a.scales_down), ids, weights, y, (int)a.inner, (int)a.k, (int)a.experts,
-        (int)a.top_k, (uint32_t)h_bytes);
+  if (few_pairs(a)) {
+    // 32 rows a workgroup where that is half a workgroup per CU or more
+    const bool two = a.k >= 32 * 128;
+    auto go = [&](auto kern) {
+      kern<<<dim3((unsigned)ceil_div(a.k, two ? 32 : 16)), dim3(64 * kFewWaves), 0, s>>>(
+          static_cast<const uint16_t*>(h), static_cast<const uint8_t*>(a.codes_down),
+          static_cast<const uint16_t*>(a.scales_down), ids, weights, y, (int)a.inner, (int)a.k, (int)a.experts,
+          (int)a.t, (int)a.top_k, (uint32_t)h_bytes);
+    };
+    if (two) go(moe_down_few_kernel<2>);
+    else go(moe_down_few_kernel<1>);
     return hipGetLastError();
   }
   e = launch_down(a, h, parts, s);
@@ -1160,16 +1201,16 @@ hipError_t launch_moe_experts(const MoeArgs& a, void* workspace, hipStream_t s) 
   return launch_moe_experts(a, nullptr, workspace, s);
 }
 
-// The whole layer.  A single token's logits lie behind h and the choice is
-// made where it is used (every workgroup of the gate and up products makes
-// it for itself): two launches fewer.
+// The whole layer.  A few tokens' logits lie behind h and the choice is made
+// where it is used (every workgroup of the gate and up products makes it for
+// itself): a launch fewer.
 hipError_t launch_moe(const MoeArgs& a, void* workspace, hipStream_t s) {
-  if (a.t > 1 || a.experts > kOneExperts || a.top_k > kPairGrid) {
+  if (a.t > kFewTokens || a.experts > kFewExperts || a.t * a.top_k > kPairGrid) {
     const hipError_t e = launch_moe_route(a, workspace, s);
     return e == hipSuccess ? launch_moe_experts(a, nullptr, workspace, s) : e;
   }
-  double* lg = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + al256((size_t)(a.top_k * a.inner * 4)));
-  moe_one_logit_kernel<<<dim3((unsigned)a.experts), dim3(256), 0, s>>>(
+  double* lg = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + al256((size_t)(a.t * a.top_k * a.inner * 4)));
+  moe_one_logit_kernel<<<dim3((unsigned)a.experts, (unsigned)a.t), dim3(256), 0, s>>>(
       static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.router), lg, (int)a.k, (int)a.experts);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? launch_moe_experts(a, lg, workspace, s) : e;

@@ -15,6 +15,7 @@ caller does not pass them, and calls ``q4lin_linear`` on the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -208,6 +209,7 @@ def q4lin_linear_lora(fmt: int, x: int, w: int, w_hi: int, scales: int, lora_a: 
                                         n, k, t, adapters, rank, workspace, workspace_bytes, stream))
 
 
+@functools.lru_cache(maxsize=4096)
 def q4lin_lora_workspace_bytes(fmt: int, n: int, k: int, t: int, adapters: int, rank: int) -> int:
     return int(load().q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank))
 
@@ -236,6 +238,7 @@ def q4lin_moe_experts(x: int, ids: int, weights: int, codes_gate: int, scales_ga
                                         stream))
 
 
+@functools.lru_cache(maxsize=4096)
 def q4lin_moe_workspace_bytes(inner: int, k: int, experts: int, top_k: int, t: int) -> int:
     return int(load().q4lin_moe_workspace_bytes(inner, k, experts, top_k, t))
 
@@ -462,6 +465,15 @@ _FMT_PLANES = {  # bytes per row of K weights: codes, high plane, scales
 }
 
 
+def _plane(name, ten, rows, per_row):
+    """The address of a weight's plane (None: the format has none)."""
+    if per_row == 0:
+        return None
+    if ten is None or not ten.is_contiguous() or ten.numel() * ten.element_size() != rows * per_row:
+        raise ValueError("%s must be a contiguous plane of %d bytes for each of the %d rows" % (name, per_row, rows))
+    return ten.data_ptr()
+
+
 def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, fmt=Q4LIN_FMT_Q4G64_F16S,
                 codes_hi=None, y=None, workspace=None, stream=None):
     """Y = W x X plus each token's own low-rank adapter, on torch device
@@ -481,27 +493,25 @@ def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, 
     adapters, rank = lora_a.shape[0], lora_a.shape[1]
     if fmt not in _FMT_PLANES:
         raise Q4LinError(Q4LIN_E_FORMAT)
-    ptr = []
-    for name, ten, per_row in zip(("codes", "codes_hi", "scales"), (codes, codes_hi, scales), _FMT_PLANES[fmt](k)):
-        if per_row == 0:
-            ptr.append(None)
-            continue
-        if ten is None or not ten.is_contiguous() or ten.numel() * ten.element_size() != n * per_row:
-            raise ValueError("%s must be a contiguous plane of %d bytes for each of the %d rows" % (name, per_row, n))
-        ptr.append(ten.data_ptr())
+    per_row = _FMT_PLANES[fmt](k)
+    wp = _plane("codes", codes, n, per_row[0])
+    hp = _plane("codes_hi", codes_hi, n, per_row[1])
+    cp = _plane("scales", scales, n, per_row[2])
     xp = _checked("x", x, (t, k), 2)
     ap = _checked("lora_a", lora_a, (adapters, rank, k), 2)
     bp = _checked("lora_b", lora_b, (adapters, n, rank), 2)
     ip = _checked("adapter_ids", adapter_ids, (t,), 4)
     sp = _checked("lora_scale", lora_scale, (adapters,), 4) if lora_scale is not None else None
+    device = x.device
     if y is None:
-        y = _new((t, n), torch.bfloat16, x.device)
-    yp = _checked("y", y, (t, n), 2)
-    lib = load()
-    wp, wb, workspace = _workspace(lib.q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank), workspace, x.device)
-    stream = _stream_of(stream, x.device, y, workspace)
-    st = lib.q4lin_linear_lora(fmt, xp, ptr[0], ptr[1], ptr[2], ap, bp, sp, ip, yp, n, k, t, adapters, rank, wp, wb,
-                               stream)
+        y = _new((t, n), torch.bfloat16, device)
+        yp = y.data_ptr()
+    else:
+        yp = _checked("y", y, (t, n), 2)
+    work, work_bytes, workspace = _workspace(q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank), workspace, device)
+    stream = _stream_of(stream, device, y, workspace)
+    st = load().q4lin_linear_lora(fmt, xp, wp, hp, cp, ap, bp, sp, ip, yp, n, k, t, adapters, rank, work, work_bytes,
+                                  stream)
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return y
@@ -560,10 +570,9 @@ def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, c
     if y is None:
         y = _new((t, k), torch.bfloat16, x.device)
     yp = _checked("y", y, (t, k), 2)
-    lib = load()
-    wp, wb, workspace = _workspace(lib.q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)
+    wp, wb, workspace = _workspace(q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)
     stream = _stream_of(stream, x.device, y, workspace)
-    st = lib.q4lin_moe_experts(xp, ip, vp, *planes, yp, inner, k, experts, top_k, t, wp, wb, stream)
+    st = load().q4lin_moe_experts(xp, ip, vp, *planes, yp, inner, k, experts, top_k, t, wp, wb, stream)
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return y
@@ -580,15 +589,15 @@ def moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, sca
     xp = _checked("x", x, (t, k), 2)
     experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
     rp = _checked("router", router, (experts, k), 2)
-    ids = _new((t, top_k), torch.int32, x.device)
-    weights = _new((t, top_k), torch.float32, x.device)
+    device = x.device
+    ids = _new((t, top_k), torch.int32, device)
+    weights = _new((t, top_k), torch.float32, device)
     if y is None:
-        y = _new((t, k), torch.bfloat16, x.device)
+        y = _new((t, k), torch.bfloat16, device)
     yp = _checked("y", y, (t, k), 2)
-    lib = load()
-    wp, wb, workspace = _workspace(lib.q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)
-    stream = _stream_of(stream, x.device, y, workspace, ids, weights)
-    st = lib.q4lin_moe(xp, rp, *planes, yp, ids.data_ptr(), weights.data_ptr(), inner, k, experts, top_k, t,
+    wp, wb, workspace = _workspace(q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, device)
+    stream = _stream_of(stream, device, y, workspace, ids, weights)
+    st = load().q4lin_moe(xp, rp, *planes, yp, ids.data_ptr(), weights.data_ptr(), inner, k, experts, top_k, t,
                        1 if renormalize else 0, wp, wb, stream)
     if st != Q4LIN_OK:
         raise Q4LinError(st)

@@ -284,7 +284,7 @@ int lora_plan(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_
               (p->route == Q4LIN_ROUTE_DECODE && q4lin::decode_plan(n, k, t, &dp) && dp.waves == 8);
   }
   p->u_bytes = q4lin::lora_u_bytes(k, t, rank);
-  p->total = p->u_bytes + (p->tail ? 0 : base);
+  p->total = p->u_bytes + base;  // (the sums' room on every route, also where the kernel adds the term itself)
   return Q4LIN_OK;
 }
 

@@ -6,22 +6,29 @@
 //     h_j = silu(Wg_e x) * (Wu_e x),         e = ids[t][j],
 //     y[t] = bf16( sum_j weights[t][j] Wd_e h_j ).
 //
-// A choice (t, j) is a "pair" p = t top_k + j.  Launches: route (one
-// workgroup per token), the gate and up products with the gate applied, the
-// down products of every pair, and their weighted sum per token.  A pair
+// A choice (t, j) is a "pair" p = t top_k + j.  Launches: the
+// logits and the choice (one kernel for small routers), the gate and up
+// products with the gate applied, the down products of every pair, and their
+// weighted sum per token; for a few tokens the choice is made inside the gate
+// and up kernel and the sum inside the down kernel.  A pair
 // whose id is outside 0..E-1 takes part in nothing.
 //
-// Expert products, bound by the weight stream (34 bytes per 64 weights of
-// each expert that some token chose, read once for up to 32 activation
-// rows): a wave takes 64 rows of one expert (32 gate rows and the same 32 up
-// rows, or 64 down rows) and all of its pairs, and streams its share of K
-// through an LDS ring; the four waves of a workgroup share K or the rows.
+// Expert products.  Their floor is the weight stream: 34 bytes per 64 weights
+// of each expert that some token chose.  Three kernels share the arithmetic
+// and differ in what a wave holds (the figures stand at the choices):
+//   gated:    gate and up rows of up to 16 activation rows a pass; the four
+//             waves of a workgroup share K, each with an LDS ring of its own;
+//   down_few: down products of a few tokens, sixteen waves over K, y written
+//             at once: every token reads its experts' rows for itself;
+//   wide:     down products of several tokens, and the gate and up products
+//             where an expert has many pairs: eight waves share the staged
+//             activations, up to 32 activation rows a pass.
 // The arithmetic is that of the library's other matrix-core routes: exact
 // bf16 values 128 + q, products of a constant all-8 operand through the same
 // instructions subtracted, the group's scale applied in binary32; the waves'
-// partials are summed in binary64.  h is kept as two bf16 parts (16
-// significant bits), as two activation rows per pair: one bf16 would cost as
-// much precision as the store of y.
+// partials are summed in a fixed order, so that a call repeats to the bit.
+// h is kept as two bf16 parts (16 significant bits), as two activation rows
+// per pair: one bf16 would cost as much precision as the store of y.
 #include "q4lin_kernels.h"
 #include "q4lin_mfma16.h"
 
@@ -136,14 +143,19 @@ __device__ __forceinline__ void choose_one(const double* lg, int E, int n, int l
   choose_rank<B>(key, n, lane, chosen);
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  // the softmax runs over the chosen experts, or over all
-  const double top = lg[chosen[0]];
-  double sum = 0.0;
-  for (int i = lane; i < (renorm ? n : E); i += 64) sum += exp(lg[renorm ? chosen[i] : i] - top);
+  // the softmax runs over the chosen experts, or over all; lane j: ranks j, j + 64, ...
+  const double l0 = lg[chosen[min(lane, n - 1)]];
+  const uint64_t tb = __builtin_bit_cast(uint64_t, l0);
+  const double top = __builtin_bit_cast(
+      double, (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)tb) |
+                  ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(tb >> 32)) << 32));
+  const double p0 = exp(l0 - top);
+  double sum = renorm && lane < n ? p0 : 0.0;
+  for (int i = renorm ? lane + 64 : lane; i < (renorm ? n : E); i += 64) sum += exp(lg[renorm ? chosen[i] : i] - top);
   sum = sum64_lanes(sum);
   for (int j = lane; j < n; j += 64) {
     ids[j] = chosen[j];
-    weights[j] = (float)(exp(lg[chosen[j]] - top) / sum);
+    weights[j] = (float)((j < 64 ? p0 : exp(lg[chosen[j]] - top)) / sum);
   }
 }
 
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(256)
 moe_logits_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ router, double* __restrict__ lg, int K,
                   int E, int T) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e0 = (blockIdx.x * 4 + wave) * EPW, t0 = blockIdx.y * TPW;
+  const int e0 = (blockIdx.y * 4 + wave) * EPW, t0 = blockIdx.x * TPW;
   if (e0 >= E) return;
   const uint16_t *r[EPW], *xr[TPW];
 #pragma unroll
@@ -1004,6 +1016,7 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
 }
 
 // y[t][n .. n + 3] = bf16( sum_j weights[t][j] sum_k parts[k][t top_k + j][n .. n + 3] ), in order
+template <int J>
 __global__ void __launch_bounds__(256)
 moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids, const float* __restrict__ weights,
                    uint16_t* __restrict__ y, int rows, int E, int top_k, int T, int ks, int vec) {
@@ -1012,15 +1025,29 @@ moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids,
   if (i >= (int64_t)T * per) return;
   const int t = (int)(i / per), n = 4 * (int)(i - (int64_t)t * per);
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < top_k; ++j) {
-    const int p = t * top_k + j;
-    if ((uint32_t)ids[p] >= (uint32_t)E) continue;
-    f32x4_t d = *reinterpret_cast<const f32x4_t*>(parts + (size_t)p * rows + n);
-    for (int k = 1; k < ks; ++k)
-      d += *reinterpret_cast<const f32x4_t*>(parts + ((size_t)k * T * top_k + p) * rows + n);
-    const float w = weights[p];
+  for (int j0 = 0; j0 < top_k; j0 += J) {
+    // (the loads of J pairs in flight; pairs past the last repeat it)
+    int e[J];
+    float w[J];
+    f32x4_t d[J];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(w, d[r], v[r]);
+    for (int j = 0; j < J; ++j) {
+      const int p = t * top_k + min(j0 + j, top_k - 1);
+      e[j] = ids[p];
+      w[j] = weights[p];
+      d[j] = *reinterpret_cast<const f32x4_t*>(parts + (size_t)p * rows + n);
+    }
+    for (int k = 1; k < ks; ++k)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        d[j] += *reinterpret_cast<const f32x4_t*>(
+            parts + ((size_t)k * T * top_k + t * top_k + min(j0 + j, top_k - 1)) * rows + n);
+    // (what lies at a pair without an expert is not used)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (j0 + j < top_k && (uint32_t)e[j] < (uint32_t)E)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(w[j], d[j][r], v[r]);
   }
   uint16_t* o = y + (size_t)t * rows + n;
   uint32_t h[4];
@@ -1144,9 +1171,10 @@ hipError_t launch_moe_route(const MoeArgs& a, void* workspace, hipStream_t s) {
     return hipGetLastError();
   }
   double* lg = static_cast<double*>(workspace);
-  // few logits: a workgroup each; many: sixteen a wave
+  // Few logits: a workgroup each (16 tokens, 64 experts of 4096: 4.7 us).  Many: four a wave (64 tokens, 128 experts
+  // of 2048: 4.8 us; sixteen a wave 6.5, and the same time from 256 tokens on).
   if ((int64_t)T * E <= kFewLogits) moe_one_logit_kernel<<<dim3((unsigned)E, (unsigned)T), dim3(256), 0, s>>>(x, router, lg, K, E);
-  else moe_logits_kernel<4, 4><<<dim3((unsigned)((E + 15) / 16), (unsigned)((T + 3) / 4)), dim3(256), 0, s>>>(x, router, lg, K, E, T);
+  else moe_logits_kernel<2, 2><<<dim3((unsigned)((T + 1) / 2), (unsigned)((E + 7) / 8)), dim3(256), 0, s>>>(x, router, lg, K, E, T);
   if (E <= 256) moe_choose_kernel<4><<<dim3((unsigned)T), dim3(64), 0, s>>>(lg, ids, weights, E, top_k, a.renorm);
   else moe_choose_kernel<kMaxExperts / 64><<<dim3((unsigned)T), dim3(64), 0, s>>>(lg, ids, weights, E, top_k, a.renorm);
   return hipGetLastError();
@@ -1191,8 +1219,11 @@ hipError_t launch_moe_experts(const MoeArgs& a, const double* lg, void* workspac
   if (e != hipSuccess) return e;
   const int64_t quads = a.t * (a.k / 4);
   const int vec = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
-  moe_combine_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s>>>(
-      parts, ids, weights, y, (int)a.k, (int)a.experts, (int)a.top_k, (int)a.t,
+  const dim3 grid((unsigned)((quads + 255) / 256));
+  // pairs whose loads are in flight together: eight of eight 4.7 us, one after the other 5.5 (64 tokens, 2048
+  // outputs); two of two 5.6, eight loads 7.0 (96 tokens, 5120 outputs)
+  (a.top_k <= 2 ? moe_combine_kernel<2> : a.top_k <= 4 ? moe_combine_kernel<4> : moe_combine_kernel<8>)
+      <<<grid, dim3(256), 0, s>>>(parts, ids, weights, y, (int)a.k, (int)a.experts, (int)a.top_k, (int)a.t,
       down_parts(a), vec);
   return hipGetLastError();
 }

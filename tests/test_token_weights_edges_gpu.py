@@ -88,6 +88,25 @@ def test_experts_with_every_row_count(t):
     tw.close(y, want, bound, "one expert")
 
 
+# few pairs per expert on the whole, many on some; many on the whole, few on some
+COUNTS = [[8, 1, 9, 16, 0, 17, 3], [2, 33, 1, 40, 1, 1, 1, 2, 1], [32, 0, 1, 8, 9, 33, 65, 16, 17], [31, 48, 49]]
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("inner,k", [(192, 320), (1088, 64)])
+def test_experts_with_unequal_counts(counts, inner, k):
+    n, t = len(counts), sum(counts)
+    planes, values = tw.expert_weights(n, inner, k, 1450)
+    x = tw.bf16((t, k), 1451 + t)
+    g = torch.Generator().manual_seed(1452)
+    chosen = torch.tensor([e for e, c in enumerate(counts) for _ in range(c)], dtype=torch.int32)
+    ids = chosen[torch.randperm(t, generator=g)][:, None].contiguous()
+    weights = torch.rand(t, 1, generator=g)
+    y = experts(x, ids, weights, planes, "counts " + "-".join(map(str, counts)))
+    want, bound = tw.experts_reference(x, ids, weights, values)
+    tw.close(y, want, bound, "unequal counts")
+
+
 @pytest.mark.parametrize("t,top_k,n,inner,k", [(2, 1, 2, 64, 8256), (40, 1, 1, 64, 8256), (2, 1, 2, 8256, 64),
                                                (40, 1, 1, 8256, 64), (70, 3, 3, 1088, 1984), (3, 2, 1024, 64, 64),
                                                (50, 2, 300, 64, 64), (600, 1, 2, 64, 64)])

@@ -800,32 +800,34 @@ moe_down_few_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* sca
 
 // ---------------------------------------------------------------------------
 // The same for workgroups whose eight waves take different rows of the weight
-// over the same K and share the activations, up to 32 activation rows a pass,
-// in stages of 128 k.  Codes go through a ring of each wave (two slots),
+// over the same K and share the activations of up to BT pairs a pass, in
+// stages of 128 k.  Codes go through a ring of each wave (two slots),
 // activations through one of the workgroup (three slots, a barrier per
-// stage); both are asked for two stages before their use.  Registers and LDS
-// for four waves per SIMD, as far as the conversion of the codes and the
-// scaling of the sums, not the weight stream, bound it: from about 16 rows.
+// stage); both are asked for two stages before their use.  The two parts of h
+// are two rows of a tile for up to eight pairs (PARTS = 1: three products a
+// tile of codes), two products into the same sums for more (PARTS = 2: every
+// sum and conversion serves both, half the scaling of twice the rows).
+// Registers and LDS for four waves per SIMD, as far as the conversion of the
+// codes and the scaling of the sums, not the weight stream, bound it: from
+// about 16 rows.
 // blockIdx.z shares K (down only: parts of the sums, added by the combine).
 // ---------------------------------------------------------------------------
 constexpr int kWideWaves = 8;
-template <int R, bool DOWN>
+template <int R, bool DOWN, int BT>
 __global__ void __launch_bounds__(64 * kWideWaves, 4)
 moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
                 const uint16_t* scales1, const int* __restrict__ ids, void* out, int K, int rows, int E, int P,
                 int top_k, uint32_t act_bytes) {
   constexpr int RP = DOWN ? 2 : 1;      // activation rows per pair
-  constexpr int BT = 32 / RP;           // pairs per pass, at most
   constexpr int RT = DOWN ? R : R / 2;  // row tiles of the output per wave
   constexpr int XROW = 256;             // bytes of an activation row in a stage (128 k here)
   constexpr int TILE = 16 * 64;         // code bytes of a row tile in a stage
   constexpr int SLOT = R * TILE;
   __shared__ __attribute__((aligned(16))) uint8_t ring0[kWideWaves * SLOT];
   __shared__ __attribute__((aligned(16))) uint8_t ring1[kWideWaves * SLOT];
-  __shared__ __attribute__((aligned(16))) uint8_t xs0[32 * XROW];
-  __shared__ __attribute__((aligned(16))) uint8_t xs1[32 * XROW];
-  __shared__ __attribute__((aligned(16))) uint8_t xs2[32 * XROW];
-  __shared__ int list[kWideWaves][BT];
+  __shared__ __attribute__((aligned(16))) uint8_t xs0[BT * RP * XROW];
+  __shared__ __attribute__((aligned(16))) uint8_t xs1[BT * RP * XROW];
+  __shared__ __attribute__((aligned(16))) uint8_t xs2[BT * RP * XROW];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int e = block_expert(ids, P, E, lane);
@@ -858,23 +860,35 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
 
   int m = 1;
   for (int b0 = 0; b0 < m; b0 += BT) {
-    m = list_pairs<BT>(ids, P, e, b0, lane, list[wave]);
+    // (the list goes by way of the wave's own slot into a register: lane i holds pair i)
+    int* const list = reinterpret_cast<int*>(ring0 + wave * SLOT);
+    m = list_pairs<BT>(ids, P, e, b0, lane, list);
     if (m == 0) return;
-    auto pass = [&](auto ntc, int mr) __device__ {
-      constexpr int NT = decltype(ntc)::value;
+    const int mine = list[lane & (BT - 1)];
+    wait_lgkm0();
+    in_order();
+    const int c = min(BT, m - b0);  // pairs of this pass
+    auto pass = [&](auto ntc, auto partsc) __device__ {
+      constexpr int NT = decltype(ntc)::value, PARTS = decltype(partsc)::value;
+      constexpr int AR = RP / PARTS;  // activation rows of a tile per pair
+      const int mr = c * AR;
       // code order of the products (x is permuted into the paired one for a single tile)
       constexpr bool PAIRED = DOWN || NT == 1;
-      constexpr int LOADS = R + 1;  // of a stage, the scales not counted
+      constexpr int DMAS = NT * PARTS == 4 ? 2 : 1;  // a wave's copies of activations per stage
+      constexpr int LOADS = R + DMAS;  // of a stage, the scales not counted
       // activation rows: a wave copies four rows, lane l the piece of
       // 16 bytes that lies at position l % 16 of row l / 16; piece p of row a
       // at position p ^ (a % 16), so that sixteen rows' reads of one piece
       // spread over the banks
+      // (two parts of 16 rows: waves 0 to 3 the one, 4 to 7 the other; of 32 rows: every wave both)
+      const int xrow = 4 * wave + (lane >> 4);
       uint32_t x_off;
       {
-        const int a = 4 * wave + (lane >> 4);
-        const int p = list[wave][min(a, mr - 1) / RP];
-        const uint32_t row = DOWN ? 2u * p + (a & 1) : (uint32_t)(p / top_k);
-        x_off = a < mr ? row * (uint32_t)K * 2u + 16u * ((lane & 15) ^ (a & 15)) : kNowhere;
+        constexpr bool HALVES = NT == 1 && PARTS == 2;
+        const int a = HALVES ? xrow & 15 : xrow;
+        const int p = __shfl(mine, min(a, mr - 1) / AR);
+        const uint32_t row = DOWN ? 2u * p + (AR == 2 ? a & 1 : HALVES ? xrow >> 4 : 0) : (uint32_t)(p / top_k);
+        x_off = a < mr ? row * (uint32_t)K * 2u + 16u * ((lane & 15) ^ (xrow & 15)) : kNowhere;
       }
       f32x4_t acc[NT][R];
 #pragma unroll
@@ -884,8 +898,10 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
 
       auto load_x = [&](uint8_t* xs, int s) __device__ {
         // (groups past K and rows past the last land as zeros)
-        const bool in = ((lane & 15) ^ ((4 * wave + (lane >> 4)) & 15)) < (s < se ? 8 * (G - 2 * s) : 0);
-        dma16(rx, in ? x_off + 256u * (uint32_t)s : kNowhere, 0, xs + 4 * wave * XROW);
+        const bool in = ((lane & 15) ^ (xrow & 15)) < (s < se ? 8 * (G - 2 * s) : 0);
+#pragma unroll
+        for (int q = 0; q < DMAS; ++q)
+          dma16(rx, in ? x_off + 256u * (uint32_t)s : kNowhere, q * 2u * (uint32_t)K, xs + (32 * q + 4 * wave) * XROW);
         in_order();
       };
       auto load_c = [&](uint8_t* ring, int s) __device__ {
@@ -900,59 +916,48 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
         uint32_t sc[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) sc[r] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * r + li) * 4, (int)d0);
-        // Tile by tile (r of group g): a tile's sums are scaled when the next
-        // tile's codes are converted and its products under way, and a
-        // group's LDS reads are issued a group ahead
-        u32x4_t x[2][NT][2];
-        u32x2_t cw[2][R];
-        f32x4_t cr[2][NT], p[2][NT];
-        auto fetch = [&](auto gc) __device__ {
-          constexpr int g = decltype(gc)::value;
+        // Half by half (h of part q of group g): both parts of a pair add
+        // up in the same sums, and a tile's converted codes serve both;
+        // the LDS reads of a half are issued a half ahead
+        u32x4_t x[2][NT], w[R][2];
+        u32x2_t cw[R];
+        f32x4_t cr[NT], p[R][NT];
+        auto fetch = [&](auto uc) __device__ {
+          constexpr int u = decltype(uc)::value, g = u / (2 * PARTS), q = u / 2 % PARTS, h = u & 1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
+            x[u & 1][nt] = *reinterpret_cast<const u32x4_t*>(xs + xd[2 * g + h] + 16 * (NT * q + nt) * XROW);
+          if constexpr (q + h == 0)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              x[g & 1][nt][h] = *reinterpret_cast<const u32x4_t*>(xs + xd[2 * g + h] + 16 * nt * XROW);
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            cw[g & 1][r] = *reinterpret_cast<const u32x2_t*>(ring + rd[g] + r * TILE);
-        };
-        auto scale = [&](auto qc) __device__ {
-          constexpr int q = decltype(qc)::value, g = q / R, r = q % R;
-          const float sv = f16_bits_to_f32((uint16_t)(g ? sc[r] >> 16 : sc[r] & 0xFFFFu));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[nt][r][i] = __builtin_fmaf(sv, p[q & 1][nt][i] - cr[g & 1][nt][i], acc[nt][r][i]);
+            for (int r = 0; r < R; ++r) cw[r] = *reinterpret_cast<const u32x2_t*>(ring + rd[g] + r * TILE);
         };
         fetch(Slot<0>{});
-        static_for<2 * R>([&](auto qc) __device__ {
-          constexpr int q = decltype(qc)::value, g = q / R, r = q % R;
-          if constexpr (r == 0) {
+        static_for<4 * PARTS>([&](auto uc) __device__ {
+          constexpr int u = decltype(uc)::value, g = u / (2 * PARTS), q = u / 2 % PARTS, h = u & 1;
+          if constexpr (q + h == 0)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (PAIRED && !DOWN) {
-                x[g & 1][nt][0] = to_paired(x[g & 1][nt][0]);
-                x[g & 1][nt][1] = to_paired(x[g & 1][nt][1]);
-              }
-              cr[g & 1][nt] = mfma(x[g & 1][nt][0], eights, zero);
+            for (int r = 0; r < R; ++r) {
+              w[r][0] = PAIRED ? q4_paired(cw[r].x) : q4_natural(cw[r].x);
+              w[r][1] = PAIRED ? q4_paired(cw[r].y) : q4_natural(cw[r].y);
             }
+          if constexpr (u + 1 < 4 * PARTS) fetch(Slot<u + 1>{});
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) cr[g & 1][nt] = mfma(x[g & 1][nt][1], eights, cr[g & 1][nt]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (PAIRED && !DOWN) x[u & 1][nt] = to_paired(x[u & 1][nt]);
+            cr[nt] = mfma(x[u & 1][nt], eights, q + h ? cr[nt] : zero);
+#pragma unroll
+            for (int r = 0; r < R; ++r) p[r][nt] = mfma(x[u & 1][nt], w[r][h], q + h ? p[r][nt] : zero);
           }
-          const u32x4_t w0 = PAIRED ? q4_paired(cw[g & 1][r].x) : q4_natural(cw[g & 1][r].x);
-          const u32x4_t w1 = PAIRED ? q4_paired(cw[g & 1][r].y) : q4_natural(cw[g & 1][r].y);
+          if constexpr (q == PARTS - 1 && h == 1)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) p[q & 1][nt] = mfma(x[g & 1][nt][0], w0, zero);
+            for (int r = 0; r < R; ++r) {
+              const float sv = f16_bits_to_f32((uint16_t)(g ? sc[r] >> 16 : sc[r] & 0xFFFFu));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) p[q & 1][nt] = mfma(x[g & 1][nt][1], w1, p[q & 1][nt]);
-          __builtin_amdgcn_sched_barrier(0);
-          if constexpr (q > 0) scale(Slot<(q > 0 ? q - 1 : 0)>{});
-          if constexpr (r == 0 && g < 1) fetch(Slot<1>{});
-          __builtin_amdgcn_sched_barrier(0);
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[nt][r][i] = __builtin_fmaf(sv, p[r][nt][i] - cr[nt][i], acc[nt][r][i]);
+            }
         });
-        scale(Slot<2 * R - 1>{});
       };
       typename RowScales<R, DOWN>::Regs S;
       uint32_t d[4];
@@ -980,6 +985,7 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
             }
             load_x((i + 2) % 3 == 0 ? xs0 : (i + 2) % 3 == 1 ? xs1 : xs2, s + 2);
             compute((i & 1) ? ring1 : ring0, i % 3 == 0 ? xs0 : i % 3 == 1 ? xs1 : xs2, d[i % 4]);
+            in_order();
             wait_lgkm0();
             in_order();
             load_c((i & 1) ? ring1 : ring0, s + 2);
@@ -992,25 +998,33 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; i += RP) {
+        for (int i = 0; i < 4; i += AR) {
           const int a = 16 * nt + 4 * lq + i;
+          const int p = __shfl(mine, a / AR);
           if (a >= mr) continue;
-          const int p = list[wave][a / RP];
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
             const int n = n0 + 16 * r + li;
             if (n >= rows) continue;
             if constexpr (DOWN) {
-              static_cast<float*>(out)[((size_t)blockIdx.z * P + p) * rows + n] = acc[nt][r][i] + acc[nt][r][i + 1];
+              static_cast<float*>(out)[((size_t)blockIdx.z * P + p) * rows + n] =
+                  AR == 2 ? acc[nt][r][i] + acc[nt][r][(i + 1) & 3] : acc[nt][r][i];
             } else {
               store_gated(acc[nt][r][i], acc[nt][RT + r][i], static_cast<uint16_t*>(out), p, rows, n);
             }
           }
         }
     };
-    const int mr = min(BT, m - b0) * RP;
-    if (mr <= 16) pass(Slot<1>{}, mr);
-    else pass(Slot<2>{}, mr);
+    if constexpr (!DOWN) {
+      if (c <= 16) pass(Slot<1>{}, Slot<1>{});
+      else pass(Slot<2>{}, Slot<1>{});
+    } else if constexpr (BT == 16) {
+      if (c <= 8) pass(Slot<1>{}, Slot<1>{});
+      else pass(Slot<1>{}, Slot<2>{});
+    } else {
+      if (c <= 16) pass(Slot<1>{}, Slot<2>{});
+      else pass(Slot<2>{}, Slot<2>{});
+    }
     __syncthreads();
   }
 }
@@ -1067,9 +1081,11 @@ constexpr int kRowTiles = 4;      // per wave (gate and up of few rows)
 constexpr int kWideRowTiles = 2;  // per wave (workgroups that share the activations)
 // Pairs per expert in use from which the gate and up products share the
 // activations in workgroups (24 of them on eight experts of 2 x 14336 x 5120:
-// 194 us against 222; 4 on 128 of 2 x 768 x 2048 58 either way; 4 on 16 of
-// 2 x 1536 x 5120 45 against 41).
-constexpr int64_t kWideGate = 18;
+// 192 us against 222; 4 on 128 of 2 x 768 x 2048 58 either way; 4 on 16 of
+// 2 x 1536 x 5120 45 against 41), and the down products take 32 pairs a pass
+// (24 on eight of 5120 x 14336: 115 us against 165 with passes of 16; up to
+// 16 on 16 of 5120 x 1536 26.3 against 24.1).
+constexpr int64_t kManyPairs = 18;
 // workgroups that the chip holds at a time (two per CU, by LDS and registers)
 constexpr int64_t kResident = 512;
 
@@ -1113,10 +1129,10 @@ hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t
   auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
   const uint32_t x_bytes = (uint32_t)(a.t * a.k * 2);
-  if (lg == nullptr && P / experts_hit(a) >= kWideGate) {
+  if (lg == nullptr && P / experts_hit(a) >= kManyPairs) {
     constexpr int R = kWideRowTiles;
     const dim3 grid((unsigned)ceil_div(a.inner, kWideWaves * 8 * R), slots);
-    moe_wide_kernel<R, false><<<grid, dim3(64 * kWideWaves), 0, s>>>(
+    moe_wide_kernel<R, false, 32><<<grid, dim3(64 * kWideWaves), 0, s>>>(
         u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up),
         static_cast<const int*>(a.ids), h, (int)a.k, (int)a.inner, (int)a.experts, P, (int)a.top_k, x_bytes);
     return hipGetLastError();
@@ -1144,9 +1160,13 @@ hipError_t launch_down(const MoeArgs& a, const void* h, float* parts, hipStream_
                   (unsigned)down_parts(a));
   const auto codes = static_cast<const uint8_t*>(a.codes_down);
   const auto scales = static_cast<const uint16_t*>(a.scales_down);
-  moe_wide_kernel<R, true><<<grid, dim3(64 * kWideWaves), 0, s>>>(
-      static_cast<const uint16_t*>(h), codes, scales, codes, scales, static_cast<const int*>(a.ids), parts,
-      (int)a.inner, (int)a.k, (int)a.experts, P, (int)a.top_k, (uint32_t)((int64_t)P * a.inner * 4));
+  auto go = [&](auto kern) {
+    kern<<<grid, dim3(64 * kWideWaves), 0, s>>>(
+        static_cast<const uint16_t*>(h), codes, scales, codes, scales, static_cast<const int*>(a.ids), parts,
+        (int)a.inner, (int)a.k, (int)a.experts, P, (int)a.top_k, (uint32_t)((int64_t)P * a.inner * 4));
+  };
+  if (P / experts_hit(a) >= kManyPairs) go(moe_wide_kernel<R, true, 32>);
+  else go(moe_wide_kernel<R, true, 16>);
   return hipGetLastError();
 }
 

@@ -20,10 +20,12 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
 constexpr uint32_t kNowhere = 0x80000000u;  // a buffer offset past every range
 
 // 16 bytes per lane from memory straight into LDS, lane l to lds_base + 16 l
-// (lds_base wave-uniform)
+// (lds_base wave-uniform; HINT: kOnce for what is not read again)
+constexpr int kOnce = 2;  // non-temporal
+template <int HINT = 0>
 __device__ __forceinline__ void dma16(rsrc_t r, uint32_t voffset, uint32_t soffset, void* lds_base) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 16, voffset,
-                                           soffset, 0, 0);
+                                           soffset, 0, HINT);
 }
 
 // waits until at most N of the wave's loads are outstanding (gfx9 encoding:

@@ -288,12 +288,13 @@ Q4LIN_API int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int6
  * nothing, a token without a valid id gets zeros, and an expert that a token
  * names twice counts twice.  The sums are binary32 or wider, h keeps 16
  * significant bits, y is rounded once.  The weights of an expert are read
- * once for up to 32 (down: 16) of its tokens.
+ * once for up to 16 of its tokens (32 where the tokens per expert are many;
+ * the down weights once per token where the tokens are few).
  *
  * K and inner: positive multiples of 64; 1 <= experts <= 1024; 1 <= top_k <=
- * experts; T K 2 bytes, 4 T top_k inner bytes and T top_k K each below 2^31.  workspace (not for q4lin_moe_route):
- * q4lin_moe_workspace_bytes() bytes, 256-byte aligned.  T = 0 is an empty
- * call.  No output may overlap an input, another output or the workspace.
+ * experts; 2 T K, 4 T top_k inner and T top_k K each below 2^31.  workspace
+ * (not for q4lin_moe_route): q4lin_moe_workspace_bytes() bytes, 256-byte
+ * aligned.  T = 0 is an empty call.  No output may overlap an input, another output or the workspace.
  * Errors as for q4lin_linear. */
 Q4LIN_API int q4lin_moe(const void *x, const void *router, const void *codes_gate, const void *scales_gate,
                       const void *codes_up, const void *scales_up, const void *codes_down, const void *scales_down,

@@ -815,7 +815,8 @@ moe_down_few_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* sca
 // in the down products; both halves of a 128-byte line asked for together,
 // with or without a place in the caches, move 5 to 20 % fewer bytes and take
 // as long or longer.)
-// blockIdx.z shares K (down only: parts of the sums, added by the combine).
+// blockIdx.z shares K (down: parts of the sums, added by the combine) or the
+// passes (gate and up).
 // ---------------------------------------------------------------------------
 constexpr int kWideWaves = 8;
 template <int R, bool DOWN, int BT>
@@ -841,7 +842,8 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
   const int G = K >> 6, stages = (G + 1) >> 1;
   // (shares of whole quads of stages, as the scales come)
   const int quads = (stages + 3) >> 2;
-  const int sb = 4 * (int)(quads * blockIdx.z / gridDim.z), se = min(4 * (int)(quads * (blockIdx.z + 1) / gridDim.z), stages);
+  const int part = DOWN ? blockIdx.z : 0, parts = DOWN ? gridDim.z : 1;
+  const int sb = 4 * (quads * part / parts), se = min(4 * (quads * (part + 1) / parts), stages);
   const uint32_t crow = (uint32_t)K >> 1;
   rsrc_t rc[R];
 #pragma unroll
@@ -863,12 +865,12 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
     for (int h = 0; h < 2; ++h) xd[2 * g + h] = li * XROW + 16 * ((8 * g + 2 * lq + h) ^ li);
   }
 
-  int m = 1;
-  for (int b0 = 0; b0 < m; b0 += BT) {
+  int m = INT32_MAX;
+  for (int b0 = DOWN ? 0 : BT * blockIdx.z; b0 < m; b0 += DOWN ? BT : BT * gridDim.z) {
     // (the list goes by way of the wave's own slot into a register: lane i holds pair i)
     int* const list = reinterpret_cast<int*>(ring0 + wave * SLOT);
     m = list_pairs<BT>(ids, P, e, b0, lane, list);
-    if (m == 0) return;
+    if (m <= b0) return;
     const int mine = list[lane & (BT - 1)];
     wait_lgkm0();
     in_order();
@@ -1136,7 +1138,11 @@ hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t
   const uint32_t x_bytes = (uint32_t)(a.t * a.k * 2);
   if (lg == nullptr && P / experts_hit(a) >= kManyPairs) {
     constexpr int R = kWideRowTiles;
-    const dim3 grid((unsigned)ceil_div(a.inner, kWideWaves * 8 * R), slots);
+    // workgroups per pass where all of them are resident (60 tokens on each of
+    // four experts of 2 x 1600 x 1280: 16 us against 28)
+    const int64_t blocks = ceil_div(a.inner, kWideWaves * 8 * R), passes = ceil_div(P / experts_hit(a), 32);
+    const int64_t room = kResident / (blocks * experts_hit(a));
+    const dim3 grid((unsigned)blocks, slots, (unsigned)(room < 1 ? 1 : room < passes ? room : passes));
     moe_wide_kernel<R, false, 32><<<grid, dim3(64 * kWideWaves), 0, s>>>(
         u16(a.x), u8(a.codes_gate), u16(a.scales_gate), u8(a.codes_up), u16(a.scales_up),
         static_cast<const int*>(a.ids), h, (int)a.k, (int)a.inner, (int)a.experts, P, (int)a.top_k, x_bytes);

@@ -408,10 +408,11 @@ __device__ __forceinline__ int list_pairs(const int* __restrict__ ids, int P, in
 }
 
 // The expert of this workgroup (its blockIdx.y), or -1: nothing to do.  Up to
-// kPairGrid pairs the grid has a row of workgroups per pair (that of an
-// expert's first pair works), beyond it one per expert.
+// kPairGrid pairs, and fewer pairs than experts, the grid has a row of
+// workgroups per pair (that of an expert's first pair works), else one per
+// expert.
 __device__ __forceinline__ int block_expert(const int* __restrict__ ids, int P, int E, int lane) {
-  if (P > kPairGrid) return blockIdx.y;
+  if (P > kPairGrid || P >= E) return blockIdx.y;
   const int id = lane < P ? ids[lane] : -1;
   const int e = __builtin_amdgcn_readlane(id, blockIdx.y);
   if ((uint32_t)e >= (uint32_t)E) return -1;
@@ -589,12 +590,12 @@ struct Choice {
   int T, renorm;
 };
 
-// The expert e of pair (blockIdx.y / top_k, blockIdx.y % top_k) and the pairs
-// that chose it, in order, into the wave's list; returns how many, 0 if an
-// earlier token chose it (whose workgroups serve it).
-template <int FT>
+// The expert e of this workgroup (rows of workgroups as for block_expert: the
+// choice of pair blockIdx.y, or blockIdx.y itself) and the pairs that chose
+// it, in order, into the wave's list; returns how many, 0 if there are none
+// or an earlier token chose it (whose workgroups serve it).  E <= 64 B.
+template <int FT, int B>
 __device__ __forceinline__ int choose_pairs(const Choice& c, int E, int top_k, int lane, int* list, int& e) {
-  constexpr int B = kFewExperts / 64;
   uint64_t key[FT][B];  // (every token's loads in flight; tokens past T repeat the last)
 #pragma unroll
   for (int t = 0; t < FT; ++t)
@@ -604,15 +605,20 @@ __device__ __forceinline__ int choose_pairs(const Choice& c, int E, int top_k, i
       const uint64_t k = route_key(c.lg[(size_t)min(t, c.T - 1) * E + min(i, E - 1)], i);
       key[t][b] = i < E ? k : 0;
     }
-  const int mine = blockIdx.y / top_k;
-  uint64_t own[B];
+  const bool by_expert = c.T * top_k >= E;
+  const int mine = by_expert ? 0 : blockIdx.y / top_k;
+  if (by_expert) {
+    e = blockIdx.y;
+  } else {
+    uint64_t own[B];
 #pragma unroll
-  for (int b = 0; b < B; ++b) {
-    own[b] = key[0][b];
+    for (int b = 0; b < B; ++b) {
+      own[b] = key[0][b];
 #pragma unroll
-    for (int t = 1; t < FT; ++t) own[b] = t == mine ? key[t][b] : own[b];
+      for (int t = 1; t < FT; ++t) own[b] = t == mine ? key[t][b] : own[b];
+    }
+    e = choose_rank<B>(own, blockIdx.y - mine * top_k + 1, lane, nullptr);
   }
-  e = choose_rank<B>(own, blockIdx.y - mine * top_k + 1, lane, nullptr);
   int m = 0;
   bool served = false;
 #pragma unroll
@@ -641,7 +647,7 @@ __device__ __forceinline__ int choose_pairs(const Choice& c, int E, int top_k, i
 // rows: of h, wk: waves that share K (the other kWaves / wk share the
 // workgroup's rows).  CHOOSE: tokens whose choice is made here, at most (0:
 // ids hold it).
-template <int R, int CHOOSE, int HINT>
+template <int R, int CHOOSE, int HINT, int B>
 __global__ void __launch_bounds__(kThreads, 2)
 moe_gated_kernel(const uint16_t* x, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
                  const uint16_t* scales1, const int* __restrict__ ids, uint16_t* h, int K, int rows, int E, int P,
@@ -664,14 +670,14 @@ moe_gated_kernel(const uint16_t* x, const uint8_t* codes0, const uint16_t* scale
 
   int e, m = 1;
   if constexpr (CHOOSE > 0) {
-    if ((int)blockIdx.y == P) {  // (a workgroup of its own writes the choice)
+    if (blockIdx.y == gridDim.y - 1) {  // (a workgroup of its own writes the choice)
       if (blockIdx.x > 0) return;
       for (int t = wave; t < choice.T; t += kWaves)
-        choose_one<kFewExperts / 64>(choice.lg + (size_t)t * E, E, top_k, lane, choice.renorm, chosen[wave],
+        choose_one<B>(choice.lg + (size_t)t * E, E, top_k, lane, choice.renorm, chosen[wave],
                                      choice.ids + (size_t)t * top_k, choice.weights + (size_t)t * top_k);
       return;
     }
-    m = choose_pairs<CHOOSE>(choice, E, top_k, lane, list[wave], e);
+    m = choose_pairs<CHOOSE, B>(choice, E, top_k, lane, list[wave], e);
     if (m == 0) return;
   } else {
     e = block_expert(ids, P, E, lane);
@@ -1058,11 +1064,22 @@ moe_combine_kernel(const float* __restrict__ parts, const int* __restrict__ ids,
       w[j] = weights[p];
       d[j] = *reinterpret_cast<const f32x4_t*>(parts + (size_t)p * rows + n);
     }
-    for (int k = 1; k < ks; ++k)
+    for (int k0 = 1; k0 < ks; k0 += 3) {
+      // (three parts' loads in flight; parts past the last repeat it: seven parts
+      // of six pairs on 640 outputs 5 us, one after the other 12.5)
+      f32x4_t more[3][J];
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        d[j] += *reinterpret_cast<const f32x4_t*>(
-            parts + ((size_t)k * T * top_k + t * top_k + min(j0 + j, top_k - 1)) * rows + n);
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          more[k][j] = *reinterpret_cast<const f32x4_t*>(
+              parts + ((size_t)min(k0 + k, ks - 1) * T * top_k + t * top_k + min(j0 + j, top_k - 1)) * rows + n);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k0 + k < ks)
+#pragma unroll
+          for (int j = 0; j < J; ++j) d[j] += more[k][j];
+    }
     // (what lies at a pair without an expert is not used)
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -1117,6 +1134,12 @@ int64_t experts_hit(const MoeArgs& a) {
   return pairs < a.experts ? pairs : a.experts;
 }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// rows of workgroups: pairs or experts, the fewer (block_expert; three tokens
+// on six of seven experts each: gate and up 12 us with seven rows, 22 with 18)
+unsigned grid_rows(const MoeArgs& a) {
+  const int64_t pairs = a.t * a.top_k;
+  return (unsigned)(pairs <= kPairGrid && pairs < a.experts ? pairs : a.experts);
+}
 
 // Whether one launch makes the down products and their sums: a single token,
 // or a few that share few experts (16 waves for every 16 or 32 rows of y; two
@@ -1132,7 +1155,7 @@ int down_parts(const MoeArgs& a) {
 hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t s) {
   // (lg: the choice is made here)
   const int P = (int)(a.t * a.top_k);
-  const unsigned slots = (unsigned)(P <= kPairGrid ? P : a.experts);
+  const unsigned slots = grid_rows(a);
   auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
   const uint32_t x_bytes = (uint32_t)(a.t * a.k * 2);
@@ -1160,9 +1183,16 @@ hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t
   };
   auto pick = [&](auto hint) {
     constexpr int HINT = decltype(hint)::value;
-    if (lg == nullptr) go(moe_gated_kernel<R, 0, HINT>, slots);
-    else if (a.t == 1) go(moe_gated_kernel<R, 1, HINT>, slots + 1);
-    else go(moe_gated_kernel<R, kFewTokens, HINT>, slots + 1);
+    // (keys of 64 B experts per token: 7 tokens on 60 experts 17.5 us with B = 1, 22 with 4)
+    auto choose = [&](auto width) {
+      constexpr int B = decltype(width)::value;
+      if (a.t == 1) go(moe_gated_kernel<R, 1, HINT, B>, slots + 1);
+      else go(moe_gated_kernel<R, kFewTokens, HINT, B>, slots + 1);
+    };
+    if (lg == nullptr) go(moe_gated_kernel<R, 0, HINT, 1>, slots);
+    else if (a.experts <= 64) choose(Slot<1>{});
+    else if (a.experts <= 128) choose(Slot<2>{});
+    else choose(Slot<kFewExperts / 64>{});
   };
   // Rows of whole 128-byte lines: every line is fetched once, by one load, and
   // need not stay in the caches (one token, two experts of 2 x 14336 x 5120
@@ -1177,8 +1207,7 @@ hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t
 hipError_t launch_down(const MoeArgs& a, const void* h, float* parts, hipStream_t s) {
   constexpr int R = kWideRowTiles;
   const int P = (int)(a.t * a.top_k);
-  const dim3 grid((unsigned)ceil_div(a.k, kWideWaves * 16 * R), (unsigned)(P <= kPairGrid ? P : a.experts),
-                  (unsigned)down_parts(a));
+  const dim3 grid((unsigned)ceil_div(a.k, kWideWaves * 16 * R), grid_rows(a), (unsigned)down_parts(a));
   const auto codes = static_cast<const uint8_t*>(a.codes_down);
   const auto scales = static_cast<const uint16_t*>(a.scales_down);
   auto go = [&](auto kern) {

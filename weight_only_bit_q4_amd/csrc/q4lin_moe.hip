@@ -817,7 +817,7 @@ moe_down_few_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* sca
 // codes and the scaling of the sums, not the weight stream, bound it: from
 // about 16 rows.
 // (96 tokens on eight experts of 14336 x 5120: vector and matrix instructions
-// take 63 + 33 % of the SIMDs' cycles in the gate and up products, 51 + 52 %
+// take 60 + 31 % of the SIMDs' cycles in the gate and up products, 55 + 56 %
 // in the down products; both halves of a 128-byte line asked for together,
 // with or without a place in the caches, move 5 to 20 % fewer bytes and take
 // as long or longer.)
@@ -1143,9 +1143,15 @@ unsigned grid_rows(const MoeArgs& a) {
 
 // Whether one launch makes the down products and their sums: a single token,
 // or a few that share few experts (16 waves for every 16 or 32 rows of y; two
-// launches fewer, but an expert is read again for every token that chose it)
+// launches fewer, but an expert is read again for every token that chose it),
+// while a workgroup's rows of all pairs are short (20 pairs of inner 5120 on
+// 640 rows: the layer 66 us against 51, 9 of 3904 on 1088 38 against 36; 6 of
+// 5632 on 832 32 against 33, 2 of 14336 on 5120 58 against 68).
+constexpr int64_t kFewColumns = 35 * 1024;
 bool few_pairs(const MoeArgs& a) {
-  return a.t == 1 || (a.t <= kFewTokens && a.t * a.top_k <= kPairGrid && 2 * a.t * a.top_k <= a.experts);
+  const int64_t pairs = a.t * a.top_k;
+  return pairs * a.inner <= kFewColumns &&
+         (a.t == 1 || (a.t <= kFewTokens && pairs <= kPairGrid && 2 * pairs <= a.experts));
 }
 // parts of the down products' sums
 int down_parts(const MoeArgs& a) {

@@ -167,14 +167,15 @@ def test_experts_of_zero_weights(t):
 
 
 # -- adapters ------------------------------------------------------------------------
-def lora(fmt, n, k, t, adapters, rank, seed, **move):
+def lora(fmt, n, k, t, adapters, rank, seed, ids=None):
     planes, w64 = tw.weight(fmt, n, k, seed)
     x = tw.bf16((t, k), seed + 1)
     std = float(w64.std())
     a = tw.bf16((adapters, rank, k), seed + 2, k ** -0.5)
     b = tw.bf16((adapters, n, rank), seed + 3, std * (k / rank) ** 0.5)
     g = torch.Generator().manual_seed(seed + 4)
-    ids = torch.randint(-1, adapters, (t,), generator=g, dtype=torch.int32)
+    own = torch.randint(-1, adapters, (t,), generator=g, dtype=torch.int32)
+    ids = own if ids is None else ids
     scale = torch.rand(adapters, generator=g) + 0.5
     announce("linear_lora fmt=%d n=%d k=%d t=%d adapters=%d rank=%d" % (fmt, n, k, t, adapters, rank))
     y = q4.linear_lora(dev(x), dev(planes[0]), dev(planes[2]), dev(a), dev(b), dev(ids), dev(scale), fmt=fmt,
@@ -199,3 +200,16 @@ def test_lora_paths(fmt, t, rank):
                                                  (600, 2048, 257, 2, 200), (96, 16448, 2, 3, 16), (96, 20544, 40, 3, 120)])
 def test_lora_larger(n, k, t, adapters, rank):
     lora(0, n, k, t, adapters, rank, 2000 + t)
+
+
+@pytest.mark.parametrize("t,adapters,rank,order", [(33, 40, 128, "mixed"), (130, 3, 40, "falling"), (257, 300, 16, "mixed"),
+                                                   (1000, 7, 8, "mixed"), (300, 1, 16, "mixed"), (600, 5, 72, "runs"),
+                                                   (4096, 9, 8, "mixed"), (4100, 9, 8, "mixed")])
+def test_lora_orders_of_tokens(t, adapters, rank, order):
+    """Many tokens whose adapters come in any order, many without one."""
+    g = torch.Generator().manual_seed(1901 + t)
+    ids = torch.randint(-2, adapters + 1, (t,), generator=g, dtype=torch.int32)
+    if order != "mixed":
+        ids = ids.sort(descending=order == "falling").values.contiguous()
+    lora(0, 100, 128, t, adapters, rank, 2100 + t, ids)
+    lora(3, 300, 192, t, adapters, rank, 2200 + t, ids)

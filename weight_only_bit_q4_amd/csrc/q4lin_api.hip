@@ -283,7 +283,7 @@ int lora_plan(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters, int64_
     p->tail = fmt != Q4LIN_FMT_Q4G64_F16S || (p->route == Q4LIN_ROUTE_SKINNY && small_uses_fmt(n, k, t)) ||
               (p->route == Q4LIN_ROUTE_DECODE && q4lin::decode_plan(n, k, t, &dp) && dp.waves == 8);
   }
-  p->u_bytes = q4lin::lora_u_bytes(k, t, rank);
+  p->u_bytes = q4lin::lora_u_bytes(k, t, rank, adapters);
   p->total = p->u_bytes + base;  // (the sums' room on every route, also where the kernel adds the term itself)
   return Q4LIN_OK;
 }

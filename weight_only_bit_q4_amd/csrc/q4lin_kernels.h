@@ -228,7 +228,7 @@ struct LoraArgs {
   int64_t n, k, t, adapters, rank;
 };
 // bytes of u, the tokens' rank values [t][rank] (in parts of a K split)
-size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank);
+size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank, int64_t adapters);
 // few tokens: u by the tokens' own products, for a base product that takes a
 // LoraTail
 bool lora_few(int64_t t, int64_t rank);

@@ -17,9 +17,11 @@
 //   finish   sums the KS parts of u, scales, multiplies with B_a and adds S:
 //            one read of S and B_a, one write of y, one rounding.  A wave
 //            takes 16 tokens and 16 NB rows of a block and goes through the
-//            distinct adapters of its tokens: one pass over B for a run of
-//            tokens of one adapter, 16 for 16 tokens of 16.  1024 tokens on
-//            6144 rows (38 MB): 14 us.
+//            distinct adapters of its tokens.  Up to 4096 tokens it takes
+//            them by adapter, in an order that the shrink's launch makes, so
+//            that B is read about once whatever their order in x (1024 tokens
+//            on 6144 rows, 38 MB: 13.8 us; mixed tokens of 8 adapters 13.8
+//            against 22 in their own order, 280 of 24 on 7703 rows 17 / 41).
 //
 // Up to 4096 rank values (T R) each token's own products make them
 // (lora_dots_kernel), and up to 32 tokens the base product's kernel adds the
@@ -43,11 +45,10 @@ constexpr int kWaves = 8;
 constexpr int kMaxSplit = 4;  // of the shrink's K
 constexpr int kThreads = 64 * kWaves;
 
-// The adapter of token t0 + i in lane 16 q + i (-1: none), and in `first` a
-// bit for each lane 0..15 whose adapter no lower lane has.
-__device__ __forceinline__ int tile_adapters(const int* __restrict__ ids, int t0, int T, int L, int li,
-                                             uint32_t& first) {
-  int id = t0 + li < T ? ids[t0 + li] : -1;
+// The adapter of the tile's token i in lane 16 q + i, given its id (-1:
+// none), and in `first` a bit for each lane 0..15 whose adapter no lower lane
+// has.
+__device__ __forceinline__ int tile_adapters(int id, int L, int li, uint32_t& first) {
   if ((uint32_t)id >= (uint32_t)L) id = -1;
   bool dup = id < 0;
 #pragma unroll
@@ -61,13 +62,34 @@ __device__ __forceinline__ int tile_adapters(const int* __restrict__ ids, int t0
 template <int RT>
 __global__ void __launch_bounds__(kThreads)
 lora_shrink_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const int* __restrict__ ids,
-                   float* __restrict__ u, int K, int T, int R, int L, int KS) {
+                   float* __restrict__ u, int* __restrict__ order, int K, int T, int R, int L, int KS) {
   __shared__ float red[kWaves][RT][16][20];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int ks = blockIdx.x % KS, t0 = blockIdx.z * 16, r0 = blockIdx.x / KS * (16 * RT);
+  // order: the tokens by adapter, then by number (those without one last), in
+  // workgroups of their own behind the others.  A token's place is the count
+  // of tokens before it: 32 lanes a token, 16 tokens a workgroup.
+  const int tiles = (T + 15) >> 4;
+  if ((int)blockIdx.z >= tiles) {
+    const int tile = ((blockIdx.z - tiles) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    if (tile >= tiles) return;
+    const int t = min(16 * tile + (int)(threadIdx.x >> 5), T - 1);
+    const uint32_t own = (uint32_t)ids[t];
+    int before = 0;
+#pragma unroll 8
+    for (int o = threadIdx.x & 31; o < T; o += 32) {
+      const uint32_t other = (uint32_t)ids[o];
+      before += other < own || (other == own && o < t);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) before += __shfl_xor(before, m);
+    order[before] = t;  // (tokens past the last repeat it)
+    return;
+  }
+
   uint32_t todo;
-  const int id = tile_adapters(ids, t0, T, L, li, todo);
+  const int id = tile_adapters(t0 + li < T ? ids[t0 + li] : -1, L, li, todo);
 
   // this wave's run of 32-k steps
   const int steps = K >> 5, parts = KS * kWaves, part = ks * kWaves + wave;
@@ -174,12 +196,13 @@ lora_dots_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
 // current one is written; the adapters' term crosses over to that order
 // through LDS (two buffers, a barrier per block).  Where a tile's tokens have
 // several adapters, the next adapter's rows are on their way while one's are
-// used, as far as registers go (179 mixed tokens of 24 adapters of rank 32,
-// 6443 rows: 13 us against 17; 64 tokens of one adapter a tile: no change).
+// used, as far as registers go (179 mixed tokens of 24 adapters of rank 32 in
+// their own order, 6443 rows: 13 us against 17).
 template <int RS, int NB>
 __global__ void __launch_bounds__(256)
 lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ scale, const int* __restrict__ ids,
-                   const float* __restrict__ u, SumSource base, uint16_t* __restrict__ y, int N, int T, int R, int L,
+                   const float* __restrict__ u, const int* __restrict__ order, SumSource base,
+                   uint16_t* __restrict__ y, int N, int T, int R, int L,
                    int KS, int vec) {
   constexpr int ROWS = 64 * NB;  // of a block
   constexpr int D = RS * NB <= 2 ? 4 : RS * NB <= 8 ? 2 : 1;  // adapters whose rows are in registers
@@ -187,8 +210,13 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int t0 = blockIdx.y * 16;
+  // this lane's token and those of the wave's rows (tokens past the last repeat it)
+  const int tl = order != nullptr ? order[min(t0 + li, T - 1)] : min(t0 + li, T - 1);
+  int tw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tw[i] = __builtin_amdgcn_readlane(tl, 4 * wave + i);
 
-  // This lane's base sums of a block: tokens t0 + 4 wave + i, rows nl .. nl + NB - 1
+  // This lane's base sums of a block: tokens tw[i], rows nl .. nl + NB - 1
   typedef float fv_t __attribute__((ext_vector_type(NB)));
   struct Sums {
     fv_t v[4];
@@ -198,8 +226,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
     const int nl = nb0 + NB * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = min(t0 + 4 * wave + i, T - 1);
-      const float* p = base.part + (size_t)t * N + nl;
+      const float* p = base.part + (size_t)tw[i] * N + nl;
       s.v[i] = fv_t{};
       if (vec) {
         if (nl < N) s.v[i] = *reinterpret_cast<const fv_t*>(p);
@@ -212,7 +239,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
     for (int k = 1; k < base.ks; ++k) {  // the other slices of a K split, in order
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float* p = base.part + (size_t)k * base.stride + (size_t)min(t0 + 4 * wave + i, T - 1) * N + nl;
+        const float* p = base.part + (size_t)k * base.stride + (size_t)tw[i] * N + nl;
 #pragma unroll
         for (int j = 0; j < NB; ++j)
           if (nl + j < N) s.v[i][j] += p[j];
@@ -223,7 +250,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   Sums cur = load_sums(blockIdx.x * ROWS);
 
   uint32_t first;
-  const int id = tile_adapters(ids, t0, T, L, li, first);
+  const int id = tile_adapters(t0 + li < T ? ids[tl] : -1, L, li, first);
   // token li's s_a u as two bf16 parts, ranks 32 s + 8 lq .. + 7 of step s
   u32x4_t uh[RS], ul[RS];
   const float sc = id >= 0 && scale != nullptr ? scale[id] : 1.0f;
@@ -231,7 +258,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   for (int r = 0; r < RS; ++r) {
     f32x4_t v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
     if (id >= 0 && 32 * r + 8 * lq < R) {
-      const f32x4_t* p = reinterpret_cast<const f32x4_t*>(u + (size_t)(t0 + li) * R + 32 * r + 8 * lq);
+      const f32x4_t* p = reinterpret_cast<const f32x4_t*>(u + (size_t)tl * R + 32 * r + 8 * lq);
       v0 = p[0];
       v1 = p[1];
       if (KS > 1) {
@@ -262,7 +289,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   }
   int te[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) te[i] = base.texp != nullptr ? base.texp[min(t0 + 4 * wave + i, T - 1)] : 0;
+  for (int i = 0; i < 4; ++i) te[i] = base.texp != nullptr ? base.texp[tw[i]] : 0;
 
   int buf = 0;
   for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS, buf ^= 1) {
@@ -332,8 +359,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
     // the base sum, the one rounding, the store
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = t0 + 4 * wave + i;
-      if (t >= T) break;
+      if (t0 + 4 * wave + i >= T) break;
       uint16_t h[NB];
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
@@ -341,7 +367,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
         const float f = __builtin_ldexpf(cur.v[i][j], te[i] - re[j]);
         h[j] = f32_to_bf16_rne(f + term[buf][4 * wave + i][NB * lane + j]);
       }
-      uint16_t* o = y + (size_t)t * N + nl;
+      uint16_t* o = y + (size_t)tw[i] * N + nl;
       if (vec && NB == 4) {
         if (nl < N)
           *reinterpret_cast<u32x2_t*>(o) =
@@ -372,6 +398,19 @@ ShrinkPlan shrink_plan(int64_t k, int64_t t, int64_t r) {
   return ShrinkPlan{rt, ks < 1 ? 1 : (int)ks};
 }
 
+// Whether the finish takes the tokens by adapter (the shrink makes the order,
+// T / 32 comparisons a lane).
+constexpr int64_t kOrderT = 4096;
+bool lora_ordered(int64_t t, int64_t rank, int64_t adapters) {
+  return t > 16 && t <= kOrderT && adapters > 1 && !lora_few(t, rank);
+}
+// the order, behind the rank values
+int* lora_order(const LoraArgs& a, const float* u) {
+  if (!lora_ordered(a.t, a.rank, a.adapters)) return nullptr;
+  const size_t bytes = lora_u_bytes(a.k, a.t, a.rank, a.adapters) - (((size_t)a.t * 4 + 255) & ~(size_t)255);
+  return reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(const_cast<float*>(u)) + bytes);
+}
+
 template <int RS>
 hipError_t launch_finish(const LoraArgs& a, const float* u, const SumSource& base, hipStream_t s) {
   const int ks = shrink_plan(a.k, a.t, a.rank).ks;
@@ -385,7 +424,7 @@ hipError_t launch_finish(const LoraArgs& a, const float* u, const SumSource& bas
   const dim3 grid((unsigned)(blocks < most ? blocks : most), (unsigned)tiles);
   auto go = [&](auto kern) {
     kern<<<grid, dim3(256), 0, s>>>(static_cast<const uint16_t*>(a.b), static_cast<const float*>(a.scale),
-                                    static_cast<const int*>(a.ids), u, base, static_cast<uint16_t*>(a.y), (int)a.n,
+                                    static_cast<const int*>(a.ids), u, lora_order(a, u), base, static_cast<uint16_t*>(a.y), (int)a.n,
                                     (int)a.t, (int)a.rank, (int)a.adapters, ks, vec);
   };
   if (wide) go(lora_finish_kernel<RS, 4>);
@@ -408,8 +447,9 @@ hipError_t launch_lora_dots(const LoraArgs& a, float* u, hipStream_t s) {
   return hipGetLastError();
 }
 
-size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank) {
-  return ((size_t)shrink_plan(k, t, rank).ks * (size_t)t * (size_t)rank * 4 + 255) & ~(size_t)255;
+size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank, int64_t adapters) {
+  const size_t u = ((size_t)shrink_plan(k, t, rank).ks * (size_t)t * (size_t)rank * 4 + 255) & ~(size_t)255;
+  return lora_ordered(t, rank, adapters) ? u + (((size_t)t * 4 + 255) & ~(size_t)255) : u;
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& a, float* u, hipStream_t s) {
@@ -421,11 +461,13 @@ hipError_t launch_lora_shrink(const LoraArgs& a, float* u, hipStream_t s) {
   int64_t slots = a.t < a.adapters ? a.t : a.adapters;
   if (slots > 16) slots = 16;
   while (slots > 1 && slots * tiles > 64) slots >>= 1;
-  const dim3 grid((unsigned)((a.rank + 16 * rt - 1) / (16 * rt) * ks), (unsigned)slots, (unsigned)tiles);
+  const int64_t ranks = (a.rank + 16 * rt - 1) / (16 * rt) * ks;
+  const int64_t extra = lora_order(a, u) != nullptr ? (tiles + ranks * slots - 1) / (ranks * slots) : 0;
+  const dim3 grid((unsigned)ranks, (unsigned)slots, (unsigned)(tiles + extra));
   auto go = [&, ks = ks](auto kern) {
     kern<<<grid, dim3(kThreads), 0, s>>>(static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.a),
-                                         static_cast<const int*>(a.ids), u, (int)a.k, (int)a.t, (int)a.rank,
-                                         (int)a.adapters, ks);
+                                         static_cast<const int*>(a.ids), u, lora_order(a, u), (int)a.k, (int)a.t,
+                                         (int)a.rank, (int)a.adapters, ks);
   };
   if (rt == 1) go(lora_shrink_kernel<1>);
   else go(lora_shrink_kernel<2>);

@@ -249,8 +249,9 @@ Q4LIN_API int64_t q4lin_fmt_workspace_bytes(int fmt, int64_t n, int64_t k, int64
  *
  * rank: a multiple of 8 from 8 to 256 (an adapter of a smaller rank is
  * padded with zeros); adapters: 1 to 2^20; T up to 2^19.  Both terms are
- * binary32 and y is rounded once.  workspace: q4lin_lora_workspace_bytes()
- * bytes, 256-byte aligned.  An infinity or NaN in one adapter stays in its
+ * binary32 and y is rounded once; a base sum that leaves binary32 is formed
+ * again exactly, as the base weight alone is.  workspace:
+ * q4lin_lora_workspace_bytes() bytes, 256-byte aligned.  An infinity or NaN in one adapter stays in its
  * own tokens' rows.  y must not overlap any input or the workspace.  Errors
  * as for q4lin_linear_fmt. */
 Q4LIN_API int q4lin_linear_lora(int fmt, const void *x, const void *w, const void *w_hi, const void *scales,

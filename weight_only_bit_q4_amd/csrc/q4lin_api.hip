@@ -614,7 +614,8 @@ int q4lin_linear_lora(int fmt, const void* x, const void* w, const void* w_hi, c
   hipStream_t s = static_cast<hipStream_t>(stream);
   float* u = static_cast<float*>(workspace);
   uint8_t* sums = static_cast<uint8_t*>(workspace) + p.u_bytes;
-  const q4lin::LoraArgs la{x, lora_a, lora_b, lora_scale, adapter_ids, y, n, k, t, adapters, rank};
+  const q4lin::LoraArgs la{x, lora_a, lora_b, lora_scale, adapter_ids, y, n, k, t, adapters, rank,
+                           fmt, w, w_hi, scales};
   if (p.tail) {  // the base product's kernel adds the adapters' term itself
     hipError_t e = q4lin::launch_lora_dots(la, u, s);
     if (e != hipSuccess) return Q4LIN_E_LAUNCH;

@@ -65,6 +65,7 @@
 //     once; an output that comes out non-finite (binary32 partials that left
 //     the range) is formed again exactly by its thread.
 #include "q4lin_device.h"
+#include "q4lin_exact.h"
 #include "q4lin_kernels.h"
 #include "q4lin_lora_tail.h"
 
@@ -201,13 +202,6 @@ __device__ __forceinline__ void w8_operands(uint32_t w0, uint32_t w1, bf16x8_t& 
   hi = __builtin_bit_cast(bf16x8_t, h);
 }
 
-// E4M3 (bias 7, subnormals) -> binary32, by its fields
-__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
-  const uint32_t e = (b >> 3) & 0xFu, m = b & 7u;
-  const float mag = e != 0u ? __builtin_bit_cast(float, ((e + 120u) << 23) | (m << 20)) : (float)m * 0x1p-9f;
-  return (b & 0x80u) ? -mag : mag;
-}
-
 // NVFP4: code dword w (E2M1 nibbles of k0..k7, even k low) times scale s ->
 // the eight exact bf16 weights in natural order.  E2M1 has at most 2
 // significant bits and E4M3 at most 4, so the binary32 product is exact
@@ -225,40 +219,6 @@ __device__ __forceinline__ bf16x8_t nvfp4_operand(uint32_t w, float s) {
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
-// Weight W[n][k] of format F in binary64, exact (the plain definition, for
-// the repair below).
-template <int F>
-__device__ double weight_exact(const uint8_t* __restrict__ lo, const uint8_t* __restrict__ hi,
-                               const uint8_t* __restrict__ sc, int K, int n, int k) {
-  const size_t r = (size_t)n;
-  if constexpr (F == FMT_BF16) {
-    return (double)bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(lo)[r * K + k]);
-  } else if constexpr (F == FMT_W8) {
-    const int c = (int)(int8_t)lo[r * K + k];
-    return (double)c * (double)f16_bits_to_f32(reinterpret_cast<const uint16_t*>(sc)[r * (K / 32) + k / 32]);
-  } else {
-    const uint32_t b = lo[r * (K / 2) + k / 2];
-    const int nib = (int)((k & 1) ? (b >> 4) : (b & 15u));
-    if constexpr (F == FMT_NVFP4) {
-      const int e = (nib >> 1) & 3, m = nib & 1;
-      double v = e == 0 ? 0.5 * m : __builtin_ldexp(1.0 + 0.5 * m, e - 1);
-      if (nib & 8) v = -v;
-      return v * (double)e4m3_to_f32(sc[r * (K / 16) + k / 16]);
-    } else {
-      const double s = (double)f16_bits_to_f32(reinterpret_cast<const uint16_t*>(sc)[r * (K / 64) + k / 64]);
-      if constexpr (F == FMT_Q4) {
-        return (double)(nib - 8) * s;
-      } else if constexpr (F == FMT_Q5) {
-        const int q = nib | ((int)((hi[r * (K / 8) + k / 8] >> (k & 7)) & 1u) << 4);
-        return (double)(q - 16) * s;
-      } else {
-        const int q = nib | ((int)((hi[r * (K / 4) + k / 4] >> (2 * (k & 3))) & 3u) << 4);
-        return (double)(q - 32) * s;
-      }
-    }
-  }
-}
-
 // An output whose binary32 partial sums left the range (activations near
 // the top of the bf16 range make the products of the offset codes overflow
 // although the exact sum may not) is formed again from the inputs: the sum
@@ -271,9 +231,7 @@ __device__ __attribute__((noinline)) uint16_t exact_output(const uint16_t* __res
                                                            const uint8_t* __restrict__ sc,
                                                            const uint16_t* __restrict__ res, int N, int K, int n,
                                                            int t) {
-  double acc = 0.0;
-  for (int k = 0; k < K; ++k)
-    acc += weight_exact<F>(lo, hi, sc, K, n, k) * (double)bf16_bits_to_f32(x[(size_t)t * K + k]);
+  double acc = exact_sum<F>(x, lo, hi, sc, K, n, t);
   if (res != nullptr) acc += (double)bf16_bits_to_f32(res[(size_t)t * N + n]);
   return f32_to_bf16_rne((float)acc);
 }
@@ -595,6 +553,7 @@ __device__ __forceinline__ void final_sum(const f32x4_t (&acc)[CT][TT], uint8_t*
       const double silu = g / (1.0 + exp(-g));
       return f32_to_bf16_rne((float)(silu * uv));
     } else if constexpr (LORA) {
+      if (!__builtin_isfinite(v)) v = exact_sum_call<F>(x, lo, hi, sc, K, n0 + col, t);  // rare
       return f32_to_bf16_rne((float)(v + (double)lora_share(lora, N, n0 + col, t, 0, 1)));
     } else {
       if (res != nullptr) v += (double)bf16_bits_to_f32(res[o]);  // LinearAdd
@@ -1123,7 +1082,12 @@ bf16_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, 
     }
     if (res != nullptr) v += (double)bf16_bits_to_f32(res[n]);  // LinearAdd
     uint16_t h = f32_to_bf16_rne((float)v);
-    if (!LORA && (h & 0x7F80u) == 0x7F80u) h = exact_output<FMT_BF16>(x, w, nullptr, nullptr, res, N, K, n, 0);  // rare
+    if ((h & 0x7F80u) == 0x7F80u) {  // rare
+      if constexpr (LORA)
+        h = f32_to_bf16_rne((float)(exact_sum_call<FMT_BF16>(x, w, nullptr, nullptr, K, n, 0) +
+                                    (double)lora_share(lora, N, n, 0, 0, 1)));
+      else h = exact_output<FMT_BF16>(x, w, nullptr, nullptr, res, N, K, n, 0);
+    }
     y[n] = h;
   };
   for (int r = gw; r < N; r += 2 * nw) {
@@ -1300,7 +1264,12 @@ fmt_gemv_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ lo, 
     }
     if (res != nullptr) v += (double)bf16_bits_to_f32(res[n]);  // LinearAdd
     uint16_t hv = f32_to_bf16_rne((float)v);
-    if (!LORA && (hv & 0x7F80u) == 0x7F80u) hv = exact_output<F>(x, lo, hi, sc, res, N, K, n, 0);  // rare
+    if ((hv & 0x7F80u) == 0x7F80u) {  // rare
+      if constexpr (LORA)
+        hv = f32_to_bf16_rne((float)(exact_sum_call<F>(x, lo, hi, sc, K, n, 0) +
+                                     (double)lora_share(lora, N, n, 0, 0, 1)));
+      else hv = exact_output<F>(x, lo, hi, sc, res, N, K, n, 0);
+    }
     y[n] = hv;
   };
   // The grid gives every wave its two rows gw and gw + nw (2 nw >= N).  All

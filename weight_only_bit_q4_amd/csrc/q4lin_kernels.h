@@ -226,6 +226,11 @@ struct LoraArgs {
   const void* ids;
   void* y;
   int64_t n, k, t, adapters, rank;
+  // the base product's weight, as in FmtArgs
+  int fmt;
+  const void* w;
+  const void* w_hi;
+  const void* w_sc;
 };
 // bytes of u, the tokens' rank values [t][rank] (in parts of a K split)
 size_t lora_u_bytes(int64_t k, int64_t t, int64_t rank, int64_t adapters);

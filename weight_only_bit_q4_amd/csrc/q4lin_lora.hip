@@ -29,6 +29,7 @@
 //
 // u is binary32 from end to end; the matrix cores take s_a u as two bf16
 // parts (split_bf16), so the adapters' term is as exact as the base sum.
+#include "q4lin_exact.h"
 #include "q4lin_kernels.h"
 #include "q4lin_mfma16.h"
 
@@ -189,6 +190,37 @@ lora_dots_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
   }
 }
 
+// The base product's weight and activations, for sums that left the range.
+struct BaseWeight {
+  const uint16_t* x;
+  const uint8_t* lo;
+  const uint8_t* hi;
+  const uint8_t* sc;
+  int fmt, K;
+};
+__device__ double exact_base(const BaseWeight& w, int n, int t) {
+  switch (w.fmt) {
+    case FMT_Q4: return exact_sum_call<FMT_Q4>(w.x, w.lo, w.hi, w.sc, w.K, n, t);
+    case FMT_Q5: return exact_sum_call<FMT_Q5>(w.x, w.lo, w.hi, w.sc, w.K, n, t);
+    case FMT_Q6: return exact_sum_call<FMT_Q6>(w.x, w.lo, w.hi, w.sc, w.K, n, t);
+    case FMT_W8: return exact_sum_call<FMT_W8>(w.x, w.lo, w.hi, w.sc, w.K, n, t);
+    case FMT_NVFP4: return exact_sum_call<FMT_NVFP4>(w.x, w.lo, w.hi, w.sc, w.K, n, t);
+    default: return exact_sum_call<FMT_BF16>(w.x, w.lo, w.hi, w.sc, w.K, n, t);
+  }
+}
+
+// s sum_r B[r] u[r] in binary32 (b: one row of an adapter, u: a token's first
+// part of KS, `part` floats apart)
+__device__ float adapter_term(const uint16_t* b, const float* u, size_t part, int R, int KS, float scale) {
+  float v = 0.f;
+  for (int r = 0; r < R; ++r) {
+    float ur = u[r];
+    for (int k = 1; k < KS; ++k) ur += u[k * part + r];
+    v = __builtin_fmaf(bf16_bits_to_f32(b[r]), ur, v);
+  }
+  return scale * v;
+}
+
 // A workgroup takes 16 tokens and every gridDim.x-th block of 64 NB rows; a
 // wave 16 NB of a block's rows.  RS: 32-rank steps that cover R.  The base
 // sums come in, and y goes out, in runs of 256 NB bytes of a token's row (a
@@ -203,7 +235,7 @@ __global__ void __launch_bounds__(256)
 lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ scale, const int* __restrict__ ids,
                    const float* __restrict__ u, const int* __restrict__ order, SumSource base,
                    uint16_t* __restrict__ y, int N, int T, int R, int L,
-                   int KS, int vec) {
+                   int KS, int vec, BaseWeight w) {
   constexpr int ROWS = 64 * NB;  // of a block
   constexpr int D = RS * NB <= 2 ? 4 : RS * NB <= 8 ? 2 : 1;  // adapters whose rows are in registers
   __shared__ __attribute__((aligned(16))) float term[2][16][ROWS + 4];
@@ -292,6 +324,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   for (int i = 0; i < 4; ++i) te[i] = base.texp != nullptr ? base.texp[tw[i]] : 0;
 
   int buf = 0;
+  bool left = false;  // one of this lane's base sums left the range
   for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS, buf ^= 1) {
     const int n0 = nb0 + wave * (16 * NB), nl = nb0 + NB * lane;
     int re[NB];
@@ -365,6 +398,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
       for (int j = 0; j < NB; ++j) {
         // (the many-token route's sums carry a power of two per token and row)
         const float f = __builtin_ldexpf(cur.v[i][j], te[i] - re[j]);
+        left |= !__builtin_isfinite(f);
         h[j] = f32_to_bf16_rne(f + term[buf][4 * wave + i][NB * lane + j]);
       }
       uint16_t* o = y + (size_t)tw[i] * N + nl;
@@ -379,6 +413,31 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
       }
     }
     cur = next;
+  }
+  if (!left) return;
+
+  // Rare: a base sum that is not finite is formed again exactly, as the base
+  // product's own kernels do, and its output with it.
+  for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS) {
+    const Sums s = load_sums(nb0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (t0 + 4 * wave + i >= T) break;
+      const int t = tw[i];
+      const uint32_t own = (uint32_t)ids[t];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int n = nb0 + NB * lane + j;
+        if (n >= N) continue;
+        const float f = __builtin_ldexpf(s.v[i][j], te[i] - (base.texp != nullptr ? base.rexp[n] : 0));
+        if (__builtin_isfinite(f)) continue;
+        float v = (float)exact_base(w, n, t);
+        if (own < (uint32_t)L)
+          v += adapter_term(b + ((size_t)own * N + n) * R, u + (size_t)t * R, (size_t)T * R, R, KS,
+                            scale != nullptr ? scale[own] : 1.0f);
+        y[(size_t)t * N + n] = f32_to_bf16_rne(v);
+      }
+    }
   }
 }
 
@@ -422,10 +481,12 @@ hipError_t launch_finish(const LoraArgs& a, const float* u, const SumSource& bas
   const int64_t blocks = (a.n + (wide ? 255 : 63)) / (wide ? 256 : 64);
   const int64_t most = 768 / tiles > 1 ? 768 / tiles : 1;
   const dim3 grid((unsigned)(blocks < most ? blocks : most), (unsigned)tiles);
+  const BaseWeight w{static_cast<const uint16_t*>(a.x), static_cast<const uint8_t*>(a.w),
+                     static_cast<const uint8_t*>(a.w_hi), static_cast<const uint8_t*>(a.w_sc), a.fmt, (int)a.k};
   auto go = [&](auto kern) {
     kern<<<grid, dim3(256), 0, s>>>(static_cast<const uint16_t*>(a.b), static_cast<const float*>(a.scale),
                                     static_cast<const int*>(a.ids), u, lora_order(a, u), base, static_cast<uint16_t*>(a.y), (int)a.n,
-                                    (int)a.t, (int)a.rank, (int)a.adapters, ks, vec);
+                                    (int)a.t, (int)a.rank, (int)a.adapters, ks, vec, w);
   };
   if (wide) go(lora_finish_kernel<RS, 4>);
   else go(lora_finish_kernel<RS, 1>);

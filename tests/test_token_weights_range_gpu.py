@@ -120,3 +120,27 @@ def test_lora_of_large_activations_on_many_tokens(n, k, t, rank):
     y = run(0, planes, x, a, b, ids, scale, "many tokens")
     want, bound = tw.lora_reference(x, w64, a, b, ids, scale, is_tiled(0, n, k, t))
     check(y, want, bound, "many tokens")
+
+
+# both sides of where the adapters' term changes its path, one and four rows a thread
+@pytest.mark.parametrize("fmt,n,t,rank", [(0, 200, 2, 16), (0, 200, 16, 64), (0, 200, 32, 128), (0, 200, 32, 136),
+                                          (0, 200, 33, 16), (0, 200, 40, 40), (0, 200, 200, 24), (0, 1040, 1100, 48),
+                                          (3, 200, 1, 16), (5, 200, 1, 200), (4, 200, 20, 24), (1, 200, 40, 256)])
+def test_lora_infinities_in_b_and_a(fmt, n, t, rank):
+    """An infinity in B is one of its row's outputs, with its sign; one in A is one of every output."""
+    planes, w64, x, a, b, ids, scale = case(fmt, n, 256, t, rank, 4400 + t + rank)
+    ids[t // 2:] = 1
+    clean = run(fmt, planes, x, a, b, ids, scale, "finite")
+    b[1, 5, 2] = float("inf")
+    b[1, 9, 3] = -float("inf")
+    b[1, 11, 0], b[1, 11, 1] = float("inf"), -float("inf")  # (an infinity or NaN, by the rank values' signs)
+    y = run(fmt, planes, x, a, b, ids, scale, "infinities in B").cpu()
+    want, _ = tw.lora_reference(x, w64, a, b, ids, scale, False)
+    edge = ~torch.isfinite(want)
+    assert edge.any() and edge.sum(1).max() == 3
+    assert torch.equal(y[edge].double().nan_to_num(nan=7.0), want[edge].nan_to_num(nan=7.0))
+    assert torch.equal(y[~edge].view(torch.int16), clean.cpu()[~edge].view(torch.int16))
+    a[1, 7, 100] = -float("inf")
+    y = run(fmt, planes, x, a, b, ids, scale, "infinities in A and B").cpu()
+    want, _ = tw.lora_reference(x, w64, a, b, ids, scale, False)
+    assert torch.equal(y[ids == 1].double().nan_to_num(nan=7.0), want[ids == 1].nan_to_num(nan=7.0))

@@ -324,7 +324,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   for (int i = 0; i < 4; ++i) te[i] = base.texp != nullptr ? base.texp[tw[i]] : 0;
 
   int buf = 0;
-  bool left = false;  // one of this lane's base sums left the range
+  bool left = false;  // one of this lane's outputs is not finite
   for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS, buf ^= 1) {
     const int n0 = nb0 + wave * (16 * NB), nl = nb0 + NB * lane;
     int re[NB];
@@ -398,8 +398,8 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
       for (int j = 0; j < NB; ++j) {
         // (the many-token route's sums carry a power of two per token and row)
         const float f = __builtin_ldexpf(cur.v[i][j], te[i] - re[j]);
-        left |= !__builtin_isfinite(f);
         h[j] = f32_to_bf16_rne(f + term[buf][4 * wave + i][NB * lane + j]);
+        left |= (h[j] & 0x7F80u) == 0x7F80u;
       }
       uint16_t* o = y + (size_t)tw[i] * N + nl;
       if (vec && NB == 4) {
@@ -416,8 +416,10 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   }
   if (!left) return;
 
-  // Rare: a base sum that is not finite is formed again exactly, as the base
-  // product's own kernels do, and its output with it.
+  // Rare: an output that is not finite is formed again: a base sum that is
+  // not finite exactly, as the base product's own kernels do, the term in
+  // binary32 as the rank values are (an infinity of B times their two parts is
+  // NaN where the second part is zero or of the other sign).
   for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS) {
     const Sums s = load_sums(nb0);
 #pragma unroll
@@ -428,10 +430,9 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int n = nb0 + NB * lane + j;
-        if (n >= N) continue;
-        const float f = __builtin_ldexpf(s.v[i][j], te[i] - (base.texp != nullptr ? base.rexp[n] : 0));
-        if (__builtin_isfinite(f)) continue;
-        float v = (float)exact_base(w, n, t);
+        if (n >= N || (y[(size_t)t * N + n] & 0x7F80u) != 0x7F80u) continue;
+        float v = __builtin_ldexpf(s.v[i][j], te[i] - (base.texp != nullptr ? base.rexp[n] : 0));
+        if (!__builtin_isfinite(v)) v = (float)exact_base(w, n, t);
         if (own < (uint32_t)L)
           v += adapter_term(b + ((size_t)own * N + n) * R, u + (size_t)t * R, (size_t)T * R, R, KS,
                             scale != nullptr ? scale[own] : 1.0f);

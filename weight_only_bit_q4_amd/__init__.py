@@ -409,30 +409,52 @@ def linear_fmt(fmt, x, w, w_hi=None, scales=None, y=None, stream=None):
     return y
 
 
-def _checked(name, ten, shape, size):
-    """The tensor's address; it must be contiguous, of this shape and element size."""
-    if ten.shape != shape or ten.element_size() != size or not ten.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of shape %s with %d-byte elements, got %s of %s" % (
-            name, shape, size, tuple(ten.shape), ten.dtype))
+_DTYPES = {}  # the element types that are read as each kind of value (bf16 and fp16 also as their bits)
+_torch = None  # the module, from the first call on (an import statement a function costs each call 0.3 us)
+
+
+def _place(x):
+    """The index of the GPU that ``x`` is on (-1: none), for the checks of the other tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch, bits = torch, (torch.int16, torch.uint16)
+        _DTYPES.update(bf16=(torch.bfloat16, *bits), fp16=(torch.float16, *bits), codes=(torch.uint8, torch.int8),
+                       int32=(torch.int32,), float32=(torch.float32,))
+    return x.get_device()
+
+
+def _checked(name, ten, shape, kind, place):
+    """The tensor's address; it must be contiguous, of this shape and kind of elements, on x's GPU."""
+    if ten.shape != shape or ten.dtype not in _DTYPES[kind] or not ten.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s with %s elements, got %s of %s" % (
+            name, tuple(shape), kind, tuple(ten.shape), ten.dtype))
+    # (an index costs the host half of what comparing devices does)
+    if ten.get_device() != place:
+        raise ValueError("%s must be on x's GPU, not on %s" % (name, ten.device))
     return ten.data_ptr()
+
+
+def _on_gpu(place):
+    if place < 0:
+        raise ValueError("the tensors must be on a GPU")
 
 
 def _new(shape, dtype, device):
     """An uninitialised contiguous matrix (``empty_strided`` costs the host less than ``empty``)."""
-    import torch
-
-    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    return _torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
 
 
 def _workspace(need, workspace, device):
     """(address, bytes, tensor to keep) of the caller's workspace or a new one of ``need`` bytes."""
-    import torch
-
     if need < 0:
         raise Q4LinError(-need)
     if workspace is None:
-        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
+        workspace = _torch.empty_strided((need,), (1,), dtype=_torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
+    if workspace.get_device() != device.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on x's GPU")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -440,15 +462,13 @@ def _stream_of(stream, device, *made):
     """The handle of ``stream`` (None: the current one).  Tensors ``made`` by
     this call belong to the current stream; on another one they are kept from
     reuse until its work is done."""
-    import torch
-
-    if stream is None and device.index is not None:
+    if stream is None:
         # the handle alone: the Stream object costs the host 2 us, as much as an allocation
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    current = torch.cuda.current_stream(device).cuda_stream
-    if stream is None or stream == current:
+        return _torch._C._cuda_getCurrentRawStream(device.index)
+    current = _torch.cuda.current_stream(device).cuda_stream
+    if stream == current:
         return current
-    other = torch.cuda.ExternalStream(stream, device=device)
+    other = _torch.cuda.ExternalStream(stream, device=device)
     for ten in made:
         if ten is not None:
             ten.record_stream(other)
@@ -465,12 +485,14 @@ _FMT_PLANES = {  # bytes per row of K weights: codes, high plane, scales
 }
 
 
-def _plane(name, ten, rows, per_row):
+def _plane(name, ten, rows, per_row, place):
     """The address of a weight's plane (None: the format has none)."""
     if per_row == 0:
         return None
     if ten is None or not ten.is_contiguous() or ten.numel() * ten.element_size() != rows * per_row:
         raise ValueError("%s must be a contiguous plane of %d bytes for each of the %d rows" % (name, per_row, rows))
+    if ten.get_device() != place:
+        raise ValueError("%s must be on x's GPU, not on %s" % (name, ten.device))
     return ten.data_ptr()
 
 
@@ -486,28 +508,27 @@ def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, 
     of 8 up to 256), ``adapter_ids`` int32 ``[T]``, ``lora_scale`` float32
     ``[L]`` or None for ones.  Returns ``y`` ``[T, N]``.
     """
-    import torch
-
     t, k = x.shape
     n = codes.shape[0]
     adapters, rank = lora_a.shape[0], lora_a.shape[1]
     if fmt not in _FMT_PLANES:
         raise Q4LinError(Q4LIN_E_FORMAT)
     per_row = _FMT_PLANES[fmt](k)
-    wp = _plane("codes", codes, n, per_row[0])
-    hp = _plane("codes_hi", codes_hi, n, per_row[1])
-    cp = _plane("scales", scales, n, per_row[2])
-    xp = _checked("x", x, (t, k), 2)
-    ap = _checked("lora_a", lora_a, (adapters, rank, k), 2)
-    bp = _checked("lora_b", lora_b, (adapters, n, rank), 2)
-    ip = _checked("adapter_ids", adapter_ids, (t,), 4)
-    sp = _checked("lora_scale", lora_scale, (adapters,), 4) if lora_scale is not None else None
-    device = x.device
+    device, place = x.device, _place(x)
+    wp = _plane("codes", codes, n, per_row[0], place)
+    hp = _plane("codes_hi", codes_hi, n, per_row[1], place)
+    cp = _plane("scales", scales, n, per_row[2], place)
+    xp = _checked("x", x, (t, k), "bf16", place)
+    ap = _checked("lora_a", lora_a, (adapters, rank, k), "bf16", place)
+    bp = _checked("lora_b", lora_b, (adapters, n, rank), "bf16", place)
+    ip = _checked("adapter_ids", adapter_ids, (t,), "int32", place)
+    sp = _checked("lora_scale", lora_scale, (adapters,), "float32", place) if lora_scale is not None else None
+    _on_gpu(place)
     if y is None:
-        y = _new((t, n), torch.bfloat16, device)
+        y = _new((t, n), _torch.bfloat16, device)
         yp = y.data_ptr()
     else:
-        yp = _checked("y", y, (t, n), 2)
+        yp = _checked("y", y, (t, n), "bf16", place)
     work, work_bytes, workspace = _workspace(q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank), workspace, device)
     stream = _stream_of(stream, device, y, workspace)
     st = load().q4lin_linear_lora(fmt, xp, wp, hp, cp, ap, bp, sp, ip, yp, n, k, t, adapters, rank, work, work_bytes,
@@ -517,16 +538,16 @@ def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, 
     return y
 
 
-def _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down):
+def _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down, place):
     """(experts, inner, the six addresses) of a layer's expert weights."""
     experts, inner = codes_gate.shape[0], codes_gate.shape[1]
     return experts, inner, (
-        _checked("codes_gate", codes_gate, (experts, inner, k // 2), 1),
-        _checked("scales_gate", scales_gate, (experts, inner, k // 64), 2),
-        _checked("codes_up", codes_up, (experts, inner, k // 2), 1),
-        _checked("scales_up", scales_up, (experts, inner, k // 64), 2),
-        _checked("codes_down", codes_down, (experts, k, inner // 2), 1),
-        _checked("scales_down", scales_down, (experts, k, inner // 64), 2))
+        _checked("codes_gate", codes_gate, (experts, inner, k // 2), "codes", place),
+        _checked("scales_gate", scales_gate, (experts, inner, k // 64), "fp16", place),
+        _checked("codes_up", codes_up, (experts, inner, k // 2), "codes", place),
+        _checked("scales_up", scales_up, (experts, inner, k // 64), "fp16", place),
+        _checked("codes_down", codes_down, (experts, k, inner // 2), "codes", place),
+        _checked("scales_down", scales_down, (experts, k, inner // 64), "fp16", place))
 
 
 def moe_route(x, router, top_k, renormalize=True, stream=None):
@@ -535,15 +556,15 @@ def moe_route(x, router, top_k, renormalize=True, stream=None):
     divided by their sum where ``renormalize``.  ``x`` bf16 ``[T, K]``,
     ``router`` bf16 ``[E, K]``.  Returns ``(ids int32 [T, top_k], weights
     float32 [T, top_k])``."""
-    import torch
-
     t, k = x.shape
     experts = router.shape[0]
-    xp = _checked("x", x, (t, k), 2)
-    rp = _checked("router", router, (experts, k), 2)
-    ids = _new((t, top_k), torch.int32, x.device)
-    weights = _new((t, top_k), torch.float32, x.device)
-    stream = _stream_of(stream, x.device, ids, weights)
+    device, place = x.device, _place(x)
+    xp = _checked("x", x, (t, k), "bf16", place)
+    rp = _checked("router", router, (experts, k), "bf16", place)
+    _on_gpu(place)
+    ids = _new((t, top_k), _torch.int32, device)
+    weights = _new((t, top_k), _torch.float32, device)
+    stream = _stream_of(stream, device, ids, weights)
     st = load().q4lin_moe_route(xp, rp, ids.data_ptr(), weights.data_ptr(), k, experts, top_k, t,
                                 1 if renormalize else 0, stream)
     if st != Q4LIN_OK:
@@ -559,19 +580,20 @@ def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, c
     gate and up codes uint8 ``[E, I, K/2]``, scales fp16 ``[E, I, K/64]``;
     down codes ``[E, K, I/2]``, scales ``[E, K, I/64]``.  Returns ``y`` bf16
     ``[T, K]``."""
-    import torch
-
     t, k = x.shape
     top_k = ids.shape[1]
-    xp = _checked("x", x, (t, k), 2)
-    ip = _checked("ids", ids, (t, top_k), 4)
-    vp = _checked("weights", weights, (t, top_k), 4)
-    experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
+    device, place = x.device, _place(x)
+    xp = _checked("x", x, (t, k), "bf16", place)
+    ip = _checked("ids", ids, (t, top_k), "int32", place)
+    vp = _checked("weights", weights, (t, top_k), "float32", place)
+    experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down,
+                                            place)
+    _on_gpu(place)
     if y is None:
-        y = _new((t, k), torch.bfloat16, x.device)
-    yp = _checked("y", y, (t, k), 2)
-    wp, wb, workspace = _workspace(q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, x.device)
-    stream = _stream_of(stream, x.device, y, workspace)
+        y = _new((t, k), _torch.bfloat16, device)
+    yp = _checked("y", y, (t, k), "bf16", place)
+    wp, wb, workspace = _workspace(q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, device)
+    stream = _stream_of(stream, device, y, workspace)
     st = load().q4lin_moe_experts(xp, ip, vp, *planes, yp, inner, k, experts, top_k, t, wp, wb, stream)
     if st != Q4LIN_OK:
         raise Q4LinError(st)
@@ -583,18 +605,18 @@ def moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, sca
     """A whole mixture-of-experts layer on torch device tensors: ``moe_route``
     and ``moe_experts`` in one call (their arguments).  Returns ``(y, ids,
     weights)``."""
-    import torch
-
     t, k = x.shape
-    xp = _checked("x", x, (t, k), 2)
-    experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down)
-    rp = _checked("router", router, (experts, k), 2)
-    device = x.device
-    ids = _new((t, top_k), torch.int32, device)
-    weights = _new((t, top_k), torch.float32, device)
+    device, place = x.device, _place(x)
+    xp = _checked("x", x, (t, k), "bf16", place)
+    experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down,
+                                            place)
+    rp = _checked("router", router, (experts, k), "bf16", place)
+    _on_gpu(place)
+    ids = _new((t, top_k), _torch.int32, device)
+    weights = _new((t, top_k), _torch.float32, device)
     if y is None:
-        y = _new((t, k), torch.bfloat16, device)
-    yp = _checked("y", y, (t, k), 2)
+        y = _new((t, k), _torch.bfloat16, device)
+    yp = _checked("y", y, (t, k), "bf16", place)
     wp, wb, workspace = _workspace(q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, device)
     stream = _stream_of(stream, device, y, workspace, ids, weights)
     st = load().q4lin_moe(xp, rp, *planes, yp, ids.data_ptr(), weights.data_ptr(), inner, k, experts, top_k, t,

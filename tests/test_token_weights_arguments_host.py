@@ -44,10 +44,9 @@ def refused(call, change, match):
         getattr(q, call)(**args)
 
 
-@pytest.mark.parametrize("call,name", EACH)
+# (the planes of a linear_lora weight are read as bytes)
+@pytest.mark.parametrize("call,name", [v for v in EACH if v not in (("linear_lora", "codes"), ("linear_lora", "scales"))])
 def test_other_types_of_the_same_size(call, name):
-    if call == "linear_lora" and name in ("codes", "scales"):
-        pytest.skip("a weight's planes are read as bytes")
     v = CALLS[call][0]()[name]
     other = {torch.bfloat16: torch.float16, torch.float16: torch.bfloat16, torch.uint8: torch.bool,
              torch.int32: torch.float32, torch.float32: torch.int32}[v.dtype]

@@ -825,6 +825,7 @@ moe_down_few_kernel(const uint16_t* h, const uint8_t* codes, const uint16_t* sca
 // passes (gate and up).
 // ---------------------------------------------------------------------------
 constexpr int kWideWaves = 8;
+constexpr int kWideQuad = 4;  // stages of a share come in quads, as the scales do
 template <int R, bool DOWN, int BT>
 __global__ void __launch_bounds__(64 * kWideWaves, 4)
 moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scales0, const uint8_t* codes1,
@@ -846,10 +847,9 @@ moe_wide_kernel(const uint16_t* act, const uint8_t* codes0, const uint16_t* scal
   if (e < 0) return;
   const int n0 = (blockIdx.x * kWideWaves + wave) * (16 * RT);  // this wave's first output row
   const int G = K >> 6, stages = (G + 1) >> 1;
-  // (shares of whole quads of stages, as the scales come)
-  const int quads = (stages + 3) >> 2;
+  const int quads = (stages + kWideQuad - 1) / kWideQuad;
   const int part = DOWN ? blockIdx.z : 0, parts = DOWN ? gridDim.z : 1;
-  const int sb = 4 * (quads * part / parts), se = min(4 * (quads * (part + 1) / parts), stages);
+  const int sb = kWideQuad * (quads * part / parts), se = min(kWideQuad * (quads * (part + 1) / parts), stages);
   const uint32_t crow = (uint32_t)K >> 1;
   rsrc_t rc[R];
 #pragma unroll
@@ -1113,15 +1113,21 @@ constexpr int64_t kManyPairs = 18;
 // workgroups that the chip holds at a time (two per CU, by LDS and registers)
 constexpr int64_t kResident = 512;
 
-// Into how many shares (of those below) to split `stages` stages of K, when
-// `groups` workgroups take a whole K each: the rounds of resident workgroups
-// times a share's stages and the `extra` that a workgroup's start and end cost.
-int k_split(int64_t groups, int64_t stages, int64_t extra, int64_t most, bool powers) {
+// Into how many shares (of those below) to split `stages` stages of K, handed
+// out in runs of `unit`, when `groups` workgroups take a whole K each: the
+// rounds of resident workgroups times the longest share's stages and the
+// `extra` that a workgroup's start and end cost; in runs, among equals the
+// most shares, whose lengths are more even on the whole.  No share is empty
+// (12 tokens on all of seven experts, inner 960: 28.7 us with two shares, 35.4
+// with two and six empty ones).
+int k_split(int64_t groups, int64_t stages, int64_t unit, int64_t extra, int64_t most, bool powers) {
+  const int64_t units = (stages + unit - 1) / unit;
   int best = 1;
   int64_t cost = INT64_MAX;
-  for (int64_t s = 1; s <= most && s <= stages; s = powers ? 2 * s : s + 1) {
-    const int64_t c = (groups * s + kResident - 1) / kResident * ((stages + s - 1) / s + extra);
-    if (c < cost) {
+  for (int64_t s = 1; s <= most && s <= units; s = powers ? 2 * s : s + 1) {
+    const int64_t longest = (units + s - 1) / s * unit;
+    const int64_t c = (groups * s + kResident - 1) / kResident * ((longest < stages ? longest : stages) + extra);
+    if (c < cost || (unit > 1 && c == cost)) {
       cost = c;
       best = (int)s;
     }
@@ -1153,9 +1159,11 @@ bool few_pairs(const MoeArgs& a) {
   return pairs * a.inner <= kFewColumns &&
          (a.t == 1 || (a.t <= kFewTokens && pairs <= kPairGrid && 2 * pairs <= a.experts));
 }
-// parts of the down products' sums
+// parts of the down products' sums (moe_wide_kernel hands out whole quads of
+// stages)
 int down_parts(const MoeArgs& a) {
-  return k_split(ceil_div(a.k, kWideWaves * 16 * kWideRowTiles) * experts_hit(a), ceil_div(a.inner, 128), 4, 8, false);
+  return k_split(ceil_div(a.k, kWideWaves * 16 * kWideRowTiles) * experts_hit(a), ceil_div(a.inner, 128), kWideQuad, 4,
+                 8, false);
 }
 
 hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t s) {
@@ -1178,7 +1186,7 @@ hipError_t launch_gated(const MoeArgs& a, void* h, const double* lg, hipStream_t
     return hipGetLastError();
   }
   constexpr int R = kRowTiles;
-  const int wk = k_split(ceil_div(a.inner, kWaves * 8 * R) * experts_hit(a), ceil_div(a.k, 256), 2, kWaves, true);
+  const int wk = k_split(ceil_div(a.inner, kWaves * 8 * R) * experts_hit(a), ceil_div(a.k, 256), 1, 2, kWaves, true);
   const unsigned blocks = (unsigned)ceil_div(a.inner, kWaves / wk * 8 * R);
   auto go = [&](auto kern, unsigned rows) {
     kern<<<dim3(blocks, rows), dim3(kThreads), 0, s>>>(

@@ -1150,14 +1150,17 @@ unsigned grid_rows(const MoeArgs& a) {
 // Whether one launch makes the down products and their sums: a single token,
 // or a few that share few experts (16 waves for every 16 or 32 rows of y; two
 // launches fewer, but an expert is read again for every token that chose it),
-// while a workgroup's rows of all pairs are short (20 pairs of inner 5120 on
-// 640 rows: the layer 66 us against 51, 9 of 3904 on 1088 38 against 36; 6 of
-// 5632 on 832 32 against 33, 2 of 14336 on 5120 58 against 68).
-constexpr int64_t kFewColumns = 35 * 1024;
+// while a workgroup's rows of all pairs are short.  The layer in us, in one
+// launch / in three: one token, 9 pairs of inner 3904 on 1088 rows 38 / 42, 16
+// of 2816 on 2048 44 / 48, 8 of 7168 on 2048 50 / 51, 16 of 4096 on 2048 56 /
+// 55, 20 of 5120 on 640 70 / 61; two tokens, 16 pairs of 1792 on 2048 32 / 34;
+// four, 16 of 1856 on 2048 33 / 33, 24 of 1408 40 / 40; three, 9 of 3904 on
+// 1088 38.3 / 36.6; eight, 16 of 2048 on 1024 27 / 25.
+constexpr int64_t kFewColumnsOne = 56 * 1024, kFewColumns = 30 * 1024;
 bool few_pairs(const MoeArgs& a) {
   const int64_t pairs = a.t * a.top_k;
-  return pairs * a.inner <= kFewColumns &&
-         (a.t == 1 || (a.t <= kFewTokens && pairs <= kPairGrid && 2 * pairs <= a.experts));
+  if (a.t == 1) return pairs * a.inner <= kFewColumnsOne;
+  return a.t <= kFewTokens && pairs <= kPairGrid && 2 * pairs <= a.experts && pairs * a.inner <= kFewColumns;
 }
 // parts of the down products' sums (moe_wide_kernel hands out whole quads of
 // stages)

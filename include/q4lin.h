@@ -287,10 +287,12 @@ Q4LIN_API int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int6
  * q4lin_moe_experts takes them (routing rules of one's own; one process's
  * share of the experts): there an id outside 0..experts-1 contributes
  * nothing, a token without a valid id gets zeros, and an expert that a token
- * names twice counts twice.  The sums are binary32 or wider, h keeps 16
- * significant bits, y is rounded once.  The weights of an expert are read
- * once for up to 16 of its tokens (32 where the tokens per expert are many;
- * the down weights once per token where the tokens are few).
+ * names twice counts twice.  (For a share of fewer experts than a token has
+ * choices, pass top_k = experts: the numbers and weights of the token's
+ * choices here in any of its places, -1 in the others.)  The sums are binary32
+ * or wider, h keeps 16 significant bits, y is rounded once.  The weights of an
+ * expert are read once for up to 16 of its tokens (32 where the tokens per
+ * expert are many; the down weights once per token where the tokens are few).
  *
  * K and inner: positive multiples of 64; 1 <= experts <= 1024; 1 <= top_k <=
  * experts; 2 T K, 4 T top_k inner and T top_k K each below 2^31.  workspace

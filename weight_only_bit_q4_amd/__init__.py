@@ -572,13 +572,24 @@ def moe_route(x, router, top_k, renormalize=True, stream=None):
     return ids, weights
 
 
+def _by_expert(ids, weights, experts):
+    """Routing of more choices than there are experts, as one place for each
+    expert: its number where the token chose it (else -1) and the sum of the
+    weights with which it did."""
+    each = _torch.arange(experts, dtype=_torch.int32, device=ids.device)
+    chosen = ids[:, None, :] == each[:, None]
+    total = _torch.where(chosen, weights[:, None, :], 0.0).sum(2)
+    return _torch.where(chosen.any(2), each, -1), total
+
+
 def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down, y=None,
                 workspace=None, stream=None):
     """``y[t] = sum_j weights[t, j] Wd_e (silu(Wg_e x[t]) * (Wu_e x[t]))`` with
     ``e = ids[t, j]`` (outside ``0..E-1``: nothing), on torch device tensors.
     ``x`` bf16 ``[T, K]``; ``ids`` int32, ``weights`` float32 ``[T, top_k]``;
     gate and up codes uint8 ``[E, I, K/2]``, scales fp16 ``[E, I, K/64]``;
-    down codes ``[E, K, I/2]``, scales ``[E, K, I/64]``.  Returns ``y`` bf16
+    down codes ``[E, K, I/2]``, scales ``[E, K, I/64]``.  ``top_k`` may exceed
+    E (a share of the experts smaller than ``top_k``).  Returns ``y`` bf16
     ``[T, K]``."""
     t, k = x.shape
     top_k = ids.shape[1]
@@ -589,6 +600,13 @@ def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, c
     experts, inner, planes = _expert_planes(k, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down,
                                             place)
     _on_gpu(place)
+    if top_k > experts:  # the library takes at most one place for each expert
+        if stream is None:
+            ids, weights = _by_expert(ids, weights, experts)
+        else:
+            with _torch.cuda.stream(_torch.cuda.ExternalStream(stream, device=device)):
+                ids, weights = _by_expert(ids, weights, experts)
+        top_k, ip, vp = experts, ids.data_ptr(), weights.data_ptr()
     if y is None:
         y = _new((t, k), _torch.bfloat16, device)
     yp = _checked("y", y, (t, k), "bf16", place)

@@ -293,6 +293,11 @@ Q4LIN_API int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int6
  * or wider, h keeps 16 significant bits, y is rounded once.  The weights of an
  * expert are read once for up to 16 of its tokens (32 where the tokens per
  * expert are many; the down weights once per token where the tokens are few).
+ * Range: |x| and |h_j| below 2^114 (the codes enter their sums as 128 + code,
+ * the offset is taken off each group's sum).  Past it, or with an infinity or
+ * NaN in x, the token's row of y holds infinities or NaN; they are not formed
+ * again, unlike the outputs of the single products above, and no other row is
+ * touched.
  *
  * K and inner: positive multiples of 64; 1 <= experts <= 1024; 1 <= top_k <=
  * experts; 2 T K, 4 T top_k inner and T top_k K each below 2^31.  workspace

@@ -144,3 +144,44 @@ def test_lora_infinities_in_b_and_a(fmt, n, t, rank):
     y = run(fmt, planes, x, a, b, ids, scale, "infinities in A and B").cpu()
     want, _ = tw.lora_reference(x, w64, a, b, ids, scale, False)
     assert torch.equal(y[ids == 1].double().nan_to_num(nan=7.0), want[ids == 1].nan_to_num(nan=7.0))
+
+
+# -- experts: within the range that the header states, and past it -------------------
+def layer_case(t, experts=6, top_k=2, inner=192, k=320, seed=4500):
+    planes, values = tw.expert_weights(experts, inner, k, seed)
+    x = tw.bf16((t, k), seed + t)
+    g = torch.Generator().manual_seed(seed + 1)
+    ids = torch.rand(t, experts, generator=g).argsort(1)[:, :top_k].to(torch.int32)
+    return planes, values, x, ids, torch.rand(t, top_k, generator=g)
+
+
+def run_experts(planes, x, ids, weights, what):
+    announce("moe_experts %s t=%d" % (what, x.shape[0]))
+    y = q4.moe_experts(x.cuda(), ids.cuda(), weights.cuda(), *[p.cuda() for p in planes])
+    torch.cuda.synchronize()
+    return y
+
+
+@pytest.mark.parametrize("t", [1, 4, 12, 40, 90])
+@pytest.mark.parametrize("power", [-60, -20, 20, 50])
+def test_experts_of_large_and_small_activations(t, power):
+    """Gated values of up to about 2^105, and down to the subnormals."""
+    planes, values, x, ids, weights = layer_case(t)
+    x = (x.double() * 2.0 ** power).to(torch.bfloat16)
+    y = run_experts(planes, x, ids, weights, "2^%d" % power)
+    want, bound = tw.experts_reference(x, ids, weights, values)
+    # (a gated value below the smallest normal bf16 keeps that one's last place)
+    check(y, want, bound + 192 * 2.0 ** -133, "large and small activations")
+
+
+@pytest.mark.parametrize("t", [2, 4, 12, 40, 90])
+@pytest.mark.parametrize("value", [2.0 ** 120, float("inf"), float("nan")])
+def test_experts_past_the_range(t, value):
+    """The row of a token with such values is not finite, all others as without them."""
+    planes, values, x, ids, weights = layer_case(t)
+    clean = run_experts(planes, x, ids, weights, "finite").cpu()
+    x[1, 64:128] = value
+    y = run_experts(planes, x, ids, weights, "past the range").cpu()
+    assert not torch.isfinite(y[1].float()).any()
+    rest = torch.arange(t) != 1
+    assert torch.equal(y[rest].view(torch.int16), clean[rest].view(torch.int16))

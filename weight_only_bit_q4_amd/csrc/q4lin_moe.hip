@@ -1116,19 +1116,21 @@ constexpr int64_t kResident = 512;
 // Into how many shares (of those below) to split `stages` stages of K, handed
 // out in runs of `unit`, when `groups` workgroups take a whole K each: the
 // rounds of resident workgroups times the longest share's stages and the
-// `extra` that a workgroup's start and end cost; in runs, among equals the
-// most shares, whose lengths are more even on the whole.  No share is empty
-// (12 tokens on all of seven experts, inner 960: 28.7 us with two shares, 35.4
-// with two and six empty ones).
+// `extra` that a workgroup's start and end cost; in runs, among equals of as
+// many rounds the most shares, whose lengths are more even on the whole.  No
+// share is empty (12 tokens on all of seven experts, inner 960: 28.7 us with
+// two shares, 35.4 with two and six empty ones).
 int k_split(int64_t groups, int64_t stages, int64_t unit, int64_t extra, int64_t most, bool powers) {
   const int64_t units = (stages + unit - 1) / unit;
   int best = 1;
-  int64_t cost = INT64_MAX;
+  int64_t cost = INT64_MAX, fewest = 0;
   for (int64_t s = 1; s <= most && s <= units; s = powers ? 2 * s : s + 1) {
+    const int64_t rounds = (groups * s + kResident - 1) / kResident;
     const int64_t longest = (units + s - 1) / s * unit;
-    const int64_t c = (groups * s + kResident - 1) / kResident * ((longest < stages ? longest : stages) + extra);
-    if (c < cost || (unit > 1 && c == cost)) {
+    const int64_t c = rounds * ((longest < stages ? longest : stages) + extra);
+    if (c < cost || (unit > 1 && c == cost && rounds == fewest)) {
       cost = c;
+      fewest = rounds;
       best = (int)s;
     }
   }

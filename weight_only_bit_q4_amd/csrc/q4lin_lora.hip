@@ -324,7 +324,7 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
   for (int i = 0; i < 4; ++i) te[i] = base.texp != nullptr ? base.texp[tw[i]] : 0;
 
   int buf = 0;
-  bool left = false;  // one of this lane's outputs is not finite
+  float left = 0.f;  // NaN when one of this lane's outputs is not finite (infinity and NaN times zero)
   for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS, buf ^= 1) {
     const int n0 = nb0 + wave * (16 * NB), nl = nb0 + NB * lane;
     int re[NB];
@@ -398,8 +398,9 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
       for (int j = 0; j < NB; ++j) {
         // (the many-token route's sums carry a power of two per token and row)
         const float f = __builtin_ldexpf(cur.v[i][j], te[i] - re[j]);
-        h[j] = f32_to_bf16_rne(f + term[buf][4 * wave + i][NB * lane + j]);
-        left |= (h[j] & 0x7F80u) == 0x7F80u;
+        const float v = f + term[buf][4 * wave + i][NB * lane + j];
+        left = __builtin_fmaf(v, 0.f, left);
+        h[j] = f32_to_bf16_rne(v);
       }
       uint16_t* o = y + (size_t)tw[i] * N + nl;
       if (vec && NB == 4) {
@@ -414,30 +415,29 @@ lora_finish_kernel(const uint16_t* __restrict__ b, const float* __restrict__ sca
     }
     cur = next;
   }
-  if (!left) return;
+  if (__builtin_amdgcn_ballot_w64(left != left) == 0) return;
 
-  // Rare: an output that is not finite is formed again: a base sum that is
-  // not finite exactly, as the base product's own kernels do, the term in
-  // binary32 as the rank values are (an infinity of B times their two parts is
-  // NaN where the second part is zero or of the other sign).
+  // Rare: an output that is not finite is formed again, by the lane that
+  // stored it: a base sum that is not finite exactly, as the base product's own
+  // kernels do, the term in binary32 as the rank values are (an infinity of B
+  // times their two parts is NaN where the second part is zero or of the other
+  // sign).
   for (int nb0 = blockIdx.x * ROWS; nb0 < N; nb0 += gridDim.x * ROWS) {
-    const Sums s = load_sums(nb0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+#pragma unroll 1
+    for (int o = 0; o < 4 * NB; ++o) {
+      const int i = o / NB, n = nb0 + NB * lane + o % NB;
+      const int t = __builtin_amdgcn_readlane(tl, 4 * wave + i);
       if (t0 + 4 * wave + i >= T) break;
-      const int t = tw[i];
+      if (n >= N || (y[(size_t)t * N + n] & 0x7F80u) != 0x7F80u) continue;
+      float v = base.part[(size_t)t * N + n];
+      for (int k = 1; k < base.ks; ++k) v += base.part[(size_t)k * base.stride + (size_t)t * N + n];
+      if (base.texp != nullptr) v = __builtin_ldexpf(v, base.texp[t] - base.rexp[n]);
+      if (!__builtin_isfinite(v)) v = (float)exact_base(w, n, t);
       const uint32_t own = (uint32_t)ids[t];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int n = nb0 + NB * lane + j;
-        if (n >= N || (y[(size_t)t * N + n] & 0x7F80u) != 0x7F80u) continue;
-        float v = __builtin_ldexpf(s.v[i][j], te[i] - (base.texp != nullptr ? base.rexp[n] : 0));
-        if (!__builtin_isfinite(v)) v = (float)exact_base(w, n, t);
-        if (own < (uint32_t)L)
-          v += adapter_term(b + ((size_t)own * N + n) * R, u + (size_t)t * R, (size_t)T * R, R, KS,
-                            scale != nullptr ? scale[own] : 1.0f);
-        y[(size_t)t * N + n] = f32_to_bf16_rne(v);
-      }
+      if (own < (uint32_t)L)
+        v += adapter_term(b + ((size_t)own * N + n) * R, u + (size_t)t * R, (size_t)T * R, R, KS,
+                          scale != nullptr ? scale[own] : 1.0f);
+      y[(size_t)t * N + n] = f32_to_bf16_rne(v);
     }
   }
 }

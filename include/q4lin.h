@@ -264,8 +264,8 @@ Q4LIN_API int q4lin_linear_lora(int fmt, const void *x, const void *w, const voi
 Q4LIN_API int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int64_t t, int64_t adapters,
                       int64_t rank);
 
-/* A mixture-of-experts layer for few tokens, its experts in q4lin_linear's
- * weight format.  With l[t][e] = sum_k router[e][k] x[t][k] and p the softmax
+/* A mixture-of-experts layer, its experts in q4lin_linear's weight format (any
+ * T within the limits below; made for few tokens).  With l[t][e] = sum_k router[e][k] x[t][k] and p the softmax
  * of a token's l over the experts, a token takes the top_k experts of the
  * largest l (equal ones: the lowest e first; a NaN counts as the lowest) with
  * weights p, divided by the sum of the chosen p where renormalize is not 0:
@@ -283,7 +283,9 @@ Q4LIN_API int64_t q4lin_lora_workspace_bytes(int fmt, int64_t n, int64_t k, int6
  *                4-byte aligned: written by q4lin_moe_route and q4lin_moe,
  *                read by q4lin_moe_experts
  *
- * q4lin_moe is the whole layer; q4lin_moe_route gives ids and weights alone;
+ * q4lin_moe is the whole layer; q4lin_moe_route gives ids and weights alone
+ * (without a workspace: one workgroup a token reads the whole router, slower
+ * than the layer's routing where experts * K is large);
  * q4lin_moe_experts takes them (routing rules of one's own; one process's
  * share of the experts): there an id outside 0..experts-1 contributes
  * nothing, a token without a valid id gets zeros, and an expert that a token

@@ -29,6 +29,8 @@
 //
 // u is binary32 from end to end; the matrix cores take s_a u as two bf16
 // parts (split_bf16), so the adapters' term is as exact as the base sum.
+// Outputs that come out non-finite are formed again from binary64 base sums
+// and a binary32 term.
 #include "q4lin_exact.h"
 #include "q4lin_kernels.h"
 #include "q4lin_mfma16.h"

@@ -28,7 +28,9 @@
 // instructions subtracted, the group's scale applied in binary32; the waves'
 // partials are summed in a fixed order, so that a call repeats to the bit.
 // h is kept as two bf16 parts (16 significant bits), as two activation rows
-// per pair: one bf16 would cost as much precision as the store of y.
+// per pair: one bf16 would cost as much precision as the store of y.  The sums
+// of 128 + q leave binary32 where |x| or |h| reaches 2^114: such a token's row
+// is not finite (it is not formed again).
 #include "q4lin_kernels.h"
 #include "q4lin_mfma16.h"
 

@@ -458,21 +458,33 @@ def _workspace(need, workspace, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _stream_of(stream, device, *made):
-    """The handle of ``stream`` (None: the current one).  Tensors ``made`` by
-    this call belong to the current stream; on another one they are kept from
-    reuse until its work is done."""
-    if stream is None:
-        # the handle alone: the Stream object costs the host 2 us, as much as an allocation
-        return _torch._C._cuda_getCurrentRawStream(device.index)
-    current = _torch.cuda.current_stream(device).cuda_stream
-    if stream == current:
-        return current
-    other = _torch.cuda.ExternalStream(stream, device=device)
-    for ten in made:
+def _current(place):
+    """The current stream's handle (the handle alone: the Stream object costs
+    the host 2 us, as much as an allocation)."""
+    return _torch._C._cuda_getCurrentRawStream(place)
+
+
+def _on_stream(stream, x, y, workspace, call):
+    """What ``call()`` gives with ``stream`` (a handle) as the current stream.
+    The tensors that the call makes are that stream's own: memory of the
+    current stream could still be in use by work of it that has not run.  What
+    it returns is kept from reuse until the current stream's work before its
+    release is done, and the caller's ``y`` and ``workspace`` until ``stream``'s
+    is."""
+    place = _place(x)
+    _on_gpu(place)
+    current = _torch.cuda.current_stream(place)
+    if stream == current.cuda_stream:
+        return call()
+    other = _torch.cuda.ExternalStream(stream, device=place)
+    with _torch.cuda.stream(other):
+        out = call()
+    for ten in out if isinstance(out, tuple) else (out,):
+        ten.record_stream(current)
+    for ten in (y, workspace):
         if ten is not None:
             ten.record_stream(other)
-    return stream
+    return out
 
 
 _FMT_PLANES = {  # bytes per row of K weights: codes, high plane, scales
@@ -508,6 +520,9 @@ def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, 
     of 8 up to 256), ``adapter_ids`` int32 ``[T]``, ``lora_scale`` float32
     ``[L]`` or None for ones.  Returns ``y`` ``[T, N]``.
     """
+    if stream is not None:
+        return _on_stream(stream, x, y, workspace, lambda: linear_lora(
+            x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale, fmt, codes_hi, y, workspace))
     t, k = x.shape
     n = codes.shape[0]
     adapters, rank = lora_a.shape[0], lora_a.shape[1]
@@ -530,9 +545,8 @@ def linear_lora(x, codes, scales, lora_a, lora_b, adapter_ids, lora_scale=None, 
     else:
         yp = _checked("y", y, (t, n), "bf16", place)
     work, work_bytes, workspace = _workspace(q4lin_lora_workspace_bytes(fmt, n, k, t, adapters, rank), workspace, device)
-    stream = _stream_of(stream, device, y, workspace)
     st = load().q4lin_linear_lora(fmt, xp, wp, hp, cp, ap, bp, sp, ip, yp, n, k, t, adapters, rank, work, work_bytes,
-                                  stream)
+                                  _current(place))
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return y
@@ -556,6 +570,8 @@ def moe_route(x, router, top_k, renormalize=True, stream=None):
     divided by their sum where ``renormalize``.  ``x`` bf16 ``[T, K]``,
     ``router`` bf16 ``[E, K]``.  Returns ``(ids int32 [T, top_k], weights
     float32 [T, top_k])``."""
+    if stream is not None:
+        return _on_stream(stream, x, None, None, lambda: moe_route(x, router, top_k, renormalize))
     t, k = x.shape
     experts = router.shape[0]
     device, place = x.device, _place(x)
@@ -564,9 +580,8 @@ def moe_route(x, router, top_k, renormalize=True, stream=None):
     _on_gpu(place)
     ids = _new((t, top_k), _torch.int32, device)
     weights = _new((t, top_k), _torch.float32, device)
-    stream = _stream_of(stream, device, ids, weights)
     st = load().q4lin_moe_route(xp, rp, ids.data_ptr(), weights.data_ptr(), k, experts, top_k, t,
-                                1 if renormalize else 0, stream)
+                                1 if renormalize else 0, _current(place))
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return ids, weights
@@ -591,6 +606,9 @@ def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, c
     down codes ``[E, K, I/2]``, scales ``[E, K, I/64]``.  ``top_k`` may exceed
     E (a share of the experts smaller than ``top_k``).  Returns ``y`` bf16
     ``[T, K]``."""
+    if stream is not None:
+        return _on_stream(stream, x, y, workspace, lambda: moe_experts(
+            x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down, y, workspace))
     t, k = x.shape
     top_k = ids.shape[1]
     device, place = x.device, _place(x)
@@ -601,18 +619,13 @@ def moe_experts(x, ids, weights, codes_gate, scales_gate, codes_up, scales_up, c
                                             place)
     _on_gpu(place)
     if top_k > experts:  # the library takes at most one place for each expert
-        if stream is None:
-            ids, weights = _by_expert(ids, weights, experts)
-        else:
-            with _torch.cuda.stream(_torch.cuda.ExternalStream(stream, device=device)):
-                ids, weights = _by_expert(ids, weights, experts)
+        ids, weights = _by_expert(ids, weights, experts)
         top_k, ip, vp = experts, ids.data_ptr(), weights.data_ptr()
     if y is None:
         y = _new((t, k), _torch.bfloat16, device)
     yp = _checked("y", y, (t, k), "bf16", place)
     wp, wb, workspace = _workspace(q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, device)
-    stream = _stream_of(stream, device, y, workspace)
-    st = load().q4lin_moe_experts(xp, ip, vp, *planes, yp, inner, k, experts, top_k, t, wp, wb, stream)
+    st = load().q4lin_moe_experts(xp, ip, vp, *planes, yp, inner, k, experts, top_k, t, wp, wb, _current(place))
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return y
@@ -623,6 +636,10 @@ def moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, sca
     """A whole mixture-of-experts layer on torch device tensors: ``moe_route``
     and ``moe_experts`` in one call (their arguments).  Returns ``(y, ids,
     weights)``."""
+    if stream is not None:
+        return _on_stream(stream, x, y, workspace, lambda: moe(
+            x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, scales_down, top_k, renormalize, y,
+            workspace))
     t, k = x.shape
     device, place = x.device, _place(x)
     xp = _checked("x", x, (t, k), "bf16", place)
@@ -636,9 +653,8 @@ def moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, sca
         y = _new((t, k), _torch.bfloat16, device)
     yp = _checked("y", y, (t, k), "bf16", place)
     wp, wb, workspace = _workspace(q4lin_moe_workspace_bytes(inner, k, experts, top_k, t), workspace, device)
-    stream = _stream_of(stream, device, y, workspace, ids, weights)
     st = load().q4lin_moe(xp, rp, *planes, yp, ids.data_ptr(), weights.data_ptr(), inner, k, experts, top_k, t,
-                       1 if renormalize else 0, wp, wb, stream)
+                          1 if renormalize else 0, wp, wb, _current(place))
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return y, ids, weights

@@ -321,6 +321,89 @@ Q4LIN_API int q4lin_moe_experts(const void *x, const void *ids, const void *weig
  * -Q4LIN_E_SHAPE.  Pure host function. */
 Q4LIN_API int64_t q4lin_moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t top_k, int64_t t);
 
+/* Activations in 8 bits, as MXFP8 (OCP Microscaling Formats): of every 32
+ * consecutive values y of a token, e is the least integer >= -127 with
+ * max |y| <= 448 * 2^e,
+ *
+ *   values   E4M3 [T][K]: y * 2^-e to nearest, ties to even (nothing
+ *            saturates), 16-byte aligned
+ *   scales   E8M0 [T][K/32]: the byte e + 127, 2-byte aligned for readers;
+ *            255 (NaN) for 32 values with an infinity or NaN among them
+ *
+ * q4lin_rmsnorm_mx8 writes the root-mean-square norm of a residual stream:
+ *
+ *     v = x (+ residual)    h = bf16(v)    y = v * weight / sqrt(mean(v^2) + eps)
+ *
+ * v is binary32 and enters the norm unrounded.  residual NULL: v = x, h is not
+ * written; weight NULL: ones.  q4lin_quantize_mx8 writes y = x, or y = silu(gate)
+ * * x (gate NULL: none; x and gate may be the halves of one product's rows).
+ *
+ *   x, residual, gate, h   bf16 [T][K], 16-byte aligned (x and gate of
+ *            q4lin_quantize_mx8: x_stride and gate_stride elements from token
+ *            to token, multiples of 8, not looked at for one token)
+ *   weight   bf16 [K], 16-byte aligned
+ *
+ * h may be x or residual itself; no other output may overlap an input or
+ * output.  Shapes and errors as for q4lin_linear; no workspace. */
+Q4LIN_API int q4lin_rmsnorm_mx8(const void *x, const void *residual, const void *weight, float eps, void *h,
+                      void *values, void *scales, int64_t k, int64_t t, void *stream);
+Q4LIN_API int q4lin_quantize_mx8(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride,
+                      void *values, void *scales, int64_t k, int64_t t, void *stream);
+
+/* Y = W x X (+ R) with the activations in 8 bits as above: W, Y and the shapes
+ * as for q4lin_linear, residual as for q4lin_linear_add (NULL: none; may be
+ * y).  Each scaled matrix instruction sums a group's 64 products with the
+ * offset of its codes, in binary32 (terms below 2^-17 of the group's largest
+ * are cut there); the groups' sums are scaled and added in binary32 and y is
+ * rounded once.  Activations below 2^100 in magnitude; past it, or with a NaN
+ * in x, outputs of that token alone may be infinite or NaN.  (For products
+ * exact to binary32, decode the values, which bf16 holds exactly, and call
+ * q4lin_linear.)  workspace: q4lin_linear_mx8_workspace_bytes() bytes, 256-byte
+ * aligned (NULL where 0).  y must not overlap any input or the workspace but
+ * the residual.  Errors as for q4lin_linear. */
+Q4LIN_API int q4lin_linear_mx8(const void *values, const void *x_scales, const void *codes, const void *scales,
+                      const void *residual, void *y, int64_t n, int64_t k, int64_t t,
+                      void *workspace, size_t workspace_bytes, void *stream);
+Q4LIN_API int64_t q4lin_linear_mx8_workspace_bytes(int64_t n, int64_t k, int64_t t);
+
+/* Log probabilities of rows of logits l[t][0..N):
+ *
+ *     logprob[t] = l[t][tokens[t]] - lse[t],  lse = log sum_n e^l[t][n]
+ *     entropy[t] = -sum_n p log p,  p = e^(l - lse)
+ *     top_logprobs[t][j], top_ids[t][j]   the `top` largest l - lse and their
+ *                  n, largest first (equal ones: the lowest n first)
+ *
+ *   logits       bf16 (f32 = 0) or float (f32 = 1), rows `stride` elements
+ *                apart (not looked at for one row), aligned to an element
+ *   tokens       int32 [T]; a number outside 0..N-1 (padding) gives 0
+ *   logprob, entropy  float [T]; top_logprobs float, top_ids int32 [T][top];
+ *                4-byte aligned
+ *
+ * tokens and logprob may be NULL together, entropy by itself, the last two
+ * where top is 0.  A logit of -infinity (a masked token) counts for nothing; a
+ * row of nothing else has entropy 0 and every log probability -infinity.  A
+ * NaN or +infinity makes the row's numbers NaN (a NaN is the last of the
+ * alternatives).  Sums are binary32 or wider.  1 <= N <= 2^24, top <= 32 and
+ * <= N.  workspace: q4lin_logprobs_workspace_bytes() bytes, 256-byte aligned.
+ * Errors as for q4lin_linear. */
+Q4LIN_API int q4lin_logprobs(const void *logits, int f32, int64_t stride, const void *tokens, void *logprob,
+                      void *entropy, void *top_logprobs, void *top_ids, int64_t n, int64_t t, int64_t top,
+                      void *workspace, size_t workspace_bytes, void *stream);
+Q4LIN_API int64_t q4lin_logprobs_workspace_bytes(int64_t n, int64_t t, int64_t top);
+
+/* LinearLogprobs: q4lin_logprobs of the logits W x X (a vocabulary's
+ * projection), which are binary32, not rounded, and only held for a run of
+ * tokens, in the workspace.  W as for q4lin_linear; x bf16 [T][K], or (x_scales
+ * not NULL) E4M3 values with their scales as above; exact codes in every
+ * product, sums in binary32; K up to 2^17.  workspace: q4lin_linear_logprobs_workspace_bytes()
+ * bytes (mx8: whether x_scales is given), 256-byte aligned.  Errors as for
+ * q4lin_linear. */
+Q4LIN_API int q4lin_linear_logprobs(const void *x, const void *x_scales, const void *codes, const void *scales,
+                      const void *tokens, void *logprob, void *entropy, void *top_logprobs, void *top_ids,
+                      int64_t n, int64_t k, int64_t t, int64_t top, void *workspace, size_t workspace_bytes,
+                      void *stream);
+Q4LIN_API int64_t q4lin_linear_logprobs_workspace_bytes(int64_t n, int64_t k, int64_t t, int64_t top, int mx8);
+
 /* Static, human-readable text for a status code (never NULL). */
 Q4LIN_API const char *q4lin_status_string(int status);
 

@@ -48,7 +48,9 @@ EXPORTED = ("q4lin_workspace_bytes", "q4lin_linear", "q4lin_linear_add", "q4lin_
             "q4lin_status_string", "q4lin_route", "q4lin_version", "q4lin_linear_noalloc",
             "q4lin_noalloc_scratch_bytes", "q4lin_linear_fmt", "q4lin_fmt_weight_bytes",
             "q4lin_fmt_workspace_bytes", "q4lin_linear_lora", "q4lin_lora_workspace_bytes", "q4lin_moe",
-            "q4lin_moe_route", "q4lin_moe_experts", "q4lin_moe_workspace_bytes")
+            "q4lin_moe_route", "q4lin_moe_experts", "q4lin_moe_workspace_bytes", "q4lin_rmsnorm_mx8",
+            "q4lin_quantize_mx8", "q4lin_linear_mx8", "q4lin_linear_mx8_workspace_bytes", "q4lin_logprobs",
+            "q4lin_logprobs_workspace_bytes", "q4lin_linear_logprobs", "q4lin_linear_logprobs_workspace_bytes")
 
 
 class Q4LinError(RuntimeError):
@@ -116,6 +118,22 @@ def _load() -> ctypes.CDLL:
     lib.q4lin_moe_experts.restype = ci
     lib.q4lin_moe_workspace_bytes.argtypes = [i64] * 5
     lib.q4lin_moe_workspace_bytes.restype = i64
+    lib.q4lin_rmsnorm_mx8.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 3 + [i64] * 2 + [vp]
+    lib.q4lin_rmsnorm_mx8.restype = ci
+    lib.q4lin_quantize_mx8.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, vp]
+    lib.q4lin_quantize_mx8.restype = ci
+    lib.q4lin_linear_mx8.argtypes = [vp] * 6 + [i64] * 3 + [vp, cz, vp]
+    lib.q4lin_linear_mx8.restype = ci
+    lib.q4lin_linear_mx8_workspace_bytes.argtypes = [i64] * 3
+    lib.q4lin_linear_mx8_workspace_bytes.restype = i64
+    lib.q4lin_logprobs.argtypes = [vp, ci, i64] + [vp] * 5 + [i64] * 3 + [vp, cz, vp]
+    lib.q4lin_logprobs.restype = ci
+    lib.q4lin_logprobs_workspace_bytes.argtypes = [i64] * 3
+    lib.q4lin_logprobs_workspace_bytes.restype = i64
+    lib.q4lin_linear_logprobs.argtypes = [vp] * 9 + [i64] * 4 + [vp, cz, vp]
+    lib.q4lin_linear_logprobs.restype = ci
+    lib.q4lin_linear_logprobs_workspace_bytes.argtypes = [i64] * 4 + [ci]
+    lib.q4lin_linear_logprobs_workspace_bytes.restype = i64
     return lib
 
 
@@ -241,6 +259,55 @@ def q4lin_moe_experts(x: int, ids: int, weights: int, codes_gate: int, scales_ga
 @functools.lru_cache(maxsize=4096)
 def q4lin_moe_workspace_bytes(inner: int, k: int, experts: int, top_k: int, t: int) -> int:
     return int(load().q4lin_moe_workspace_bytes(inner, k, experts, top_k, t))
+
+
+def q4lin_rmsnorm_mx8(x: int, residual: int, weight: int, eps: float, h: int, values: int, scales: int, k: int, t: int,
+                      stream: int) -> int:
+    """Raw call of the root-mean-square norm into MXFP8; returns the status."""
+    return int(load().q4lin_rmsnorm_mx8(x, residual, weight, eps, h, values, scales, k, t, stream))
+
+
+def q4lin_quantize_mx8(x: int, x_stride: int, gate: int, gate_stride: int, values: int, scales: int, k: int, t: int,
+                       stream: int) -> int:
+    """Raw call of the (gated) quantization into MXFP8; returns the status."""
+    return int(load().q4lin_quantize_mx8(x, x_stride, gate, gate_stride, values, scales, k, t, stream))
+
+
+def q4lin_linear_mx8(values: int, x_scales: int, codes: int, scales: int, residual: int, y: int, n: int, k: int,
+                     t: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    """Raw call of the product of MXFP8 activations; returns the status."""
+    return int(load().q4lin_linear_mx8(values, x_scales, codes, scales, residual, y, n, k, t, workspace,
+                                       workspace_bytes, stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def q4lin_linear_mx8_workspace_bytes(n: int, k: int, t: int) -> int:
+    return int(load().q4lin_linear_mx8_workspace_bytes(n, k, t))
+
+
+def q4lin_logprobs(logits: int, f32: int, stride: int, tokens: int, logprob: int, entropy: int, top_logprobs: int,
+                   top_ids: int, n: int, t: int, top: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    """Raw call of the log probabilities of logits; returns the status."""
+    return int(load().q4lin_logprobs(logits, f32, stride, tokens, logprob, entropy, top_logprobs, top_ids, n, t, top,
+                                     workspace, workspace_bytes, stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def q4lin_logprobs_workspace_bytes(n: int, t: int, top: int) -> int:
+    return int(load().q4lin_logprobs_workspace_bytes(n, t, top))
+
+
+def q4lin_linear_logprobs(x: int, x_scales: int, codes: int, scales: int, tokens: int, logprob: int, entropy: int,
+                          top_logprobs: int, top_ids: int, n: int, k: int, t: int, top: int, workspace: int,
+                          workspace_bytes: int, stream: int) -> int:
+    """Raw call of the log probabilities of a product; returns the status."""
+    return int(load().q4lin_linear_logprobs(x, x_scales, codes, scales, tokens, logprob, entropy, top_logprobs,
+                                            top_ids, n, k, t, top, workspace, workspace_bytes, stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def q4lin_linear_logprobs_workspace_bytes(n: int, k: int, t: int, top: int, mx8: int) -> int:
+    return int(load().q4lin_linear_logprobs_workspace_bytes(n, k, t, top, mx8))
 
 
 def q4lin_status_string(status: int) -> str:
@@ -421,7 +488,8 @@ def _place(x):
 
         _torch, bits = torch, (torch.int16, torch.uint16)
         _DTYPES.update(bf16=(torch.bfloat16, *bits), fp16=(torch.float16, *bits), codes=(torch.uint8, torch.int8),
-                       int32=(torch.int32,), float32=(torch.float32,))
+                       int32=(torch.int32,), float32=(torch.float32,), e4m3=(torch.float8_e4m3fn, torch.uint8),
+                       e8m0=(torch.float8_e8m0fnu, torch.uint8))
     return x.get_device()
 
 
@@ -480,7 +548,8 @@ def _on_stream(stream, x, y, workspace, call):
     with _torch.cuda.stream(other):
         out = call()
     for ten in out if isinstance(out, tuple) else (out,):
-        ten.record_stream(current)
+        if ten is not None:
+            ten.record_stream(current)
     for ten in (y, workspace):
         if ten is not None:
             ten.record_stream(other)
@@ -658,3 +727,154 @@ def moe(x, router, codes_gate, scales_gate, codes_up, scales_up, codes_down, sca
     if st != Q4LIN_OK:
         raise Q4LinError(st)
     return y, ids, weights
+
+
+def rmsnorm_mx8(x, weight=None, eps=1e-6, residual=None, h=None, stream=None):
+    """The root-mean-square norm of ``x`` (plus ``residual``) in 8 bits, on
+    torch device tensors: ``v = x + residual``, ``y = v / sqrt(mean(v^2) + eps) *
+    weight``, in blocks of 32 that share a power of two (MXFP8, as laid out in
+    ``include/q4lin.h``).  ``x``, ``residual`` bf16 ``[T, K]``, ``weight`` bf16
+    ``[K]`` or None for ones.  Returns ``(values float8_e4m3fn [T, K], scales
+    float8_e8m0fnu [T, K/32])``, and with ``residual`` also ``h``, bf16 of ``v``
+    (``h`` may be given, also as ``x`` or ``residual`` itself)."""
+    if stream is not None:
+        return _on_stream(stream, x, h, None, lambda: rmsnorm_mx8(x, weight, eps, residual, h))
+    t, k = x.shape
+    device, place = x.device, _place(x)
+    xp = _checked("x", x, (t, k), "bf16", place)
+    wp = _checked("weight", weight, (k,), "bf16", place) if weight is not None else None
+    rp = hp = None
+    if residual is not None:
+        rp = _checked("residual", residual, (t, k), "bf16", place)
+        _on_gpu(place)
+        if h is None:
+            h = _new((t, k), _torch.bfloat16, device)
+        hp = _checked("h", h, (t, k), "bf16", place)
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    _on_gpu(place)
+    values = _new((t, k), _torch.float8_e4m3fn, device)
+    scales = _new((t, k // 32), _torch.float8_e8m0fnu, device)
+    st = load().q4lin_rmsnorm_mx8(xp, rp, wp, eps, hp, values.data_ptr(), scales.data_ptr(), k, t, _current(place))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return (values, scales) if residual is None else (values, scales, h)
+
+
+def _rows(name, ten, shape, dtypes, place):
+    """(address, elements between rows) of a matrix whose rows are contiguous."""
+    if ten.shape != shape or ten.dtype not in dtypes or (shape[1] > 1 and ten.stride(1) != 1):
+        raise ValueError("%s must be a tensor of shape %s with contiguous rows of %s, got %s of %s" % (
+            name, tuple(shape), dtypes[0], tuple(ten.shape), ten.dtype))
+    if ten.get_device() != place:
+        raise ValueError("%s must be on x's GPU, not on %s" % (name, ten.device))
+    return ten.data_ptr(), ten.stride(0)
+
+
+def quantize_mx8(x, gate=None, stream=None):
+    """``x``, or ``silu(gate) * x``, in 8 bits (``rmsnorm_mx8``'s form) on torch
+    device tensors: bf16 ``[T, K]``, rows contiguous and any multiple of eight
+    elements apart (the halves of one product's rows).  Returns ``(values,
+    scales)``."""
+    if stream is not None:
+        return _on_stream(stream, x, None, None, lambda: quantize_mx8(x, gate))
+    t, k = x.shape
+    device, place = x.device, _place(x)
+    xp, xs = _rows("x", x, (t, k), _DTYPES["bf16"], place)
+    gp, gs = _rows("gate", gate, (t, k), _DTYPES["bf16"], place) if gate is not None else (None, 0)
+    _on_gpu(place)
+    values = _new((t, k), _torch.float8_e4m3fn, device)
+    scales = _new((t, k // 32), _torch.float8_e8m0fnu, device)
+    st = load().q4lin_quantize_mx8(xp, xs, gp, gs, values.data_ptr(), scales.data_ptr(), k, t, _current(place))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return values, scales
+
+
+def linear_mx8(values, x_scales, codes, scales, residual=None, y=None, workspace=None, stream=None):
+    """Y = W x X (+ R) with activations in 8 bits, on torch device tensors:
+    ``values`` float8_e4m3fn ``[T, K]`` and ``x_scales`` float8_e8m0fnu ``[T,
+    K/32]`` as ``rmsnorm_mx8`` and ``quantize_mx8`` give them (or their bytes);
+    ``codes`` uint8 ``[N, K/2]``, ``scales`` fp16 ``[N, K/64]``; ``residual`` bf16
+    ``[T, N]`` (may be ``y``).  Returns ``y`` bf16 ``[T, N]``."""
+    if stream is not None:
+        return _on_stream(stream, values, y, workspace, lambda: linear_mx8(
+            values, x_scales, codes, scales, residual, y, workspace))
+    t, k = values.shape
+    n = codes.shape[0]
+    device, place = values.device, _place(values)
+    vp = _checked("values", values, (t, k), "e4m3", place)
+    ep = _checked("x_scales", x_scales, (t, k // 32), "e8m0", place)
+    cp = _checked("codes", codes, (n, k // 2), "codes", place)
+    sp = _checked("scales", scales, (n, k // 64), "fp16", place)
+    rp = _checked("residual", residual, (t, n), "bf16", place) if residual is not None else None
+    _on_gpu(place)
+    if y is None:
+        y = _new((t, n), _torch.bfloat16, device)
+    yp = _checked("y", y, (t, n), "bf16", place)
+    wp, wb, workspace = _workspace(q4lin_linear_mx8_workspace_bytes(n, k, t), workspace, device)
+    st = load().q4lin_linear_mx8(vp, ep, cp, sp, rp, yp, n, k, t, wp, wb, _current(place))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return y
+
+
+def _logprob_outputs(tokens, t, top, place, device):
+    """(tokens' address, the four outputs, their addresses) of a log probability call."""
+    tp = _checked("tokens", tokens, (t,), "int32", place) if tokens is not None else None
+    _on_gpu(place)
+    if top < 0:
+        raise Q4LinError(Q4LIN_E_SHAPE)
+    logprob = _torch.empty_strided((t,), (1,), dtype=_torch.float32, device=device) if tokens is not None else None
+    entropy = _torch.empty_strided((t,), (1,), dtype=_torch.float32, device=device)
+    best = _new((t, top), _torch.float32, device)
+    ids = _new((t, top), _torch.int32, device)
+    return tp, (logprob, entropy, best, ids), (logprob.data_ptr() if tokens is not None else None, entropy.data_ptr(),
+                                               best.data_ptr(), ids.data_ptr())
+
+
+def logprobs(logits, tokens=None, top=0, workspace=None, stream=None):
+    """Log probabilities of rows of logits on torch device tensors: ``logits``
+    bf16 or float32 ``[T, N]`` (rows contiguous, any distance apart),
+    ``tokens`` int32 ``[T]`` (a number outside the row gives 0) or None.
+    Returns ``(logprob, entropy, top_logprobs, top_ids)``: float32 ``[T]`` (None
+    without ``tokens``), float32 ``[T]``, float32 and int32 ``[T, top]``, largest
+    first and equal ones by the lowest number (``top`` up to 32)."""
+    if stream is not None:
+        return _on_stream(stream, logits, None, workspace, lambda: logprobs(logits, tokens, top, workspace))
+    t, n = logits.shape
+    device, place = logits.device, _place(logits)
+    f32 = logits.dtype == _torch.float32
+    lp, stride = _rows("logits", logits, (t, n), _DTYPES["float32" if f32 else "bf16"], place)
+    tp, outs, at = _logprob_outputs(tokens, t, top, place, device)
+    wp, wb, workspace = _workspace(q4lin_logprobs_workspace_bytes(n, t, top), workspace, device)
+    st = load().q4lin_logprobs(lp, 1 if f32 else 0, stride, tp, *at, n, t, top, wp, wb, _current(place))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return outs
+
+
+def linear_logprobs(x, x_scales, codes, scales, tokens=None, top=0, workspace=None, stream=None):
+    """``logprobs`` of the logits ``W x X`` (the vocabulary's projection), which
+    are neither rounded nor kept, on torch device tensors: ``x`` float8_e4m3fn
+    ``[T, K]`` with ``x_scales`` (as for ``linear_mx8``), or bf16 ``[T, K]`` with
+    ``x_scales`` None; ``codes`` uint8 ``[N, K/2]``, ``scales`` fp16 ``[N, K/64]``.
+    Returns what ``logprobs`` does."""
+    if stream is not None:
+        return _on_stream(stream, x, None, workspace, lambda: linear_logprobs(
+            x, x_scales, codes, scales, tokens, top, workspace))
+    t, k = x.shape
+    n = codes.shape[0]
+    device, place = x.device, _place(x)
+    mx8 = x_scales is not None
+    xp = _checked("x", x, (t, k), "e4m3" if mx8 else "bf16", place)
+    ep = _checked("x_scales", x_scales, (t, k // 32), "e8m0", place) if mx8 else None
+    cp = _checked("codes", codes, (n, k // 2), "codes", place)
+    sp = _checked("scales", scales, (n, k // 64), "fp16", place)
+    tp, outs, at = _logprob_outputs(tokens, t, top, place, device)
+    wp, wb, workspace = _workspace(q4lin_linear_logprobs_workspace_bytes(n, k, t, top, 1 if mx8 else 0), workspace,
+                                   device)
+    st = load().q4lin_linear_logprobs(xp, ep, cp, sp, tp, *at, n, k, t, top, wp, wb, _current(place))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st)
+    return outs

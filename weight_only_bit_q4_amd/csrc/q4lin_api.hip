@@ -313,6 +313,57 @@ int check_experts(const void* x, const void* ids, const void* weights, const voi
   return aligned(workspace, 256) ? Q4LIN_OK : Q4LIN_E_ALIGN;
 }
 
+// Log probabilities' limits: 32-bit positions in a row, 2^40 bytes in all.
+constexpr int64_t kMaxTop = 32;
+bool logprobs_shape_ok(int64_t n, int64_t t, int64_t top) {
+  return n >= 1 && n <= kMaxN && t >= 0 && t <= kMaxT && top >= 0 && top <= kMaxTop && top <= n &&
+         t * n * 4 < kMaxBytes;
+}
+// The outputs that are asked for, and what they go by.
+int check_logprobs(const void* tokens, const void* logprob, const void* entropy, const void* top_logprobs,
+                   const void* top_ids, int64_t top) {
+  if ((tokens == nullptr) != (logprob == nullptr) || (top > 0 && (!top_logprobs || !top_ids))) return Q4LIN_E_NULL;
+  if (!aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(top_logprobs, 4) ||
+      !aligned(top_ids, 4))
+    return Q4LIN_E_ALIGN;
+  return Q4LIN_OK;
+}
+int check_workspace(const void* workspace, size_t workspace_bytes, size_t need) {
+  if (need == 0) return Q4LIN_OK;
+  if (workspace_bytes < need) return Q4LIN_E_WORKSPACE;
+  if (!workspace) return Q4LIN_E_NULL;
+  return aligned(workspace, 256) ? Q4LIN_OK : Q4LIN_E_ALIGN;
+}
+
+// LinearLogprobs: runs of `run` tokens whose logits lie in the workspace as
+// binary32, after the bf16 form of all activations where they come in 8 bits.
+// The products are those of a route with exact codes (the many-token route
+// rounds the weights to 11 bits, which would show in a log probability), the
+// most tokens per weight read that such a route takes.
+struct ScorePlan {
+  int64_t run;
+  size_t x_bytes, logit_bytes, total;
+};
+constexpr int64_t kMaxScoreK = int64_t(1) << 17;  // (up to there every run of tokens has such a route)
+int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, bool mx8, ScorePlan* p) {
+  if (!shape_ok(n, k, t) || !logprobs_shape_ok(n, t, top) || k > kMaxScoreK) return Q4LIN_E_SHAPE;
+  *p = ScorePlan{0, 0, 0, 0};
+  if (t == 0) return Q4LIN_OK;
+  for (int64_t most : {kMidLastT, int64_t(32), int64_t(4), int64_t(1)}) {
+    const int64_t runs = (t + most - 1) / most, run = (t + runs - 1) / runs;
+    // (the last run may be shorter: its route is checked too)
+    const int64_t last = t - (t - 1) / run * run;
+    if (pick_route(n, k, run) == Q4LIN_ROUTE_TILED || pick_route(n, k, last) == Q4LIN_ROUTE_TILED) continue;
+    p->run = run;
+    break;
+  }
+  if (p->run == 0) return Q4LIN_E_SHAPE;
+  p->x_bytes = mx8 ? al256((size_t)(t * k * 2)) : 0;
+  p->logit_bytes = al256((size_t)(p->run * n * 4));
+  p->total = p->x_bytes + p->logit_bytes + q4lin::logprobs_workspace_bytes(n, p->run, (int)top);
+  return Q4LIN_OK;
+}
+
 // ---------------------------------------------------------------------------
 // The no-allocation variant's scratch: a static device array (each GPU the
 // library runs on holds its own copy until the process ends).  Host code
@@ -711,6 +762,130 @@ int q4lin_moe(const void* x, const void* router, const void* codes_gate, const v
                          scales_down, y, inner, k, experts, top_k, t, renormalize ? 1 : 0};
   const hipError_t e = q4lin::launch_moe(a, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int q4lin_rmsnorm_mx8(const void* x, const void* residual, const void* weight, float eps, void* h, void* values,
+                      void* scales, int64_t k, int64_t t, void* stream) {
+  if (!shape_ok(0, k, t)) return Q4LIN_E_SHAPE;
+  if (t == 0) return Q4LIN_OK;
+  if (!x || !values || !scales || (residual && !h)) return Q4LIN_E_NULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(values, 16))
+    return Q4LIN_E_ALIGN;
+  const hipError_t e = q4lin::launch_rmsnorm_mx8(x, residual, weight, h, values, scales, k, t, eps,
+                                                 static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int q4lin_quantize_mx8(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, void* values,
+                       void* scales, int64_t k, int64_t t, void* stream) {
+  if (!shape_ok(0, k, t)) return Q4LIN_E_SHAPE;
+  if (t == 0) return Q4LIN_OK;
+  // rows are whole 16-byte pieces; a stride may be anything for a single row
+  if (t > 1 && (x_stride < 0 || x_stride % 8 != 0 || x_stride * t * 2 >= kMaxBytes)) return Q4LIN_E_SHAPE;
+  if (t > 1 && gate && (gate_stride < 0 || gate_stride % 8 != 0 || gate_stride * t * 2 >= kMaxBytes))
+    return Q4LIN_E_SHAPE;
+  if (!x || !values || !scales) return Q4LIN_E_NULL;
+  if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(values, 16)) return Q4LIN_E_ALIGN;
+  const hipError_t e = q4lin::launch_quantize_mx8(x, gate, values, scales, k, t, t > 1 ? x_stride : 0,
+                                                  t > 1 ? gate_stride : 0, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int64_t q4lin_linear_mx8_workspace_bytes(int64_t n, int64_t k, int64_t t) {
+  if (!shape_ok(n, k, t)) return -Q4LIN_E_SHAPE;
+  return n == 0 || t == 0 ? 0 : (int64_t)q4lin::mx8_workspace_bytes(n, k, t);
+}
+
+int q4lin_linear_mx8(const void* values, const void* x_scales, const void* codes, const void* scales,
+                     const void* residual, void* y, int64_t n, int64_t k, int64_t t, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!shape_ok(n, k, t)) return Q4LIN_E_SHAPE;
+  if (n == 0 || t == 0) return Q4LIN_OK;
+  if (!values || !x_scales || !codes || !scales || !y) return Q4LIN_E_NULL;
+  if (!aligned(values, 16) || !aligned(x_scales, 2) || !aligned(codes, 16) || !aligned(scales, 2) ||
+      !aligned(residual, 2) || !aligned(y, 2))
+    return Q4LIN_E_ALIGN;
+  const int st = check_workspace(workspace, workspace_bytes, q4lin::mx8_workspace_bytes(n, k, t));
+  if (st != Q4LIN_OK) return st;
+  const hipError_t e = q4lin::launch_mx8(q4lin::Mx8Args{values, x_scales, codes, scales, residual, y, n, k, t},
+                                         workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int64_t q4lin_logprobs_workspace_bytes(int64_t n, int64_t t, int64_t top) {
+  if (!logprobs_shape_ok(n, t, top)) return -Q4LIN_E_SHAPE;
+  return t == 0 ? 0 : (int64_t)q4lin::logprobs_workspace_bytes(n, t, (int)top);
+}
+
+int q4lin_logprobs(const void* logits, int f32, int64_t stride, const void* tokens, void* logprob, void* entropy,
+                   void* top_logprobs, void* top_ids, int64_t n, int64_t t, int64_t top, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (!logprobs_shape_ok(n, t, top)) return Q4LIN_E_SHAPE;
+  if (t == 0) return Q4LIN_OK;
+  if (t > 1 && (stride < 0 || stride * t * 4 >= kMaxBytes)) return Q4LIN_E_SHAPE;
+  if (!logits) return Q4LIN_E_NULL;
+  if (!aligned(logits, f32 ? 4 : 2)) return Q4LIN_E_ALIGN;
+  int st = check_logprobs(tokens, logprob, entropy, top_logprobs, top_ids, top);
+  if (st == Q4LIN_OK)
+    st = check_workspace(workspace, workspace_bytes, q4lin::logprobs_workspace_bytes(n, t, (int)top));
+  if (st != Q4LIN_OK) return st;
+  const hipError_t e = q4lin::launch_logprobs(
+      q4lin::LogprobsArgs{logits, f32 != 0, t > 1 ? stride : 0, tokens, logprob, entropy, top_logprobs, top_ids, n, t,
+                          (int)top},
+      workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
+}
+
+int64_t q4lin_linear_logprobs_workspace_bytes(int64_t n, int64_t k, int64_t t, int64_t top, int mx8) {
+  ScorePlan p;
+  const int st = score_plan(n, k, t, top, mx8 != 0, &p);
+  return st == Q4LIN_OK ? (int64_t)p.total : -(int64_t)st;
+}
+
+int q4lin_linear_logprobs(const void* x, const void* x_scales, const void* codes, const void* scales,
+                          const void* tokens, void* logprob, void* entropy, void* top_logprobs, void* top_ids,
+                          int64_t n, int64_t k, int64_t t, int64_t top, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  ScorePlan p;
+  int st = score_plan(n, k, t, top, x_scales != nullptr, &p);
+  if (st != Q4LIN_OK || t == 0) return st;
+  if (!x || !codes || !scales) return Q4LIN_E_NULL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2)) return Q4LIN_E_ALIGN;
+  st = check_logprobs(tokens, logprob, entropy, top_logprobs, top_ids, top);
+  if (st == Q4LIN_OK) st = check_workspace(workspace, workspace_bytes, p.total);
+  if (st != Q4LIN_OK) return st;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  float* const logits = reinterpret_cast<float*>(ws + p.x_bytes);
+  hipError_t e = hipSuccess;
+  const uint8_t* xb = static_cast<const uint8_t*>(x);
+  if (x_scales) {
+    e = q4lin::launch_mx8_to_bf16(x, x_scales, ws, k, t, s);
+    if (e != hipSuccess) return Q4LIN_E_LAUNCH;
+    xb = ws;
+  }
+  for (int64_t t0 = 0; t0 < t; t0 += p.run) {
+    const int64_t c = t - t0 < p.run ? t - t0 : p.run;
+    const int route = pick_route(n, k, c);
+    q4lin::GemvArgs a{xb + (size_t)(t0 * k * 2), codes, scales, logits, n, k, c};
+    a.f32 = true;
+    if (route == Q4LIN_ROUTE_DECODE || route == Q4LIN_ROUTE_GEMV ||
+        (route == Q4LIN_ROUTE_SKINNY && !small_uses_fmt(n, k, c)))
+      e = launch_sums(route, a, s);
+    else
+      e = q4lin::launch_fmt(q4_fmt_args(a), s);
+    if (e != hipSuccess) return Q4LIN_E_LAUNCH;
+    auto from = [&](void* base, int64_t each) -> void* {
+      return base ? static_cast<uint8_t*>(base) + (size_t)(4 * each * t0) : nullptr;
+    };
+    e = q4lin::launch_logprobs(
+        q4lin::LogprobsArgs{logits, true, n, from(const_cast<void*>(tokens), 1), from(logprob, 1), from(entropy, 1),
+                            from(top_logprobs, top), from(top_ids, top), n, c, (int)top},
+        ws + p.x_bytes + p.logit_bytes, s);
+    if (e != hipSuccess) return Q4LIN_E_LAUNCH;
+  }
+  return Q4LIN_OK;
 }
 
 const char* q4lin_status_string(int status) {

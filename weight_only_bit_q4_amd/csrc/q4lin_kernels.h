@@ -267,4 +267,43 @@ size_t moe_workspace_bytes(int64_t inner, int64_t k, int64_t experts, int64_t to
 hipError_t launch_moe_experts(const MoeArgs& a, void* workspace, hipStream_t stream);
 hipError_t launch_moe(const MoeArgs& a, void* workspace, hipStream_t stream);
 
+// Activations in 8 bits (q4lin_quant.hip): E4M3 values [t][k] and E8M0 scales
+// [t][k/32] of the norm of x (+ residual; then h = bf16 of the sum), of x or
+// of silu(gate) x (row strides in elements), and back to bf16.
+hipError_t launch_rmsnorm_mx8(const void* x, const void* residual, const void* weight, void* h, void* values,
+                              void* scales, int64_t k, int64_t t, float eps, hipStream_t stream);
+hipError_t launch_quantize_mx8(const void* x, const void* gate, void* values, void* scales, int64_t k, int64_t t,
+                               int64_t x_stride, int64_t gate_stride, hipStream_t stream);
+hipError_t launch_mx8_to_bf16(const void* values, const void* scales, void* out, int64_t k, int64_t t,
+                              hipStream_t stream);
+
+// The Q4 product of such activations (q4lin_mx8.hip).
+struct Mx8Args {
+  const void* x;
+  const void* xs;
+  const void* codes;
+  const void* scales;
+  const void* res;  // bf16 [t][n] or nullptr
+  void* y;
+  int64_t n, k, t;
+};
+size_t mx8_workspace_bytes(int64_t n, int64_t k, int64_t t);
+hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream);
+
+// Log probabilities of rows of logits, bf16 or binary32 (q4lin_logprobs.hip).
+struct LogprobsArgs {
+  const void* logits;
+  bool f32;
+  int64_t stride;      // elements between rows
+  const void* tokens;  // nullptr: no logprob
+  void* logprob;
+  void* entropy;  // nullptr: none
+  void* top_logprobs;
+  void* top_ids;
+  int64_t n, t;
+  int top;
+};
+size_t logprobs_workspace_bytes(int64_t n, int64_t t, int top);
+hipError_t launch_logprobs(const LogprobsArgs& a, void* workspace, hipStream_t stream);
+
 }  // namespace q4lin

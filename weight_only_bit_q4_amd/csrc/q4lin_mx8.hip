@@ -1,0 +1,533 @@
+// q4lin_mx8.hip -- Y = Q4 weight x MXFP8 activations on the scaled matrix
+// cores (the operands: q4lin_mx8.h).
+//
+//   y[t][n] = bf16( sum_g s[n][g] P[t][n][g] (+ residual) ),
+//   P = sum over the group of (q - 8) x 2^e, on the matrix cores
+//
+// A matrix instruction's K is one 64-group: per group and 32 x 32 outputs
+// one v_mfma_scale_f32_32x32x64_f8f6f4 (64 clocks) and sixteen multiply-adds
+// with the group's scale (64 clocks of the vector ALU), against four bf16
+// instructions of 32 clocks for bf16 activations.  The products' own sums are
+// binary32 with the instruction's alignment (terms below about 2^-17 of a
+// group's largest are cut: measured 1e-5 of an output's standard deviation
+// per group), the sums over groups binary32 (and binary64 across waves).
+//
+// Tokens are the rows of D and weight rows its columns, so that a lane holds
+// one weight row and its scale is one register.
+#include "q4lin_kernels.h"
+#include "q4lin_mfma16.h"
+#include "q4lin_mx8.h"
+
+namespace q4lin {
+namespace {
+
+using mfma16::dma16;
+using mfma16::kNowhere;
+using mfma16::make_rsrc;
+using mfma16::rsrc_t;
+using mfma16::wait_lgkm0;
+using mfma16::wait_vm;
+using mx8::v8i_t;
+
+struct Mx8Kernel {
+  const uint8_t* x;    // E4M3 [T][K]
+  const uint8_t* xs;   // E8M0 [T][K/32]
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint16_t* res;  // nullptr: none
+  uint16_t* y;
+  float* part;  // K split: binary32 sums [share][T][N]
+  int N, K, T;
+};
+
+// Two bytes per group (a weight row's fp16 scales, a token's two block
+// scales) of G8 groups from group g on, groups at or past `end` as zeros.
+// The rows need not be aligned.
+template <int GROUPS>
+struct Strip {
+  uint32_t w[(GROUPS + 1) / 2];
+};
+template <int GROUPS>
+__device__ __forceinline__ Strip<GROUPS> load_strip(const uint8_t* row, int g, int end) {
+  Strip<GROUPS> s;
+  if (g + GROUPS <= end) {
+    __builtin_memcpy(&s, row + 2 * (size_t)g, 2 * GROUPS);
+  } else {
+#pragma unroll
+    for (int j = 0; j < GROUPS / 2; ++j) s.w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j)
+      if (g + j < end) {
+        uint16_t v;
+        __builtin_memcpy(&v, row + 2 * (size_t)(g + j), 2);
+        s.w[j / 2] |= (uint32_t)v << (16 * (j & 1));
+      }
+  }
+  return s;
+}
+__device__ __forceinline__ float scale_of(uint32_t w, int odd) {
+  return f16_bits_to_f32((uint16_t)(odd ? w >> 16 : w));
+}
+
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// one output: the sum, the residual, one rounding
+__device__ __forceinline__ uint16_t finished(double v, const uint16_t* res, size_t at) {
+  if (res != nullptr) v += (double)bf16_bits_to_f32(res[at]);
+  return f32_to_bf16_rne((float)v);
+}
+
+// ---------------------------------------------------------------------------
+// Up to 128 tokens.  One workgroup of eight waves per block of BN rows; the
+// waves share K, so the weight is read once (twice above 64 tokens, by two
+// token ranges).  Each wave copies its codes (chunks of CH groups, two slots)
+// and activations (groups, NX slots) straight into its own part of LDS,
+// whole runs of memory per instruction, and reads them back in operand order;
+// no barrier until the eight waves' sums meet.
+//
+// Every copy of the loop is issued whether or not its group exists (past the
+// wave's share it reads nothing), so that the counts of the waits hold.
+// ---------------------------------------------------------------------------
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+
+template <int RT, int TT, int CH, int NX>
+__global__ void __launch_bounds__(kThreads, 2)
+mx8_stream_kernel(Mx8Kernel a, int BN) {
+  static_assert(NX <= CH && (2 * CH) % NX == 0, "slots");
+  constexpr int CROW = CH * 32;                // bytes of a row in a chunk
+  constexpr int CPC = CROW / 16;               // 16-byte pieces of it
+  constexpr int CSLOT = RT * 32 * CROW;        // a wave's codes of a chunk
+  constexpr int XSLOT = TT * 32 * 64;          // a wave's activations of a group
+  constexpr int NC = CSLOT / 1024, NI = XSLOT / 1024;
+  // (an object per slot, so that a read of one is known not to depend on a
+  // copy in flight into another)
+  __shared__ __attribute__((aligned(16))) uint8_t c0[kWaves * CSLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t c1[kWaves * CSLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t x0[kWaves * XSLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t x1[kWaves * XSLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t x2[NX > 2 ? kWaves * XSLOT : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t x3[NX > 2 ? kWaves * XSLOT : 16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 31, lh = lane >> 5;
+  const int K = a.K, G = K >> 6;
+  const int n0 = blockIdx.x * BN, rows = min(BN, a.N - n0);
+  const int t0 = blockIdx.y * (32 * TT), tokens = min(32 * TT, a.T - t0);
+  const int gb = (int)((int64_t)G * wave / kWaves), cnt = (int)((int64_t)G * (wave + 1) / kWaves) - gb;
+  const uint32_t crow = (uint32_t)K >> 1;
+
+  const rsrc_t rc = make_rsrc(a.codes + (size_t)n0 * crow, (uint32_t)rows * crow);
+  const rsrc_t rx = make_rsrc(a.x + (size_t)t0 * K, (uint32_t)tokens * (uint32_t)K);
+  // Row r keeps its pieces permuted (piece p at p ^ key(r)), so that reads of
+  // one piece of neighbouring rows spread over the banks.
+  auto ckey = [](int r) { return CPC == 8 ? r & 7 : (r >> 1) & 3; };
+  auto xkey = [](int r) { return (r >> 1) & 3; };
+  constexpr int CPI = 64 / CPC;  // rows of a copy
+  uint32_t coff[NC], xoff[NI];
+  int cgroup;  // the group of this lane's piece (the key of a row repeats with the copies' rows)
+  {
+    const int r = lane / CPC, p = (lane % CPC) ^ ckey(r);
+    cgroup = p >> 1;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int row = j * CPI + r;
+      coff[j] = row < rows ? (uint32_t)row * crow + 32u * gb + 16u * p : kNowhere;
+    }
+    const int t = lane >> 2, xp = (lane & 3) ^ xkey(t);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int tok = 16 * j + t;
+      xoff[j] = tok < tokens ? (uint32_t)tok * (uint32_t)K + 64u * gb + 16u * xp : kNowhere;
+    }
+  }
+  static_assert(CPC == 8 ? CPI % 8 == 0 : CPI % 8 == 0, "a key per lane");
+  auto issue_codes = [&](uint8_t* slot, int c) __device__ {
+    const bool in = c * CH + cgroup < cnt;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      dma16<2>(rc, in ? coff[j] + (uint32_t)c * CROW : kNowhere, 0, slot + wave * CSLOT + j * 1024);
+  };
+  auto issue_x = [&](uint8_t* slot, int q) __device__ {
+    const bool in = q < cnt;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) dma16(rx, in ? xoff[j] + 64u * (uint32_t)q : kNowhere, 0, slot + wave * XSLOT + j * 1024);
+  };
+  struct Scales {
+    Strip<CH> w[RT], x[TT];
+  };
+  const uint8_t* wrow[RT];
+  const uint8_t* xrow[TT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    wrow[r] = reinterpret_cast<const uint8_t*>(a.scales + (size_t)(n0 + min(32 * r + li, rows - 1)) * G);
+#pragma unroll
+  for (int t = 0; t < TT; ++t) xrow[t] = a.xs + (size_t)(t0 + min(32 * t + li, tokens - 1)) * (K >> 5);
+  auto load_scales = [&](Scales& s, int c) __device__ {
+    const int g = gb + c * CH;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s.w[r] = load_strip<CH>(wrow[r], g, G);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) s.x[t] = load_strip<CH>(xrow[t], g, G);
+  };
+
+  f32x16_t acc[RT][TT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[r][t] = f32x16_t{};
+
+  // group J of a chunk
+  auto group = [&](auto jc, const uint8_t* cs, const uint8_t* xs, const Scales& s) __device__ {
+    constexpr int J = decltype(jc)::value, SEL = 2 * (J & 1);
+    const uint8_t* cw = cs + wave * CSLOT;
+    const uint8_t* xw = xs + wave * XSLOT;
+    v8i_t q[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const uint8_t* p = cw + (32 * r + li) * CROW + 8 * lh;
+      q[r] = mx8::code_operand(*reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * J) ^ ckey(li))),
+                               *reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * J + 1) ^ ckey(li))));
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const uint8_t* p = xw + (32 * t + li) * 64;
+      const v8i_t v = mx8::value_operand(*reinterpret_cast<const u32x4_t*>(p + 16 * (lh ^ xkey(li))),
+                                         *reinterpret_cast<const u32x4_t*>(p + 16 * ((2 + lh) ^ xkey(li))));
+      const uint32_t e = s.x[t].w[J / 2] >> (8 * lh);
+      const f32x16_t off = mx8::offset_sums<SEL>(v, e);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const f32x16_t d = mx8::product<SEL>(v, q[r], off, e);
+        const float f = scale_of(s.w[r].w[J / 2], J & 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[r][t][i] = __builtin_fmaf(f, d[i], acc[r][t][i]);
+      }
+    }
+  };
+  auto xslot = [&](int q) __device__ -> uint8_t* { return q % NX == 0 ? x0 : q % NX == 1 ? x1 : q % NX == 2 ? x2 : x3; };
+
+  if (cnt > 0) {
+    Scales s0, s1;
+    issue_codes(c0, 0);
+    load_scales(s0, 0);
+    in_order();
+    static_for<NX>([&](auto q) __device__ { issue_x(xslot(decltype(q)::value), decltype(q)::value); });
+    issue_codes(c1, 1);
+    in_order();
+    if (CH < cnt) load_scales(s1, 1);
+    // a chunk; false: it held the wave's last group.  Before group q the
+    // copies issued after x(q) may be in flight: NX - 1 groups of
+    // activations, and the codes of the next chunk if they lie between.
+    auto chunk = [&](auto oddc, uint8_t* cs, Scales& s, int c) __device__ {
+      bool more = true;
+      static_for<CH>([&](auto jc) __device__ {
+        constexpr int J = decltype(jc)::value, Q = CH * decltype(oddc)::value + J;
+        if (!more) return;
+        in_order();
+        wait_vm<(NX - 1) * NI + (J < NX ? NC : 0)>();
+        in_order();
+        group(jc, cs, xslot(Q), s);
+        more = c * CH + J + 1 < cnt;
+        wait_lgkm0();
+        in_order();
+        issue_x(xslot(Q), c * CH + J + NX);
+        in_order();
+      });
+      if (!more) return false;
+      issue_codes(cs, c + 2);
+      in_order();
+      if ((c + 2) * CH < cnt) load_scales(s, c + 2);
+      return true;
+    };
+    for (int c = 0;; c += 2) {
+      if (!chunk(Slot<0>{}, c0, s0, c)) break;
+      if (!chunk(Slot<1>{}, c1, s1, c + 1)) break;
+    }
+    wait_vm<0>();  // (nothing lands in the slots any more)
+  }
+  __syncthreads();
+
+  // the waves' sums: a tile of 32 tokens x 32 rows per wave in each of RT TT
+  // slots of LDS
+  constexpr int TILE = 32 * 32 * 4;
+  static_assert(kWaves * CSLOT >= kWaves * TILE && (RT * TT <= 2 || kWaves * XSLOT >= kWaves * TILE), "room");
+  auto room = [&](int i) __device__ -> float* {
+    return reinterpret_cast<float*>(i == 0 ? c0 : i == 1 ? c1 : i == 2 ? x0 : x1);
+  };
+  static_for<RT * TT>([&](auto ic) __device__ {
+    constexpr int I = decltype(ic)::value;
+    float* p = room(I) + wave * 1024 + 128 * lh + li;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[32 * (8 * (i >> 2) + (i & 3))] = acc[I % RT][I / RT][i];
+  });
+  __syncthreads();
+  static_for<RT * TT>([&](auto ic) __device__ {
+    constexpr int I = decltype(ic)::value;
+    const float* p = room(I);
+#pragma unroll
+    for (int o = tid; o < 1024; o += kThreads) {
+      const int r = 32 * (I % RT) + (o & 31), t = 32 * (I / RT) + (o >> 5);
+      if (r >= rows || t >= tokens) continue;
+      double v = 0.0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) v += (double)p[w * 1024 + o];
+      const size_t at = (size_t)(t0 + t) * a.N + n0 + r;
+      a.y[at] = finished(v, a.res, at);
+    }
+  });
+}
+
+// ---------------------------------------------------------------------------
+// More tokens.  A workgroup of four waves (WR x WT) takes WR RT 32 rows and
+// WT TT 32 tokens; stages of two groups (128 bytes of a token, 64 of a row)
+// go through four slots of LDS, asked for three stages ahead, one barrier
+// per stage.  blockIdx.y: a share of K (binary32 sums to `part`).
+// ---------------------------------------------------------------------------
+constexpr int kTileThreads = 256;
+constexpr int kBlock = 8;  // groups between two loads of scales: four stages
+
+template <int WR, int WT, int RT, int TT>
+__global__ void __launch_bounds__(kTileThreads, 1)
+mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
+  static_assert(WR * WT == 4 && (WR * RT) % 2 == 0, "four waves, whole copies");
+  constexpr int ROWS = WR * RT * 32, TOKENS = WT * TT * 32;
+  constexpr int CBYTES = ROWS * 64, XBYTES = TOKENS * 128, SLOT = CBYTES + XBYTES;
+  constexpr int NC = CBYTES / 4096, NI = XBYTES / 4096, LOADS = NC + NI;  // a wave's copies of a stage
+  __shared__ __attribute__((aligned(16))) uint8_t l0[SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t l1[SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t l2[SLOT];
+  __shared__ __attribute__((aligned(16))) uint8_t l3[SLOT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 31, lh = lane >> 5;
+  const int wr = wave % WR, wt = wave / WR;
+  // consecutive workgroups go to the eight XCDs in turn: each XCD takes a run
+  // of tiles, the tokens of a few rows, so that its L2 holds those rows once
+  int tile = blockIdx.x;
+  {
+    const int total = tiles_n * tiles_t, each = total / 8, rest = total % 8;
+    const int xcd = tile & 7, at = tile >> 3;
+    tile = xcd * each + min(xcd, rest) + at;
+  }
+  const int n0 = tile / tiles_t * ROWS, t0 = tile % tiles_t * TOKENS;
+  const int K = a.K, G = K >> 6;
+  const int rows = min(ROWS, a.N - n0), tokens = min(TOKENS, a.T - t0);
+  const int blocks = (G + kBlock - 1) / kBlock;
+  const int gb = (int)((int64_t)blocks * blockIdx.y / shares) * kBlock;
+  const int ge = min((int)((int64_t)blocks * (blockIdx.y + 1) / shares) * kBlock, G);
+  const uint32_t crow = (uint32_t)K >> 1;
+
+  const rsrc_t rc = make_rsrc(a.codes + (size_t)n0 * crow, (uint32_t)rows * crow);
+  const rsrc_t rx = make_rsrc(a.x + (size_t)t0 * K, (uint32_t)tokens * (uint32_t)K);
+  auto ckey = [](int r) { return (r >> 1) & 3; };
+  auto xkey = [](int r) { return r & 7; };
+  uint32_t coff[NC], xoff[NI];
+  int cgroup, xgroup;  // of this lane's pieces
+  {
+    const int r = lane >> 2, p = (lane & 3) ^ ckey(r);
+    cgroup = p >> 1;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int row = (j * 4 + wave) * 16 + r;
+      coff[j] = row < rows ? (uint32_t)row * crow + 16u * p : kNowhere;
+    }
+    const int t = lane >> 3, xp = (lane & 7) ^ xkey(t);
+    xgroup = xp >> 2;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int tok = (j * 4 + wave) * 8 + t;
+      xoff[j] = tok < tokens ? (uint32_t)tok * (uint32_t)K + 16u * xp : kNowhere;
+    }
+  }
+  // (every copy is issued, past the share's end it reads nothing: the waits count on it)
+  auto issue = [&](uint8_t* slot, int g) __device__ {
+    const bool cin = g + cgroup < ge, xin = g + xgroup < ge;
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      dma16(rx, xin ? xoff[j] + 64u * (uint32_t)g : kNowhere, 0, slot + CBYTES + (j * 4 + wave) * 1024);
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      dma16(rc, cin ? coff[j] + 32u * (uint32_t)g : kNowhere, 0, slot + (j * 4 + wave) * 1024);
+  };
+  struct Scales {
+    Strip<kBlock> w[RT], x[TT];
+  };
+  const uint8_t* wrow[RT];
+  const uint8_t* xrow[TT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    wrow[r] = reinterpret_cast<const uint8_t*>(a.scales + (size_t)(n0 + min((wr * RT + r) * 32 + li, rows - 1)) * G);
+#pragma unroll
+  for (int t = 0; t < TT; ++t) xrow[t] = a.xs + (size_t)(t0 + min((wt * TT + t) * 32 + li, tokens - 1)) * (K >> 5);
+  auto load_scales = [&](Scales& s, int g) __device__ {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s.w[r] = load_strip<kBlock>(wrow[r], g, G);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) s.x[t] = load_strip<kBlock>(xrow[t], g, G);
+  };
+
+  f32x16_t acc[RT][TT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[r][t] = f32x16_t{};
+
+  // group J of a block (J % 2 of its stage)
+  auto group = [&](auto jc, const uint8_t* slot, const Scales& s) __device__ {
+    constexpr int J = decltype(jc)::value, SEL = 2 * (J & 1), H = J & 1;
+    v8i_t v[TT];
+    uint32_t e[TT];
+    f32x16_t off[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const uint8_t* p = slot + CBYTES + ((wt * TT + t) * 32 + li) * 128;
+      v[t] = mx8::value_operand(*reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * H + lh) ^ xkey(li))),
+                                *reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * H + 2 + lh) ^ xkey(li))));
+      e[t] = s.x[t].w[J / 2] >> (8 * lh);
+      off[t] = mx8::offset_sums<SEL>(v[t], e[t]);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const uint8_t* p = slot + ((wr * RT + r) * 32 + li) * 64 + 8 * lh;
+      const v8i_t q = mx8::code_operand(*reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * H) ^ ckey(li))),
+                                        *reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * H + 1) ^ ckey(li))));
+      const float f = scale_of(s.w[r].w[J / 2], J & 1);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const f32x16_t d = mx8::product<SEL>(v[t], q, off[t], e[t]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[r][t][i] = __builtin_fmaf(f, d[i], acc[r][t][i]);
+      }
+    }
+  };
+
+  if (gb < ge) {
+    Scales cur, next;
+    load_scales(cur, gb);
+    in_order();
+    issue(l0, gb);
+    issue(l1, gb + 2);
+    issue(l2, gb + 4);
+    in_order();
+    for (int g0 = gb; g0 < ge; g0 += kBlock) {
+      if (g0 + kBlock < ge) load_scales(next, g0 + kBlock);
+      static_for<4>([&](auto sc) __device__ {
+        constexpr int S = decltype(sc)::value;
+        const int g = g0 + 2 * S;
+        uint8_t* const here = S == 0 ? l0 : S == 1 ? l1 : S == 2 ? l2 : l3;
+        uint8_t* const ahead = S == 0 ? l3 : S == 1 ? l0 : S == 2 ? l1 : l2;
+        in_order();
+        wait_vm<2 * LOADS>();  // this stage's copies; two stages' are in flight
+        wait_lgkm0();          // and the reads of the slot that is filled next are done
+        __builtin_amdgcn_s_barrier();
+        in_order();
+        issue(ahead, g + 6);
+        in_order();
+        if (g < ge) group(Slot<2 * S>{}, here, cur);
+        if (g + 1 < ge) group(Slot<2 * S + 1>{}, here, cur);
+      });
+      cur = next;
+    }
+    wait_vm<0>();  // (nothing lands in the slots any more)
+  }
+
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int n = (wr * RT + r) * 32 + li;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int tok = (wt * TT + t) * 32 + 8 * (i >> 2) + 4 * lh + (i & 3);
+        if (n >= rows || tok >= tokens) continue;
+        const size_t at = (size_t)(t0 + tok) * a.N + n0 + n;
+        if (shares > 1) a.part[(size_t)blockIdx.y * a.T * a.N + at] = acc[r][t][i];
+        else a.y[at] = finished((double)acc[r][t][i], a.res, at);
+      }
+  }
+}
+
+// y = bf16(the shares' sums (+ residual)); a thread takes an output
+__global__ void __launch_bounds__(256)
+mx8_join_kernel(const float* part, const uint16_t* res, uint16_t* y, int64_t outputs, int shares) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= outputs) return;
+  double v = 0.0;
+  for (int s = 0; s < shares; ++s) v += (double)part[(size_t)s * outputs + at];
+  y[at] = finished(v, res, (size_t)at);
+}
+
+constexpr int kCUs = 256;
+constexpr int64_t kStreamTokens = 128;
+
+struct TilePlan {
+  int config;  // 0: 192 x 128, 1: 128 x 64
+  int rows, tokens, tiles_n, tiles_t, shares;
+};
+TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
+  TilePlan best{};
+  double least = 0;
+  const int64_t blocks = (k / 64 + kBlock - 1) / kBlock;
+  for (int c = 0; c < 2; ++c) {
+    TilePlan p{c, c == 0 ? 192 : 128, c == 0 ? 128 : 64, 0, 0, 1};
+    p.tiles_n = (int)((n + p.rows - 1) / p.rows);
+    p.tiles_t = (int)((t + p.tokens - 1) / p.tokens);
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;
+    for (int shares = 1; shares <= 8 && shares <= blocks; shares *= 2) {
+      p.shares = shares;
+      const double rounds = (double)((tiles * shares + kCUs - 1) / kCUs);
+      // us: a block of eight groups, start and end of a workgroup, the pass
+      // over the shares' sums
+      const double time = rounds * ((blocks + shares - 1) / shares * (c == 0 ? 3.0 : 1.3) + 5.0) +
+                          (shares > 1 ? 4.0 + (double)shares * n * t * 8 / 4e6 : 0.0);
+      if ((c == 0 && shares == 1) || time < least) {
+        least = time;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
+template <int RT, int TT, int CH, int NX>
+void launch_stream(const Mx8Kernel& k, int bn, int ranges, hipStream_t stream) {
+  mx8_stream_kernel<RT, TT, CH, NX><<<dim3((unsigned)((k.N + bn - 1) / bn), (unsigned)ranges), kThreads, 0, stream>>>(k, bn);
+}
+
+}  // namespace
+
+size_t mx8_workspace_bytes(int64_t n, int64_t k, int64_t t) {
+  if (t <= kStreamTokens) return 0;
+  const TilePlan p = tile_plan(n, k, t);
+  return p.shares > 1 ? (size_t)p.shares * n * t * 4 : 0;
+}
+
+hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
+  const Mx8Kernel k{static_cast<const uint8_t*>(a.x),      static_cast<const uint8_t*>(a.xs),
+                    static_cast<const uint8_t*>(a.codes),  static_cast<const uint16_t*>(a.scales),
+                    static_cast<const uint16_t*>(a.res),   static_cast<uint16_t*>(a.y),
+                    static_cast<float*>(workspace),        (int)a.n,
+                    (int)a.k,                              (int)a.t};
+  if (a.t <= kStreamTokens) {
+    // rows per workgroup: whole rounds of one workgroup per CU
+    const int64_t rounds = (a.n + 64 * kCUs - 1) / (64 * kCUs);
+    const int bn = (int)((a.n + kCUs * rounds - 1) / (kCUs * rounds));
+    const int ranges = a.t <= 64 ? 1 : 2;
+    const bool two = a.t > 32;
+    if (bn <= 32 && !two) launch_stream<1, 1, 4, 4>(k, bn, ranges, stream);
+    else if (bn <= 32) launch_stream<1, 2, 4, 2>(k, bn, ranges, stream);
+    else if (!two) launch_stream<2, 1, 2, 2>(k, bn, ranges, stream);
+    else launch_stream<2, 2, 2, 2>(k, bn, ranges, stream);
+    return hipGetLastError();
+  }
+  const TilePlan p = tile_plan(a.n, a.k, a.t);
+  const dim3 grid((unsigned)(p.tiles_n * p.tiles_t), (unsigned)p.shares);
+  if (p.config == 0) mx8_tile_kernel<2, 2, 3, 2><<<grid, kTileThreads, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  else mx8_tile_kernel<2, 2, 2, 1><<<grid, kTileThreads, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.shares == 1) return e;
+  const int64_t outputs = a.n * a.t;
+  mx8_join_kernel<<<dim3((unsigned)((outputs + 255) / 256)), 256, 0, stream>>>(k.part, k.res, k.y, outputs, p.shares);
+  return hipGetLastError();
+}
+
+}  // namespace q4lin

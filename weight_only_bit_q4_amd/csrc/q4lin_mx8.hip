@@ -48,25 +48,30 @@ struct Strip {
   uint32_t w[(GROUPS + 1) / 2];
 };
 template <int GROUPS>
-__device__ __forceinline__ Strip<GROUPS> load_strip(const uint8_t* row, int g, int end) {
+__device__ __forceinline__ Strip<GROUPS> load_strip(const uint8_t* base, uint32_t row, int g, int end) {
   Strip<GROUPS> s;
+  const uint8_t* p = base + 2 * (size_t)g;
   if (g + GROUPS <= end) {
-    __builtin_memcpy(&s, row + 2 * (size_t)g, 2 * GROUPS);
+    __builtin_memcpy(&s, p + row, 2 * GROUPS);
   } else {
 #pragma unroll
-    for (int j = 0; j < GROUPS / 2; ++j) s.w[j] = 0;
+    for (int j = 0; j < (GROUPS + 1) / 2; ++j) s.w[j] = 0;
 #pragma unroll
     for (int j = 0; j < GROUPS; ++j)
       if (g + j < end) {
         uint16_t v;
-        __builtin_memcpy(&v, row + 2 * (size_t)(g + j), 2);
+        __builtin_memcpy(&v, p + 2 * j + row, 2);
         s.w[j / 2] |= (uint32_t)v << (16 * (j & 1));
       }
   }
   return s;
 }
+// (opaque, so that the multiply-adds take the converted scale: left to choose,
+// the compiler converts in each of them)
 __device__ __forceinline__ float scale_of(uint32_t w, int odd) {
-  return f16_bits_to_f32((uint16_t)(odd ? w >> 16 : w));
+  float f = f16_bits_to_f32((uint16_t)(odd ? w >> 16 : w));
+  asm("" : "+v"(f));
+  return f;
 }
 
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
@@ -155,19 +160,20 @@ mx8_stream_kernel(Mx8Kernel a, int BN) {
   struct Scales {
     Strip<CH> w[RT], x[TT];
   };
-  const uint8_t* wrow[RT];
-  const uint8_t* xrow[TT];
+  // (32-bit offsets from the workgroup's first row)
+  const uint8_t* const wbase = reinterpret_cast<const uint8_t*>(a.scales + (size_t)n0 * G);
+  const uint8_t* const xbase = a.xs + (size_t)t0 * (K >> 5);
+  uint32_t wrow[RT], xrow[TT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    wrow[r] = reinterpret_cast<const uint8_t*>(a.scales + (size_t)(n0 + min(32 * r + li, rows - 1)) * G);
+  for (int r = 0; r < RT; ++r) wrow[r] = (uint32_t)min(32 * r + li, rows - 1) * 2u * (uint32_t)G;
 #pragma unroll
-  for (int t = 0; t < TT; ++t) xrow[t] = a.xs + (size_t)(t0 + min(32 * t + li, tokens - 1)) * (K >> 5);
+  for (int t = 0; t < TT; ++t) xrow[t] = (uint32_t)min(32 * t + li, tokens - 1) * 2u * (uint32_t)G;
   auto load_scales = [&](Scales& s, int c) __device__ {
     const int g = gb + c * CH;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) s.w[r] = load_strip<CH>(wrow[r], g, G);
+    for (int r = 0; r < RT; ++r) s.w[r] = load_strip<CH>(wbase, wrow[r], g, G);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) s.x[t] = load_strip<CH>(xrow[t], g, G);
+    for (int t = 0; t < TT; ++t) s.x[t] = load_strip<CH>(xbase, xrow[t], g, G);
   };
 
   f32x16_t acc[RT][TT];
@@ -278,25 +284,38 @@ mx8_stream_kernel(Mx8Kernel a, int BN) {
 }
 
 // ---------------------------------------------------------------------------
-// More tokens.  A workgroup of four waves (WR x WT) takes WR RT 32 rows and
-// WT TT 32 tokens; stages of two groups (128 bytes of a token, 64 of a row)
-// go through four slots of LDS, asked for three stages ahead, one barrier
-// per stage.  blockIdx.y: a share of K (binary32 sums to `part`).
+// More tokens.  A workgroup of WR x WT waves takes WR RT 32 rows and WT TT 32
+// tokens.  Stages of two groups (128 bytes of a token, 64 of a row) go
+// straight into four slots of LDS, asked for three stages ahead, their copies
+// spread over a stage's products (a burst of them holds the waves up at the
+// address unit); one barrier per stage.  The scales of kRun groups are read
+// row by row (whole runs of memory), one thread a row or token, and put into
+// LDS by group, where a lane finds its row's without a gather.
+// blockIdx.y: a share of K (binary32 sums to `part`).
 // ---------------------------------------------------------------------------
-constexpr int kTileThreads = 256;
-constexpr int kBlock = 8;  // groups between two loads of scales: four stages
+constexpr int kRun = 16;   // groups between two loads of scales: eight stages
+constexpr int kSlots = 4;
 
 template <int WR, int WT, int RT, int TT>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(64 * WR * WT, 2)
 mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
-  static_assert(WR * WT == 4 && (WR * RT) % 2 == 0, "four waves, whole copies");
-  constexpr int ROWS = WR * RT * 32, TOKENS = WT * TT * 32;
-  constexpr int CBYTES = ROWS * 64, XBYTES = TOKENS * 128, SLOT = CBYTES + XBYTES;
-  constexpr int NC = CBYTES / 4096, NI = XBYTES / 4096, LOADS = NC + NI;  // a wave's copies of a stage
+  constexpr int WAVES = WR * WT, ROWS = WR * RT * 32, TOKENS = WT * TT * 32, LINES = ROWS + TOKENS;
+  // a wave's copies of a stage, 16 rows' codes or eight tokens each (the last
+  // may be of no row: it reads nothing)
+  constexpr int NC = (ROWS / 16 + WAVES - 1) / WAVES, NI = TOKENS / 8 / WAVES, LOADS = NC + NI;
+  static_assert(NI * WAVES * 8 == TOKENS, "whole copies");
+  constexpr int CBYTES = NC * WAVES * 1024, XBYTES = TOKENS * 128, SLOT = CBYTES + XBYTES;
+  static_assert(LINES <= 64 * WAVES, "a thread per row and token");
+  // (an object per slot: see the kernel above)
   __shared__ __attribute__((aligned(16))) uint8_t l0[SLOT];
   __shared__ __attribute__((aligned(16))) uint8_t l1[SLOT];
   __shared__ __attribute__((aligned(16))) uint8_t l2[SLOT];
   __shared__ __attribute__((aligned(16))) uint8_t l3[SLOT];
+  // by group: the rows' fp16 scales, then the tokens' two E8M0 bytes; those of
+  // a lane's rows (tokens), 32 apart, beside each other
+  constexpr int RP = RT == 3 ? 4 : RT, ROWROOM = WR * RP * 32, ROOM = ROWROOM + TOKENS;
+  static_assert(RT <= 4 && TT <= 2, "one read of a lane's scales");
+  __shared__ __attribute__((aligned(8))) uint16_t table[2 * kRun * ROOM];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, lh = lane >> 5;
   const int wr = wave % WR, wt = wave / WR;
@@ -311,9 +330,9 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   const int n0 = tile / tiles_t * ROWS, t0 = tile % tiles_t * TOKENS;
   const int K = a.K, G = K >> 6;
   const int rows = min(ROWS, a.N - n0), tokens = min(TOKENS, a.T - t0);
-  const int blocks = (G + kBlock - 1) / kBlock;
-  const int gb = (int)((int64_t)blocks * blockIdx.y / shares) * kBlock;
-  const int ge = min((int)((int64_t)blocks * (blockIdx.y + 1) / shares) * kBlock, G);
+  const int stages = (G + 1) >> 1;
+  const int gb = (int)((int64_t)stages * blockIdx.y / shares) * 2;
+  const int ge = min((int)((int64_t)stages * (blockIdx.y + 1) / shares) * 2, G);
   const uint32_t crow = (uint32_t)K >> 1;
 
   const rsrc_t rc = make_rsrc(a.codes + (size_t)n0 * crow, (uint32_t)rows * crow);
@@ -327,42 +346,52 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
     cgroup = p >> 1;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int row = (j * 4 + wave) * 16 + r;
+      const int row = (j * WAVES + wave) * 16 + r;
       coff[j] = row < rows ? (uint32_t)row * crow + 16u * p : kNowhere;
     }
     const int t = lane >> 3, xp = (lane & 7) ^ xkey(t);
     xgroup = xp >> 2;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int tok = (j * 4 + wave) * 8 + t;
+      const int tok = (j * WAVES + wave) * 8 + t;
       xoff[j] = tok < tokens ? (uint32_t)tok * (uint32_t)K + 16u * xp : kNowhere;
     }
   }
-  // (every copy is issued, past the share's end it reads nothing: the waits count on it)
-  auto issue = [&](uint8_t* slot, int g) __device__ {
-    const bool cin = g + cgroup < ge, xin = g + xgroup < ge;
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-      dma16(rx, xin ? xoff[j] + 64u * (uint32_t)g : kNowhere, 0, slot + CBYTES + (j * 4 + wave) * 1024);
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-      dma16(rc, cin ? coff[j] + 32u * (uint32_t)g : kNowhere, 0, slot + (j * 4 + wave) * 1024);
+  // Copy j of the stage at group g.  (Every copy is issued, past the share's
+  // end it reads nothing: the waits count on it.  CHECK: g + 2 may pass it.)
+  auto copy = [&](auto jc, auto check, uint8_t* slot, int g) __device__ {
+    constexpr int J = decltype(jc)::value;
+    constexpr bool X = J < NI;
+    constexpr int I = X ? J : J - NI;
+    const rsrc_t r = X ? rx : rc;
+    uint8_t* const to = slot + (X ? CBYTES : 0) + (I * WAVES + wave) * 1024;
+    const uint32_t step = X ? 64u : 32u;
+    uint32_t off = X ? xoff[X ? I : 0] : coff[X ? 0 : I];
+    if constexpr (decltype(check)::value) {
+      off = g + (X ? xgroup : cgroup) < ge ? off + step * (uint32_t)g : kNowhere;
+      dma16(r, off, 0, to);
+    } else {
+      dma16(r, off, step * (uint32_t)g, to);
+    }
   };
-  struct Scales {
-    Strip<kBlock> w[RT], x[TT];
+
+  // this thread's line of scales (32-bit offsets from the workgroup's first)
+  const bool of_rows = tid < ROWS;
+  const uint8_t* const lbase = of_rows ? reinterpret_cast<const uint8_t*>(a.scales + (size_t)n0 * G)
+                                       : a.xs + (size_t)t0 * (K >> 5);
+  const uint32_t line = (uint32_t)(of_rows ? min(tid, rows - 1) : min(tid - ROWS, tokens - 1)) * 2u * (uint32_t)G;
+  auto load_line = [&](Strip<kRun>& s, int g) __device__ {
+    if (tid < LINES) s = load_strip<kRun>(lbase, line, g, ge);
   };
-  const uint8_t* wrow[RT];
-  const uint8_t* xrow[TT];
+  // (half: where the table's half begins, 0 or kRun ROOM; an index that the
+  // compiler must compute keeps every access a plain one of this object)
+  const int at32 = tid >> 5, tok32 = at32 - ROWS / 32;
+  const int place = of_rows ? at32 / RT * (RP * 32) + (tid & 31) * RP + at32 % RT
+                            : ROWROOM + tok32 / TT * (TT * 32) + (tid & 31) * TT + tok32 % TT;
+  auto put_line = [&](const Strip<kRun>& s, int half) __device__ {
+    if (tid < LINES)
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    wrow[r] = reinterpret_cast<const uint8_t*>(a.scales + (size_t)(n0 + min((wr * RT + r) * 32 + li, rows - 1)) * G);
-#pragma unroll
-  for (int t = 0; t < TT; ++t) xrow[t] = a.xs + (size_t)(t0 + min((wt * TT + t) * 32 + li, tokens - 1)) * (K >> 5);
-  auto load_scales = [&](Scales& s, int g) __device__ {
-#pragma unroll
-    for (int r = 0; r < RT; ++r) s.w[r] = load_strip<kBlock>(wrow[r], g, G);
-#pragma unroll
-    for (int t = 0; t < TT; ++t) s.x[t] = load_strip<kBlock>(xrow[t], g, G);
+      for (int j = 0; j < kRun; ++j) table[half + j * ROOM + place] = (uint16_t)(s.w[j / 2] >> (16 * (j & 1)));
   };
 
   f32x16_t acc[RT][TT];
@@ -371,114 +400,223 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[r][t] = f32x16_t{};
 
-  // group J of a block (J % 2 of its stage)
-  auto group = [&](auto jc, const uint8_t* slot, const Scales& s) __device__ {
-    constexpr int J = decltype(jc)::value, SEL = 2 * (J & 1), H = J & 1;
-    v8i_t v[TT];
-    uint32_t e[TT];
-    f32x16_t off[TT];
+  // (offsets that the compiler cannot relate: it would pair the reads of two
+  // row tiles, and hold the pair back until every copy in flight has landed)
+  uint32_t roff[RT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
+  for (int r = 0; r < RT; ++r) {
+    roff[r] = (uint32_t)(((wr * RT + r) * 32 + li) * 64 + 8 * lh);
+    asm("" : "+v"(roff[r]));
+  }
+  // group J of a stage; scales: where its line of the table begins; copies(i):
+  // room for a copy beside the i-th of two products
+  auto group = [&](auto jc, const uint8_t* slot, int scales, auto&& copies) __device__ {
+    constexpr int H = decltype(jc)::value;
+    v8i_t v[TT];
+    f32x16_t off[TT];
+    const uint16_t* const fp = table + scales + (wr * 32 + li) * RP;
+    const uint16_t* const ep = table + scales + ROWROOM + (wt * 32 + li) * TT;
+    u32x2_t fs;
+    if constexpr (RP == 4) fs = *reinterpret_cast<const u32x2_t*>(fp);
+    else if constexpr (RP == 2) fs.x = *reinterpret_cast<const uint32_t*>(fp);
+    else fs.x = *fp;
+    const uint32_t e = (TT == 2 ? *reinterpret_cast<const uint32_t*>(ep) : (uint32_t)*ep) >> (8 * lh);
+    static_for<TT>([&](auto tc) __device__ {
+      constexpr int t = decltype(tc)::value;
       const uint8_t* p = slot + CBYTES + ((wt * TT + t) * 32 + li) * 128;
       v[t] = mx8::value_operand(*reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * H + lh) ^ xkey(li))),
                                 *reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * H + 2 + lh) ^ xkey(li))));
-      e[t] = s.x[t].w[J / 2] >> (8 * lh);
-      off[t] = mx8::offset_sums<SEL>(v[t], e[t]);
-    }
+      off[t] = mx8::offset_sums<2 * t>(v[t], e);
+    });
+    copies(Slot<0>{});
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const uint8_t* p = slot + ((wr * RT + r) * 32 + li) * 64 + 8 * lh;
+      const uint8_t* p = slot + roff[r];
       const v8i_t q = mx8::code_operand(*reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * H) ^ ckey(li))),
                                         *reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * H + 1) ^ ckey(li))));
-      const float f = scale_of(s.w[r].w[J / 2], J & 1);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const f32x16_t d = mx8::product<SEL>(v[t], q, off[t], e[t]);
+      const float f = scale_of(r < 2 ? fs.x : fs.y, r & 1);
+      static_for<TT>([&](auto tc) __device__ {
+        constexpr int t = decltype(tc)::value;
+        const f32x16_t d = mx8::product<2 * t>(v[t], q, off[t], e);
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[r][t][i] = __builtin_fmaf(f, d[i], acc[r][t][i]);
-      }
+        // (the sums are needed here: left alone, the compiler moves them past
+        // the stages and keeps every product until then)
+        asm volatile("" : "+v"(acc[r][t]));
+      });
+      if (r == 0) copies(Slot<1>{});
     }
+  };
+  auto slot_of = [&](int s) __device__ -> uint8_t* {
+    return s % kSlots == 0 ? l0 : s % kSlots == 1 ? l1 : s % kSlots == 2 ? l2 : l3;
   };
 
   if (gb < ge) {
-    Scales cur, next;
-    load_scales(cur, gb);
+    Strip<kRun> strip;
+    load_line(strip, gb);
     in_order();
-    issue(l0, gb);
-    issue(l1, gb + 2);
-    issue(l2, gb + 4);
+    static_for<kSlots - 1>([&](auto sc) __device__ {
+      constexpr int S = decltype(sc)::value;
+      static_for<LOADS>([&](auto j) __device__ { copy(j, Slot<1>{}, slot_of(S), gb + 2 * S); });
+    });
     in_order();
-    for (int g0 = gb; g0 < ge; g0 += kBlock) {
-      if (g0 + kBlock < ge) load_scales(next, g0 + kBlock);
-      static_for<4>([&](auto sc) __device__ {
+    put_line(strip, 0);
+    // A turn of the loop: a run of scales, eight stages.  WHOLE: all of its
+    // groups exist, and those of the three stages behind it.
+    auto turn = [&](auto whole, int half, int g0) __device__ {
+      constexpr bool WHOLE = decltype(whole)::value;
+      static_for<kRun / 2>([&](auto sc) __device__ {
         constexpr int S = decltype(sc)::value;
         const int g = g0 + 2 * S;
-        uint8_t* const here = S == 0 ? l0 : S == 1 ? l1 : S == 2 ? l2 : l3;
-        uint8_t* const ahead = S == 0 ? l3 : S == 1 ? l0 : S == 2 ? l1 : l2;
+        if (!WHOLE && g >= ge) return;
         in_order();
-        wait_vm<2 * LOADS>();  // this stage's copies; two stages' are in flight
-        wait_lgkm0();          // and the reads of the slot that is filled next are done
+        wait_vm<(kSlots - 2) * LOADS>();  // this stage's copies; two stages' are in flight
+        wait_lgkm0();                     // and the reads of the slot that is filled next are done
         __builtin_amdgcn_s_barrier();
         in_order();
-        issue(ahead, g + 6);
-        in_order();
-        if (g < ge) group(Slot<2 * S>{}, here, cur);
-        if (g + 1 < ge) group(Slot<2 * S + 1>{}, here, cur);
+        if (S == 0 && g0 + kRun < ge) load_line(strip, g0 + kRun);
+        if (S == 4 && g0 + kRun < ge) put_line(strip, kRun * ROOM - half);
+        uint8_t* const next = slot_of(S + kSlots - 1);
+        // a stage's copies in four places
+        auto some = [&](auto place) __device__ {
+          constexpr int P = decltype(place)::value;
+          in_order();
+          static_for<LOADS>([&](auto j) __device__ {
+            if constexpr (decltype(j)::value * 4 / LOADS == P) copy(j, Slot<WHOLE ? 0 : 1>{}, next, g + 2 * (kSlots - 1));
+          });
+          in_order();
+        };
+        group(Slot<0>{}, slot_of(S), half + 2 * S * ROOM, some);
+        if (WHOLE || g + 1 < ge)
+          group(Slot<1>{}, slot_of(S), half + (2 * S + 1) * ROOM,
+                [&](auto p) __device__ { some(Slot<2 + decltype(p)::value>{}); });
+        else {
+          some(Slot<2>{});
+          some(Slot<3>{});
+        }
       });
-      cur = next;
-    }
+    };
+    int g0 = gb, half = 0;
+    auto next_run = [&]() __device__ {
+      g0 += kRun;
+      half = kRun * ROOM - half;
+      asm("" : "+s"(half));
+    };
+    for (; g0 + kRun + 2 * (kSlots - 1) <= ge; next_run()) turn(Slot<1>{}, half, g0);
+    for (; g0 < ge; next_run()) turn(Slot<0>{}, half, g0);
     wait_vm<0>();  // (nothing lands in the slots any more)
   }
 
+  // The sums by way of LDS, each wave's own part of the slots (two 32 x 32
+  // tiles at most at a time), so that a lane stores eight rows of a token: 16
+  // bytes, whole runs of y.
+  __syncthreads();
+  constexpr int WIDTH = RT * 32, LD = WIDTH + 4;  // (a token's row of sums, shifted by four banks from the last)
+  constexpr int PER = SLOT / (32 * LD * 4);  // waves of a slot
+  static_assert(PER * kSlots >= WAVES, "room");
+  float* const mine = reinterpret_cast<float*>(slot_of(wave / PER) + wave % PER * (32 * LD * 4));
+  const bool wide = (a.N & 7) == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.res & 15) == 0 && shares == 1;
+  static_for<TT>([&](auto tc) __device__ {
+    constexpr int t = decltype(tc)::value;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int n = (wr * RT + r) * 32 + li;
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+      for (int i = 0; i < 16; ++i) mine[(8 * (i >> 2) + 4 * lh + (i & 3)) * LD + 32 * r + li] = acc[r][t][i];
+    wait_lgkm0();
+    in_order();
+    const int tok0 = (wt * TT + t) * 32, row0 = wr * RT * 32;
+    for (int o = lane; o < 32 * WIDTH / 8; o += 64) {
+      const int tok = o / (WIDTH / 8), c = o % (WIDTH / 8) * 8;
+      if (tok0 + tok >= tokens || row0 + c >= rows) continue;
+      const float* const v = mine + tok * LD + c;
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(v), hi = *reinterpret_cast<const f32x4_t*>(v + 4);
+      const size_t at = (size_t)(t0 + tok0 + tok) * a.N + n0 + row0 + c;
+      if (wide) {
+        float s[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int tok = (wt * TT + t) * 32 + 8 * (i >> 2) + 4 * lh + (i & 3);
-        if (n >= rows || tok >= tokens) continue;
-        const size_t at = (size_t)(t0 + tok) * a.N + n0 + n;
-        if (shares > 1) a.part[(size_t)blockIdx.y * a.T * a.N + at] = acc[r][t][i];
-        else a.y[at] = finished((double)acc[r][t][i], a.res, at);
+        for (int i = 0; i < 8; ++i) s[i] = i < 4 ? lo[i] : hi[i - 4];
+        if (a.res != nullptr) {
+          const u32x4_t r = *reinterpret_cast<const u32x4_t*>(a.res + at);
+          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s[i] = (float)((double)s[i] + (double)bf16_bits_to_f32(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu));
+        }
+        u32x4_t out;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          out[i] = (uint32_t)f32_to_bf16_rne(s[2 * i]) | ((uint32_t)f32_to_bf16_rne(s[2 * i + 1]) << 16);
+        *reinterpret_cast<u32x4_t*>(a.y + at) = out;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (row0 + c + i >= rows) break;
+          const float sum = i < 4 ? lo[i] : hi[i - 4];
+          if (shares > 1) a.part[(size_t)blockIdx.y * a.T * a.N + at + i] = sum;
+          else a.y[at + i] = finished((double)sum, a.res, at + i);
+        }
       }
-  }
+    }
+    wait_lgkm0();
+    in_order();
+  });
 }
 
-// y = bf16(the shares' sums (+ residual)); a thread takes an output
+// y = bf16(the shares' sums (+ residual)); a thread takes four outputs
 __global__ void __launch_bounds__(256)
 mx8_join_kernel(const float* part, const uint16_t* res, uint16_t* y, int64_t outputs, int shares) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t at = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (at >= outputs) return;
-  double v = 0.0;
-  for (int s = 0; s < shares; ++s) v += (double)part[(size_t)s * outputs + at];
-  y[at] = finished(v, res, (size_t)at);
+  double v[4] = {};
+  const int n = outputs - at < 4 ? (int)(outputs - at) : 4;
+  if (n == 4 && (outputs & 3) == 0) {
+    for (int s = 0; s < shares; ++s) {
+      const f32x4_t p = *reinterpret_cast<const f32x4_t*>(part + (size_t)s * outputs + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += (double)p[i];
+    }
+  } else {
+    for (int s = 0; s < shares; ++s)
+      for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] += (double)part[(size_t)s * outputs + at + i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) y[at + i] = finished(v[i], res, (size_t)(at + i));
 }
 
 constexpr int kCUs = 256;
 constexpr int64_t kStreamTokens = 128;
 
+// Tile shapes: rows and tokens of a workgroup, the time of a stage (us; alone
+// on its CU, and two workgroups there if so many fit), of a workgroup's start
+// and end.  Measured on 6144 x 5120 at 256 to 2048 tokens and 34816 x 5120 at
+// 1024: 63 / 53 / 69 us at 1024 tokens, 48 / 44 / 33 at 256.
+struct TileShape {
+  int rows, tokens;
+  double stage, both, ends;
+};
+constexpr TileShape kTiles[] = {{256, 128, 1.42, 0, 6.0}, {192, 128, 1.17, 0, 6.0}, {128, 64, 0.70, 1.05, 5.0}};
 struct TilePlan {
-  int config;  // 0: 192 x 128, 1: 128 x 64
-  int rows, tokens, tiles_n, tiles_t, shares;
+  int shape, tiles_n, tiles_t, shares;
 };
 TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
   TilePlan best{};
   double least = 0;
-  const int64_t blocks = (k / 64 + kBlock - 1) / kBlock;
-  for (int c = 0; c < 2; ++c) {
-    TilePlan p{c, c == 0 ? 192 : 128, c == 0 ? 128 : 64, 0, 0, 1};
-    p.tiles_n = (int)((n + p.rows - 1) / p.rows);
-    p.tiles_t = (int)((t + p.tokens - 1) / p.tokens);
+  const int64_t stages = (k / 64 + 1) / 2;
+  for (int c = 0; c < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++c) {
+    const TileShape& s = kTiles[c];
+    TilePlan p{c, (int)((n + s.rows - 1) / s.rows), (int)((t + s.tokens - 1) / s.tokens), 1};
     const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;
-    for (int shares = 1; shares <= 8 && shares <= blocks; shares *= 2) {
+    for (int shares = 1; shares <= 8 && (shares == 1 || 4 * shares <= stages); shares *= 2) {
       p.shares = shares;
-      const double rounds = (double)((tiles * shares + kCUs - 1) / kCUs);
-      // us: a block of eight groups, start and end of a workgroup, the pass
-      // over the shares' sums
-      const double time = rounds * ((blocks + shares - 1) / shares * (c == 0 ? 3.0 : 1.3) + 5.0) +
-                          (shares > 1 ? 4.0 + (double)shares * n * t * 8 / 4e6 : 0.0);
+      const double length = (double)((stages + shares - 1) / shares);
+      const int64_t all = tiles * shares, full = s.both > 0 ? all / (2 * kCUs) : 0, rest = all - full * 2 * kCUs;
+      const int64_t rounds = (rest + kCUs - 1) / kCUs;
+      // the rest: one workgroup a CU, or (two fit) two on some of them
+      const double last = s.both > 0 ? (rounds == 2 ? s.both : rounds * s.stage) : rounds * s.stage;
+      const double time = length * (full * s.both + last) + (full + (s.both > 0 && rounds > 0 ? 1 : rounds)) * s.ends +
+                          (shares > 1 ? 3.0 + (double)shares * n * t * 8 / 6e6 : 0.0);
       if ((c == 0 && shares == 1) || time < least) {
         least = time;
         best = p;
@@ -521,12 +659,13 @@ hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
   }
   const TilePlan p = tile_plan(a.n, a.k, a.t);
   const dim3 grid((unsigned)(p.tiles_n * p.tiles_t), (unsigned)p.shares);
-  if (p.config == 0) mx8_tile_kernel<2, 2, 3, 2><<<grid, kTileThreads, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
-  else mx8_tile_kernel<2, 2, 2, 1><<<grid, kTileThreads, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  if (p.shape == 0) mx8_tile_kernel<4, 2, 2, 2><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  else if (p.shape == 1) mx8_tile_kernel<2, 4, 3, 1><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  else mx8_tile_kernel<2, 2, 2, 1><<<grid, 256, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.shares == 1) return e;
   const int64_t outputs = a.n * a.t;
-  mx8_join_kernel<<<dim3((unsigned)((outputs + 255) / 256)), 256, 0, stream>>>(k.part, k.res, k.y, outputs, p.shares);
+  mx8_join_kernel<<<dim3((unsigned)((outputs + 1023) / 1024)), 256, 0, stream>>>(k.part, k.res, k.y, outputs, p.shares);
   return hipGetLastError();
 }
 

@@ -337,19 +337,22 @@ int check_workspace(const void* workspace, size_t workspace_bytes, size_t need) 
 
 // LinearLogprobs: runs of `run` tokens whose logits lie in the workspace as
 // binary32, after the bf16 form of all activations where they come in 8 bits.
-// The products are those of a route with exact codes (the many-token route
-// rounds the weights to 11 bits, which would show in a log probability), the
-// most tokens per weight read that such a route takes.
+// The products have exact codes (the many-token route rounds the weights to
+// 11 bits, which would show in a log probability): the few-token stream where
+// it takes all tokens (few; activations in its paired order), else the most
+// tokens per weight read that a route with exact codes takes.
 struct ScorePlan {
+  bool few;
   int64_t run;
   size_t x_bytes, logit_bytes, total;
 };
 constexpr int64_t kMaxScoreK = int64_t(1) << 17;  // (up to there every run of tokens has such a route)
 int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, bool mx8, ScorePlan* p) {
   if (!shape_ok(n, k, t) || !logprobs_shape_ok(n, t, top) || k > kMaxScoreK) return Q4LIN_E_SHAPE;
-  *p = ScorePlan{0, 0, 0, 0};
+  *p = ScorePlan{q4lin::few_bf16_ok(k, t), 0, 0, 0, 0};
   if (t == 0) return Q4LIN_OK;
-  for (int64_t most : {kMidLastT, int64_t(32), int64_t(4), int64_t(1)}) {
+  if (p->few) p->run = t;
+  else for (int64_t most : {kMidLastT, int64_t(32), int64_t(4), int64_t(1)}) {
     const int64_t runs = (t + most - 1) / most, run = (t + runs - 1) / runs;
     // (the last run may be shorter: its route is checked too)
     const int64_t last = t - (t - 1) / run * run;
@@ -358,7 +361,7 @@ int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, bool mx8, ScorePlan
     break;
   }
   if (p->run == 0) return Q4LIN_E_SHAPE;
-  p->x_bytes = mx8 ? al256((size_t)(t * k * 2)) : 0;
+  p->x_bytes = mx8 || p->few ? al256((size_t)(t * k * 2)) : 0;
   p->logit_bytes = al256((size_t)(p->run * n * 4));
   p->total = p->x_bytes + p->logit_bytes + q4lin::logprobs_workspace_bytes(n, p->run, (int)top);
   return Q4LIN_OK;
@@ -860,8 +863,8 @@ int q4lin_linear_logprobs(const void* x, const void* x_scales, const void* codes
   float* const logits = reinterpret_cast<float*>(ws + p.x_bytes);
   hipError_t e = hipSuccess;
   const uint8_t* xb = static_cast<const uint8_t*>(x);
-  if (x_scales) {
-    e = q4lin::launch_mx8_to_bf16(x, x_scales, ws, k, t, s);
+  if (x_scales || p.few) {
+    e = x_scales ? q4lin::launch_mx8_to_bf16(x, x_scales, ws, k, t, p.few, s) : q4lin::launch_pair_bf16(x, ws, k, t, s);
     if (e != hipSuccess) return Q4LIN_E_LAUNCH;
     xb = ws;
   }
@@ -870,7 +873,9 @@ int q4lin_linear_logprobs(const void* x, const void* x_scales, const void* codes
     const int route = pick_route(n, k, c);
     q4lin::GemvArgs a{xb + (size_t)(t0 * k * 2), codes, scales, logits, n, k, c};
     a.f32 = true;
-    if (route == Q4LIN_ROUTE_DECODE || route == Q4LIN_ROUTE_GEMV ||
+    if (p.few)
+      e = q4lin::launch_few_logits(xb, codes, scales, logits, n, k, t, s);
+    else if (route == Q4LIN_ROUTE_DECODE || route == Q4LIN_ROUTE_GEMV ||
         (route == Q4LIN_ROUTE_SKINNY && !small_uses_fmt(n, k, c)))
       e = launch_sums(route, a, s);
     else

@@ -274,8 +274,10 @@ hipError_t launch_rmsnorm_mx8(const void* x, const void* residual, const void* w
                               void* scales, int64_t k, int64_t t, float eps, hipStream_t stream);
 hipError_t launch_quantize_mx8(const void* x, const void* gate, void* values, void* scales, int64_t k, int64_t t,
                                int64_t x_stride, int64_t gate_stride, hipStream_t stream);
-hipError_t launch_mx8_to_bf16(const void* values, const void* scales, void* out, int64_t k, int64_t t,
+hipError_t launch_mx8_to_bf16(const void* values, const void* scales, void* out, int64_t k, int64_t t, bool paired,
                               hipStream_t stream);
+// bf16 in the paired order: of every eight k0 k4 k1 k5 k2 k6 k3 k7
+hipError_t launch_pair_bf16(const void* x, void* out, int64_t k, int64_t t, hipStream_t stream);
 
 // The Q4 product of such activations (q4lin_mx8.hip).
 struct Mx8Args {
@@ -289,6 +291,15 @@ struct Mx8Args {
 };
 size_t mx8_workspace_bytes(int64_t n, int64_t k, int64_t t);
 hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream);
+
+// A few tokens as one stream over the weight (q4lin_few.hip): MXFP8
+// activations, or bf16 ones in the paired order (launch_pair_bf16) with exact
+// codes and binary32 outputs.
+bool few_mx8_ok(int64_t k, int64_t t);
+bool few_bf16_ok(int64_t k, int64_t t);
+hipError_t launch_few_mx8(const Mx8Args& a, hipStream_t stream);
+hipError_t launch_few_logits(const void* x_paired, const void* codes, const void* scales, float* logits, int64_t n,
+                             int64_t k, int64_t t, hipStream_t stream);
 
 // Log probabilities of rows of logits, bf16 or binary32 (q4lin_logprobs.hip).
 struct LogprobsArgs {

@@ -515,7 +515,8 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   constexpr int PER = SLOT / (32 * LD * 4);  // waves of a slot
   static_assert(PER * kSlots >= WAVES, "room");
   float* const mine = reinterpret_cast<float*>(slot_of(wave / PER) + wave % PER * (32 * LD * 4));
-  const bool wide = (a.N & 7) == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.res & 15) == 0 && shares == 1;
+  // (rows of y that begin on 16 bytes; of binary32 sums too)
+  const bool wide = (a.N & 7) == 0 && (shares > 1 || (((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.res & 15) == 0));
   static_for<TT>([&](auto tc) __device__ {
     constexpr int t = decltype(tc)::value;
 #pragma unroll
@@ -531,7 +532,11 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
       const float* const v = mine + tok * LD + c;
       const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(v), hi = *reinterpret_cast<const f32x4_t*>(v + 4);
       const size_t at = (size_t)(t0 + tok0 + tok) * a.N + n0 + row0 + c;
-      if (wide) {
+      if (wide && shares > 1) {
+        float* const to = a.part + (size_t)blockIdx.y * a.T * a.N + at;
+        *reinterpret_cast<f32x4_t*>(to) = lo;
+        *reinterpret_cast<f32x4_t*>(to + 4) = hi;
+      } else if (wide) {
         float s[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = i < 4 ? lo[i] : hi[i - 4];
@@ -591,12 +596,12 @@ constexpr int64_t kStreamTokens = 128;
 // Tile shapes: rows and tokens of a workgroup, the time of a stage (us; alone
 // on its CU, and two workgroups there if so many fit), of a workgroup's start
 // and end.  Measured on 6144 x 5120 at 256 to 2048 tokens and 34816 x 5120 at
-// 1024: 63 / 53 / 69 us at 1024 tokens, 48 / 44 / 33 at 256.
+// 1024: 63 / 53 / 69 us at 1024 tokens, 61 / 49 / 39 at 512, 48 / 49 / 33 at 256.
 struct TileShape {
   int rows, tokens;
   double stage, both, ends;
 };
-constexpr TileShape kTiles[] = {{256, 128, 1.42, 0, 6.0}, {192, 128, 1.17, 0, 6.0}, {128, 64, 0.70, 1.05, 5.0}};
+constexpr TileShape kTiles[] = {{256, 128, 1.42, 0, 6.0}, {192, 128, 1.17, 0, 6.0}, {128, 64, 0.70, 0.84, 5.0}};
 struct TilePlan {
   int shape, tiles_n, tiles_t, shares;
 };
@@ -616,7 +621,7 @@ TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
       // the rest: one workgroup a CU, or (two fit) two on some of them
       const double last = s.both > 0 ? (rounds == 2 ? s.both : rounds * s.stage) : rounds * s.stage;
       const double time = length * (full * s.both + last) + (full + (s.both > 0 && rounds > 0 ? 1 : rounds)) * s.ends +
-                          (shares > 1 ? 3.0 + (double)shares * n * t * 8 / 6e6 : 0.0);
+                          (shares > 1 ? 1.5 + (double)shares * n * t * (n % 8 == 0 ? 2e-6 : 6e-6) : 0.0);
       if ((c == 0 && shares == 1) || time < least) {
         least = time;
         best = p;
@@ -645,6 +650,7 @@ hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
                     static_cast<const uint16_t*>(a.res),   static_cast<uint16_t*>(a.y),
                     static_cast<float*>(workspace),        (int)a.n,
                     (int)a.k,                              (int)a.t};
+  if (few_mx8_ok(a.k, a.t)) return launch_few_mx8(a, stream);
   if (a.t <= kStreamTokens) {
     // rows per workgroup: whole rounds of one workgroup per CU
     const int64_t rounds = (a.n + 64 * kCUs - 1) / (64 * kCUs);

@@ -518,6 +518,8 @@ def _workspace(need, workspace, device):
     """(address, bytes, tensor to keep) of the caller's workspace or a new one of ``need`` bytes."""
     if need < 0:
         raise Q4LinError(-need)
+    if need == 0 and workspace is None:
+        return None, 0, None
     if workspace is None:
         workspace = _torch.empty_strided((need,), (1,), dtype=_torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
@@ -749,7 +751,9 @@ def rmsnorm_mx8(x, weight=None, eps=1e-6, residual=None, h=None, stream=None):
         _on_gpu(place)
         if h is None:
             h = _new((t, k), _torch.bfloat16, device)
-        hp = _checked("h", h, (t, k), "bf16", place)
+            hp = h.data_ptr()
+        else:
+            hp = _checked("h", h, (t, k), "bf16", place)
     elif h is not None:
         raise ValueError("h is written only with a residual")
     _on_gpu(place)
@@ -811,7 +815,9 @@ def linear_mx8(values, x_scales, codes, scales, residual=None, y=None, workspace
     _on_gpu(place)
     if y is None:
         y = _new((t, n), _torch.bfloat16, device)
-    yp = _checked("y", y, (t, n), "bf16", place)
+        yp = y.data_ptr()
+    else:
+        yp = _checked("y", y, (t, n), "bf16", place)
     wp, wb, workspace = _workspace(q4lin_linear_mx8_workspace_bytes(n, k, t), workspace, device)
     st = load().q4lin_linear_mx8(vp, ep, cp, sp, rp, yp, n, k, t, wp, wb, _current(place))
     if st != Q4LIN_OK:

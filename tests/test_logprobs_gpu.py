@@ -140,7 +140,7 @@ def test_offsets_past_32_bits():
     check(q4.logprobs(l, tokens.cuda(), 4), reference(l.cpu(), tokens, 4), l, "far rows")
 
 
-SCORES = [(1000, 512, 1, 5), (3001, 1024, 3, 20), (40000, 256, 7, 8), (2000, 2048, 40, 4), (5003, 320, 128, 2),
+SCORES = [(1000, 512, 1, 5), (1000, 256, 9, 3), (511, 640, 65, 2), (8200, 320, 8, 2), (50, 192, 3, 4), (3001, 1024, 3, 20), (40000, 256, 7, 8), (2000, 2048, 40, 4), (5003, 320, 128, 2),
           (1500, 512, 129, 3), (900, 192, 300, 2), (130, 64, 2, 32), (777, 20480, 6, 3)]
 
 

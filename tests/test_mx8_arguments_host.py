@@ -77,25 +77,23 @@ def test_workspaces():
     assert linear(n=512, k=8192, t=200, ws=None) == q.Q4LIN_E_NULL
     assert linear(n=512, k=8192, t=200, ws=P + 128) == q.Q4LIN_E_ALIGN
     assert logprobs(wb=q.q4lin_logprobs_workspace_bytes(500, 2, 3) - 1) == q.Q4LIN_E_WORKSPACE
-    assert scores(wb=q.q4lin_linear_logprobs_workspace_bytes(96, 128, 2, 3, 1) - 1) == q.Q4LIN_E_WORKSPACE
-    assert q.q4lin_linear_logprobs_workspace_bytes(96, 128, 2, 3, 0) < q.q4lin_linear_logprobs_workspace_bytes(
-        96, 128, 2, 3, 1)
-    assert q.q4lin_linear_logprobs_workspace_bytes(96, 128, 2, 97, 0) == -q.Q4LIN_E_SHAPE
+    assert scores(wb=q.q4lin_linear_logprobs_workspace_bytes(96, 128, 2, 3) - 1) == q.Q4LIN_E_WORKSPACE
+    assert q.q4lin_linear_logprobs_workspace_bytes(96, 128, 2, 97) == -q.Q4LIN_E_SHAPE
     assert q.q4lin_logprobs_workspace_bytes(96, 2, 33) == -q.Q4LIN_E_SHAPE
     assert q.q4lin_linear_mx8_workspace_bytes(96, 100, 2) == -q.Q4LIN_E_SHAPE
 
 
 def test_scoring_holds_a_run_of_tokens_only():
-    """The logits' room does not grow with the prompt."""
-    one = q.q4lin_linear_logprobs_workspace_bytes(100000, 512, 128, 5, 0)
-    assert q.q4lin_linear_logprobs_workspace_bytes(100000, 512, 128 * 64, 5, 0) <= one
+    """The logits' room does not grow with the prompt, only the activations' does."""
+    one = q.q4lin_linear_logprobs_workspace_bytes(100000, 512, 128, 5)
+    assert q.q4lin_linear_logprobs_workspace_bytes(100000, 512, 128 * 64, 5) == one + 2 * 512 * 128 * 63
 
 
 @pytest.mark.parametrize("k", [64, 4096, 20480, 65536, 1 << 17])
 @pytest.mark.parametrize("t", [1, 2, 5, 31, 33, 127, 129, 1000, 1025])
 def test_scoring_takes_every_size(k, t):
-    assert q.q4lin_linear_logprobs_workspace_bytes(1000, k, t, 5, 0) > 0
-    assert q.q4lin_linear_logprobs_workspace_bytes(1000, (1 << 17) + 64, t, 5, 0) == -q.Q4LIN_E_SHAPE
+    assert q.q4lin_linear_logprobs_workspace_bytes(1000, k, t, 5) > 0
+    assert q.q4lin_linear_logprobs_workspace_bytes(1000, (1 << 17) + 64, t, 5) == -q.Q4LIN_E_SHAPE
 
 
 # -- the torch calls ---------------------------------------------------------------

@@ -132,7 +132,7 @@ def _load() -> ctypes.CDLL:
     lib.q4lin_logprobs_workspace_bytes.restype = i64
     lib.q4lin_linear_logprobs.argtypes = [vp] * 9 + [i64] * 4 + [vp, cz, vp]
     lib.q4lin_linear_logprobs.restype = ci
-    lib.q4lin_linear_logprobs_workspace_bytes.argtypes = [i64] * 4 + [ci]
+    lib.q4lin_linear_logprobs_workspace_bytes.argtypes = [i64] * 4
     lib.q4lin_linear_logprobs_workspace_bytes.restype = i64
     return lib
 
@@ -306,8 +306,8 @@ def q4lin_linear_logprobs(x: int, x_scales: int, codes: int, scales: int, tokens
 
 
 @functools.lru_cache(maxsize=4096)
-def q4lin_linear_logprobs_workspace_bytes(n: int, k: int, t: int, top: int, mx8: int) -> int:
-    return int(load().q4lin_linear_logprobs_workspace_bytes(n, k, t, top, mx8))
+def q4lin_linear_logprobs_workspace_bytes(n: int, k: int, t: int, top: int) -> int:
+    return int(load().q4lin_linear_logprobs_workspace_bytes(n, k, t, top))
 
 
 def q4lin_status_string(status: int) -> str:
@@ -878,8 +878,7 @@ def linear_logprobs(x, x_scales, codes, scales, tokens=None, top=0, workspace=No
     cp = _checked("codes", codes, (n, k // 2), "codes", place)
     sp = _checked("scales", scales, (n, k // 64), "fp16", place)
     tp, outs, at = _logprob_outputs(tokens, t, top, place, device)
-    wp, wb, workspace = _workspace(q4lin_linear_logprobs_workspace_bytes(n, k, t, top, 1 if mx8 else 0), workspace,
-                                   device)
+    wp, wb, workspace = _workspace(q4lin_linear_logprobs_workspace_bytes(n, k, t, top), workspace, device)
     st = load().q4lin_linear_logprobs(xp, ep, cp, sp, tp, *at, n, k, t, top, wp, wb, _current(place))
     if st != Q4LIN_OK:
         raise Q4LinError(st)

@@ -336,32 +336,24 @@ int check_workspace(const void* workspace, size_t workspace_bytes, size_t need) 
 }
 
 // LinearLogprobs: runs of `run` tokens whose logits lie in the workspace as
-// binary32, after the bf16 form of all activations where they come in 8 bits.
-// The products have exact codes (the many-token route rounds the weights to
-// 11 bits, which would show in a log probability): the few-token stream where
-// it takes all tokens (few; activations in its paired order), else the most
-// tokens per weight read that a route with exact codes takes.
+// binary32, after all activations in the kernels' order.  The products have
+// exact codes and are exact to binary32: the many-token route of the plain
+// product rounds the weights to 11 bits, the scaled matrix instructions cut
+// small terms of a group, and either would show in a log probability.
+constexpr int64_t kScoreRun = 128;                // tokens (their logits stay in the caches)
+constexpr int64_t kMaxScoreK = int64_t(1) << 17;
 struct ScorePlan {
   bool few;
   int64_t run;
   size_t x_bytes, logit_bytes, total;
 };
-constexpr int64_t kMaxScoreK = int64_t(1) << 17;  // (up to there every run of tokens has such a route)
-int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, bool mx8, ScorePlan* p) {
+int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, ScorePlan* p) {
   if (!shape_ok(n, k, t) || !logprobs_shape_ok(n, t, top) || k > kMaxScoreK) return Q4LIN_E_SHAPE;
   *p = ScorePlan{q4lin::few_bf16_ok(k, t), 0, 0, 0, 0};
   if (t == 0) return Q4LIN_OK;
-  if (p->few) p->run = t;
-  else for (int64_t most : {kMidLastT, int64_t(32), int64_t(4), int64_t(1)}) {
-    const int64_t runs = (t + most - 1) / most, run = (t + runs - 1) / runs;
-    // (the last run may be shorter: its route is checked too)
-    const int64_t last = t - (t - 1) / run * run;
-    if (pick_route(n, k, run) == Q4LIN_ROUTE_TILED || pick_route(n, k, last) == Q4LIN_ROUTE_TILED) continue;
-    p->run = run;
-    break;
-  }
-  if (p->run == 0) return Q4LIN_E_SHAPE;
-  p->x_bytes = mx8 || p->few ? al256((size_t)(t * k * 2)) : 0;
+  const int64_t runs = (t + kScoreRun - 1) / kScoreRun;
+  p->run = (t + runs - 1) / runs;
+  p->x_bytes = al256((size_t)(t * k * 2));
   p->logit_bytes = al256((size_t)(p->run * n * 4));
   p->total = p->x_bytes + p->logit_bytes + q4lin::logprobs_workspace_bytes(n, p->run, (int)top);
   return Q4LIN_OK;
@@ -839,9 +831,9 @@ int q4lin_logprobs(const void* logits, int f32, int64_t stride, const void* toke
   return e == hipSuccess ? Q4LIN_OK : Q4LIN_E_LAUNCH;
 }
 
-int64_t q4lin_linear_logprobs_workspace_bytes(int64_t n, int64_t k, int64_t t, int64_t top, int mx8) {
+int64_t q4lin_linear_logprobs_workspace_bytes(int64_t n, int64_t k, int64_t t, int64_t top) {
   ScorePlan p;
-  const int st = score_plan(n, k, t, top, mx8 != 0, &p);
+  const int st = score_plan(n, k, t, top, &p);
   return st == Q4LIN_OK ? (int64_t)p.total : -(int64_t)st;
 }
 
@@ -850,7 +842,7 @@ int q4lin_linear_logprobs(const void* x, const void* x_scales, const void* codes
                           int64_t n, int64_t k, int64_t t, int64_t top, void* workspace, size_t workspace_bytes,
                           void* stream) {
   ScorePlan p;
-  int st = score_plan(n, k, t, top, x_scales != nullptr, &p);
+  int st = score_plan(n, k, t, top, &p);
   if (st != Q4LIN_OK || t == 0) return st;
   if (!x || !codes || !scales) return Q4LIN_E_NULL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2)) return Q4LIN_E_ALIGN;
@@ -861,25 +853,13 @@ int q4lin_linear_logprobs(const void* x, const void* x_scales, const void* codes
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   float* const logits = reinterpret_cast<float*>(ws + p.x_bytes);
-  hipError_t e = hipSuccess;
-  const uint8_t* xb = static_cast<const uint8_t*>(x);
-  if (x_scales || p.few) {
-    e = x_scales ? q4lin::launch_mx8_to_bf16(x, x_scales, ws, k, t, p.few, s) : q4lin::launch_pair_bf16(x, ws, k, t, s);
-    if (e != hipSuccess) return Q4LIN_E_LAUNCH;
-    xb = ws;
-  }
+  hipError_t e = x_scales ? q4lin::launch_mx8_to_bf16(x, x_scales, ws, k, t, s) : q4lin::launch_pair_bf16(x, ws, k, t, s);
+  if (e != hipSuccess) return Q4LIN_E_LAUNCH;
   for (int64_t t0 = 0; t0 < t; t0 += p.run) {
     const int64_t c = t - t0 < p.run ? t - t0 : p.run;
-    const int route = pick_route(n, k, c);
-    q4lin::GemvArgs a{xb + (size_t)(t0 * k * 2), codes, scales, logits, n, k, c};
-    a.f32 = true;
-    if (p.few)
-      e = q4lin::launch_few_logits(xb, codes, scales, logits, n, k, t, s);
-    else if (route == Q4LIN_ROUTE_DECODE || route == Q4LIN_ROUTE_GEMV ||
-        (route == Q4LIN_ROUTE_SKINNY && !small_uses_fmt(n, k, c)))
-      e = launch_sums(route, a, s);
-    else
-      e = q4lin::launch_fmt(q4_fmt_args(a), s);
+    const uint8_t* const xr = ws + (size_t)(t0 * k * 2);
+    e = p.few ? q4lin::launch_few_logits(xr, codes, scales, logits, n, k, c, s)
+              : q4lin::launch_tile_logits(xr, codes, scales, logits, n, k, c, s);
     if (e != hipSuccess) return Q4LIN_E_LAUNCH;
     auto from = [&](void* base, int64_t each) -> void* {
       return base ? static_cast<uint8_t*>(base) + (size_t)(4 * each * t0) : nullptr;

@@ -15,7 +15,6 @@
 // tokens past T are not scaled or stored (tokens 0..3 and 4..7 are four
 // registers of a lane).
 #include "q4lin_kernels.h"
-#include "q4lin_mfma16.h"
 #include "q4lin_mx8.h"
 
 namespace q4lin {
@@ -27,67 +26,14 @@ using mfma16::make_rsrc;
 using mfma16::rsrc_t;
 using mfma16::wait_lgkm0;
 using mfma16::wait_vm;
-using mx8::v8i_t;
+using mx8::OpBf16;
+using mx8::OpMx8;
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kChunk = 4;  // groups
 
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
-
-// MXFP8 activations: 64 bytes and two scale bytes of a token per group.
-struct OpMx8 {
-  static constexpr int XB = 64;
-  static constexpr bool kScaled = true;
-  // xp: the token's group (pieces permuted by `key`), cp: the row's two pieces
-  template <int J>
-  static __device__ __forceinline__ f32x16_t product(const uint8_t* xrow, int key, const uint8_t* crow, int ckey,
-                                                     int lh, uint32_t e) {
-    const v8i_t v =
-        mx8::value_operand(*reinterpret_cast<const u32x4_t*>(xrow + 16 * ((4 * J + lh) ^ key)),
-                           *reinterpret_cast<const u32x4_t*>(xrow + 16 * ((4 * J + 2 + lh) ^ key)));
-    const v8i_t q = mx8::code_operand(*reinterpret_cast<const u32x2_t*>(crow + 16 * ((2 * J) ^ ckey) + 8 * lh),
-                                      *reinterpret_cast<const u32x2_t*>(crow + 16 * ((2 * J + 1) ^ ckey) + 8 * lh));
-    constexpr int SEL = 2 * (J & 1);
-    return mx8::product<SEL>(v, q, mx8::offset_sums<SEL>(v, e), e);
-  }
-};
-
-// bf16 activations in the codes' order (of every eight: k0 k4 k1 k5 k2 k6 k3
-// k7), codes as the exact bf16 128 + q and their offset from the same
-// instructions on the constant 136.  Lane half h takes k = 32 h + 8 m .. + 7 in
-// instruction m.
-struct OpBf16 {
-  static constexpr int XB = 128;
-  static constexpr bool kScaled = false;
-  typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ f32x16_t mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
-                                                   0, 0, 0);
-  }
-  template <int J>
-  static __device__ __forceinline__ f32x16_t product(const uint8_t* xrow, int key, const uint8_t* crow, int ckey,
-                                                     int lh, uint32_t) {
-    constexpr uint32_t m136 = 0xC308C308u;  // -136, twice
-    const u32x4_t minus = {m136, m136, m136, m136};
-    const u32x4_t c = *reinterpret_cast<const u32x4_t*>(crow + 16 * ((2 * J + lh) ^ ckey));
-    u32x4_t x[4];
-    f32x16_t d = {};
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      x[m] = *reinterpret_cast<const u32x4_t*>(xrow + 16 * ((8 * J + 4 * lh + m) ^ key));
-      d = mfma(x[m], minus, d);
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      u32x4_t q;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = mfma16::and_or(c[m] >> (4 * i), 0x000F000Fu, 0x43004300u);
-      d = mfma(x[m], q, d);
-    }
-    return d;
-  }
-};
 
 struct FewKernel {
   const uint8_t* x;   // OpMx8: E4M3 [T][K]; OpBf16: bf16 [T][K], paired order
@@ -187,8 +133,10 @@ few_kernel(FewKernel a) {
   auto group = [&](auto jc, const uint8_t* slot, const Scales& s) __device__ {
     constexpr int J = decltype(jc)::value;
     const uint32_t e = (uint32_t)(s.x >> (32 * (J >> 1))) >> (8 * lh);
-    const f32x16_t d = OP::template product<J>(slot + wave * SLOT + CSLOT + tok * XROW, tok & 7,
-                                               slot + wave * SLOT + li * (kChunk * 32), li & 7, lh, e);
+    constexpr int SEL = 2 * (J & 1);
+    const typename OP::X v = OP::template load_x<J>(slot + wave * SLOT + CSLOT + tok * XROW, tok & 7, lh);
+    const typename OP::Q q = OP::template load_q<J>(slot + wave * SLOT + li * (kChunk * 32), li & 7, lh);
+    const f32x16_t d = OP::template product<SEL>(v, q, OP::template offset<SEL>(v, e), e);
     const float f = f16_bits_to_f32((uint16_t)(s.w >> (16 * J)));
 #pragma unroll
     for (int i = 0; i < REGS; ++i) {

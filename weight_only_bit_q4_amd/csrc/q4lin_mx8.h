@@ -18,6 +18,7 @@
 #pragma once
 
 #include "q4lin_device.h"
+#include "q4lin_mfma16.h"
 
 namespace q4lin {
 namespace mx8 {
@@ -67,6 +68,86 @@ __device__ __forceinline__ f32x16_t offset_sums(v8i_t x, uint32_t xs) {
   const f32x16_t zero = {};
   return product<SEL>(x, minus8, zero, xs);
 }
+
+// The two kinds of activations a kernel is written for.  A lane's operands of
+// a group from LDS: `x` a token's run of groups, `c` a row's, J the group's
+// number in it, 16-byte pieces permuted by `key`.
+
+// MXFP8: 64 bytes and two scale bytes of a token per group.
+struct OpMx8 {
+  static constexpr int XB = 64;
+  static constexpr bool kScaled = true;
+  typedef v8i_t X;
+  typedef v8i_t Q;
+  template <int J>
+  static __device__ __forceinline__ X load_x(const uint8_t* x, int key, int lh) {
+    return value_operand(*reinterpret_cast<const u32x4_t*>(x + 16 * ((4 * J + lh) ^ key)),
+                         *reinterpret_cast<const u32x4_t*>(x + 16 * ((4 * J + 2 + lh) ^ key)));
+  }
+  template <int J>
+  static __device__ __forceinline__ Q load_q(const uint8_t* c, int key, int lh) {
+    return code_operand(*reinterpret_cast<const u32x2_t*>(c + 8 * lh + 16 * ((2 * J) ^ key)),
+                        *reinterpret_cast<const u32x2_t*>(c + 8 * lh + 16 * ((2 * J + 1) ^ key)));
+  }
+  template <int SEL>
+  static __device__ __forceinline__ f32x16_t offset(const X& x, uint32_t e) {
+    return offset_sums<SEL>(x, e);
+  }
+  template <int SEL>
+  static __device__ __forceinline__ f32x16_t product(const X& x, const Q& q, const f32x16_t& off, uint32_t e) {
+    return mx8::product<SEL>(x, q, off, e);
+  }
+};
+
+// bf16 in the codes' order (of every eight: k0 k4 k1 k5 k2 k6 k3 k7), codes as
+// the exact bf16 128 + q and their offset from the same instructions on the
+// constant 136: sums exact to binary32.  Lane half h takes k = 32 h + 8 m ..
+// + 7 in instruction m.
+struct OpBf16 {
+  static constexpr int XB = 128;
+  static constexpr bool kScaled = false;
+  struct X {
+    u32x4_t v[4];
+  };
+  typedef u32x4_t Q;
+  typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ f32x16_t mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  }
+  template <int J>
+  static __device__ __forceinline__ X load_x(const uint8_t* x, int key, int lh) {
+    X r;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) r.v[m] = *reinterpret_cast<const u32x4_t*>(x + 16 * ((8 * J + 4 * lh + m) ^ key));
+    return r;
+  }
+  template <int J>
+  static __device__ __forceinline__ Q load_q(const uint8_t* c, int key, int lh) {
+    return *reinterpret_cast<const u32x4_t*>(c + 16 * ((2 * J + lh) ^ key));
+  }
+  template <int SEL>
+  static __device__ __forceinline__ f32x16_t offset(const X& x, uint32_t) {
+    constexpr uint32_t m136 = 0xC308C308u;  // -136, twice
+    const u32x4_t minus = {m136, m136, m136, m136};
+    f32x16_t d = {};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) d = mfma(x.v[m], minus, d);
+    return d;
+  }
+  template <int SEL>
+  static __device__ __forceinline__ f32x16_t product(const X& x, const Q& c, const f32x16_t& off, uint32_t) {
+    f32x16_t d = off;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      u32x4_t q;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = mfma16::and_or(c[m] >> (4 * i), 0x000F000Fu, 0x43004300u);
+      d = mfma(x.v[m], q, d);
+    }
+    return d;
+  }
+};
 
 }  // namespace mx8
 }  // namespace q4lin

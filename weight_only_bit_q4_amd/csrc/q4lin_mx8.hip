@@ -15,7 +15,6 @@
 // Tokens are the rows of D and weight rows its columns, so that a lane holds
 // one weight row and its scale is one register.
 #include "q4lin_kernels.h"
-#include "q4lin_mfma16.h"
 #include "q4lin_mx8.h"
 
 namespace q4lin {
@@ -27,6 +26,8 @@ using mfma16::make_rsrc;
 using mfma16::rsrc_t;
 using mfma16::wait_lgkm0;
 using mfma16::wait_vm;
+using mx8::OpBf16;
+using mx8::OpMx8;
 using mx8::v8i_t;
 
 struct Mx8Kernel {
@@ -291,20 +292,25 @@ mx8_stream_kernel(Mx8Kernel a, int BN) {
 // address unit); one barrier per stage.  The scales of kRun groups are read
 // row by row (whole runs of memory), one thread a row or token, and put into
 // LDS by group, where a lane finds its row's without a gather.
-// blockIdx.y: a share of K (binary32 sums to `part`).
+// blockIdx.y: a share of K (binary32 sums to `part`).  OpBf16: bf16 activations
+// in the paired order, binary32 outputs to `part` (the logits of
+// q4lin_linear_logprobs; twice the bytes of an activation, four matrix
+// instructions of 32 clocks a tile instead of one of 64).
 // ---------------------------------------------------------------------------
 constexpr int kRun = 16;   // groups between two loads of scales: eight stages
 constexpr int kSlots = 4;
 
-template <int WR, int WT, int RT, int TT>
+template <class OP, int WR, int WT, int RT, int TT>
 __global__ void __launch_bounds__(64 * WR * WT, 2)
 mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   constexpr int WAVES = WR * WT, ROWS = WR * RT * 32, TOKENS = WT * TT * 32, LINES = ROWS + TOKENS;
-  // a wave's copies of a stage, 16 rows' codes or eight tokens each (the last
-  // may be of no row: it reads nothing)
-  constexpr int NC = (ROWS / 16 + WAVES - 1) / WAVES, NI = TOKENS / 8 / WAVES, LOADS = NC + NI;
-  static_assert(NI * WAVES * 8 == TOKENS, "whole copies");
-  constexpr int CBYTES = NC * WAVES * 1024, XBYTES = TOKENS * 128, SLOT = CBYTES + XBYTES;
+  constexpr bool F32 = !OP::kScaled;                                 // outputs
+  constexpr int XROW = 2 * OP::XB, PPT = XROW / 16, TPC = 64 / PPT;  // bytes of a token in a stage, pieces; tokens of a copy
+  // a wave's copies of a stage, 16 rows' codes or TPC tokens each (the last may
+  // be of no row: it reads nothing)
+  constexpr int NC = (ROWS / 16 + WAVES - 1) / WAVES, NI = TOKENS / TPC / WAVES, LOADS = NC + NI;
+  static_assert(NI * WAVES * TPC == TOKENS, "whole copies");
+  constexpr int CBYTES = NC * WAVES * 1024, XBYTES = TOKENS * XROW, SLOT = CBYTES + XBYTES;
   static_assert(LINES <= 64 * WAVES, "a thread per row and token");
   // (an object per slot: see the kernel above)
   __shared__ __attribute__((aligned(16))) uint8_t l0[SLOT];
@@ -336,11 +342,12 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   const uint32_t crow = (uint32_t)K >> 1;
 
   const rsrc_t rc = make_rsrc(a.codes + (size_t)n0 * crow, (uint32_t)rows * crow);
-  const rsrc_t rx = make_rsrc(a.x + (size_t)t0 * K, (uint32_t)tokens * (uint32_t)K);
+  const uint32_t xrow = (uint32_t)K * (OP::XB / 64);  // bytes of a token
+  const rsrc_t rx = make_rsrc(a.x + (size_t)t0 * xrow, (uint32_t)tokens * xrow);
   auto ckey = [](int r) { return (r >> 1) & 3; };
   auto xkey = [](int r) { return r & 7; };
   uint32_t coff[NC], xoff[NI];
-  int cgroup, xgroup;  // of this lane's pieces
+  int cgroup, xgroup[NI];  // of this lane's pieces
   {
     const int r = lane >> 2, p = (lane & 3) ^ ckey(r);
     cgroup = p >> 1;
@@ -349,12 +356,12 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
       const int row = (j * WAVES + wave) * 16 + r;
       coff[j] = row < rows ? (uint32_t)row * crow + 16u * p : kNowhere;
     }
-    const int t = lane >> 3, xp = (lane & 7) ^ xkey(t);
-    xgroup = xp >> 2;
+    const int t = lane / PPT;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int tok = (j * WAVES + wave) * 8 + t;
-      xoff[j] = tok < tokens ? (uint32_t)tok * (uint32_t)K + 16u * xp : kNowhere;
+      const int tok = (j * WAVES + wave) * TPC + t, xp = (lane % PPT) ^ xkey(tok);
+      xgroup[j] = xp / (OP::XB / 16);
+      xoff[j] = tok < tokens ? (uint32_t)tok * xrow + 16u * xp : kNowhere;
     }
   }
   // Copy j of the stage at group g.  (Every copy is issued, past the share's
@@ -365,10 +372,10 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
     constexpr int I = X ? J : J - NI;
     const rsrc_t r = X ? rx : rc;
     uint8_t* const to = slot + (X ? CBYTES : 0) + (I * WAVES + wave) * 1024;
-    const uint32_t step = X ? 64u : 32u;
+    const uint32_t step = X ? (uint32_t)OP::XB : 32u;
     uint32_t off = X ? xoff[X ? I : 0] : coff[X ? 0 : I];
     if constexpr (decltype(check)::value) {
-      off = g + (X ? xgroup : cgroup) < ge ? off + step * (uint32_t)g : kNowhere;
+      off = g + (X ? xgroup[X ? I : 0] : cgroup) < ge ? off + step * (uint32_t)g : kNowhere;
       dma16(r, off, 0, to);
     } else {
       dma16(r, off, step * (uint32_t)g, to);
@@ -377,11 +384,12 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
 
   // this thread's line of scales (32-bit offsets from the workgroup's first)
   const bool of_rows = tid < ROWS;
-  const uint8_t* const lbase = of_rows ? reinterpret_cast<const uint8_t*>(a.scales + (size_t)n0 * G)
+  const bool has_line = tid < (OP::kScaled ? LINES : ROWS);
+  const uint8_t* const lbase = of_rows || !OP::kScaled ? reinterpret_cast<const uint8_t*>(a.scales + (size_t)n0 * G)
                                        : a.xs + (size_t)t0 * (K >> 5);
   const uint32_t line = (uint32_t)(of_rows ? min(tid, rows - 1) : min(tid - ROWS, tokens - 1)) * 2u * (uint32_t)G;
   auto load_line = [&](Strip<kRun>& s, int g) __device__ {
-    if (tid < LINES) s = load_strip<kRun>(lbase, line, g, ge);
+    if (has_line) s = load_strip<kRun>(lbase, line, g, ge);
   };
   // (half: where the table's half begins, 0 or kRun ROOM; an index that the
   // compiler must compute keeps every access a plain one of this object)
@@ -389,7 +397,7 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   const int place = of_rows ? at32 / RT * (RP * 32) + (tid & 31) * RP + at32 % RT
                             : ROWROOM + tok32 / TT * (TT * 32) + (tid & 31) * TT + tok32 % TT;
   auto put_line = [&](const Strip<kRun>& s, int half) __device__ {
-    if (tid < LINES)
+    if (has_line)
 #pragma unroll
       for (int j = 0; j < kRun; ++j) table[half + j * ROOM + place] = (uint16_t)(s.w[j / 2] >> (16 * (j & 1)));
   };
@@ -405,14 +413,14 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   uint32_t roff[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    roff[r] = (uint32_t)(((wr * RT + r) * 32 + li) * 64 + 8 * lh);
+    roff[r] = (uint32_t)(((wr * RT + r) * 32 + li) * 64);
     asm("" : "+v"(roff[r]));
   }
   // group J of a stage; scales: where its line of the table begins; copies(i):
   // room for a copy beside the i-th of two products
   auto group = [&](auto jc, const uint8_t* slot, int scales, auto&& copies) __device__ {
     constexpr int H = decltype(jc)::value;
-    v8i_t v[TT];
+    typename OP::X v[TT];
     f32x16_t off[TT];
     const uint16_t* const fp = table + scales + (wr * 32 + li) * RP;
     const uint16_t* const ep = table + scales + ROWROOM + (wt * 32 + li) * TT;
@@ -420,24 +428,21 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
     if constexpr (RP == 4) fs = *reinterpret_cast<const u32x2_t*>(fp);
     else if constexpr (RP == 2) fs.x = *reinterpret_cast<const uint32_t*>(fp);
     else fs.x = *fp;
-    const uint32_t e = (TT == 2 ? *reinterpret_cast<const uint32_t*>(ep) : (uint32_t)*ep) >> (8 * lh);
+    uint32_t e = 0;
+    if constexpr (OP::kScaled) e = (TT == 2 ? *reinterpret_cast<const uint32_t*>(ep) : (uint32_t)*ep) >> (8 * lh);
     static_for<TT>([&](auto tc) __device__ {
       constexpr int t = decltype(tc)::value;
-      const uint8_t* p = slot + CBYTES + ((wt * TT + t) * 32 + li) * 128;
-      v[t] = mx8::value_operand(*reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * H + lh) ^ xkey(li))),
-                                *reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * H + 2 + lh) ^ xkey(li))));
-      off[t] = mx8::offset_sums<2 * t>(v[t], e);
+      v[t] = OP::template load_x<H>(slot + CBYTES + ((wt * TT + t) * 32 + li) * XROW, xkey(li), lh);
+      off[t] = OP::template offset<2 * t>(v[t], e);
     });
     copies(Slot<0>{});
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const uint8_t* p = slot + roff[r];
-      const v8i_t q = mx8::code_operand(*reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * H) ^ ckey(li))),
-                                        *reinterpret_cast<const u32x2_t*>(p + 16 * ((2 * H + 1) ^ ckey(li))));
+      const typename OP::Q q = OP::template load_q<H>(slot + roff[r], ckey(li), lh);
       const float f = scale_of(r < 2 ? fs.x : fs.y, r & 1);
       static_for<TT>([&](auto tc) __device__ {
         constexpr int t = decltype(tc)::value;
-        const f32x16_t d = mx8::product<2 * t>(v[t], q, off[t], e);
+        const f32x16_t d = OP::template product<2 * t>(v[t], q, off[t], e);
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[r][t][i] = __builtin_fmaf(f, d[i], acc[r][t][i]);
         // (the sums are needed here: left alone, the compiler moves them past
@@ -516,7 +521,7 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   static_assert(PER * kSlots >= WAVES, "room");
   float* const mine = reinterpret_cast<float*>(slot_of(wave / PER) + wave % PER * (32 * LD * 4));
   // (rows of y that begin on 16 bytes; of binary32 sums too)
-  const bool wide = (a.N & 7) == 0 && (shares > 1 || (((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.res & 15) == 0));
+  const bool wide = (a.N & 7) == 0 && (F32 || shares > 1 || (((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.res & 15) == 0));
   static_for<TT>([&](auto tc) __device__ {
     constexpr int t = decltype(tc)::value;
 #pragma unroll
@@ -532,7 +537,7 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
       const float* const v = mine + tok * LD + c;
       const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(v), hi = *reinterpret_cast<const f32x4_t*>(v + 4);
       const size_t at = (size_t)(t0 + tok0 + tok) * a.N + n0 + row0 + c;
-      if (wide && shares > 1) {
+      if (wide && (F32 || shares > 1)) {
         float* const to = a.part + (size_t)blockIdx.y * a.T * a.N + at;
         *reinterpret_cast<f32x4_t*>(to) = lo;
         *reinterpret_cast<f32x4_t*>(to + 4) = hi;
@@ -557,7 +562,7 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
         for (int i = 0; i < 8; ++i) {
           if (row0 + c + i >= rows) break;
           const float sum = i < 4 ? lo[i] : hi[i - 4];
-          if (shares > 1) a.part[(size_t)blockIdx.y * a.T * a.N + at + i] = sum;
+          if (F32 || shares > 1) a.part[(size_t)blockIdx.y * a.T * a.N + at + i] = sum;
           else a.y[at + i] = finished((double)sum, a.res, at + i);
         }
       }
@@ -665,13 +670,22 @@ hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
   }
   const TilePlan p = tile_plan(a.n, a.k, a.t);
   const dim3 grid((unsigned)(p.tiles_n * p.tiles_t), (unsigned)p.shares);
-  if (p.shape == 0) mx8_tile_kernel<4, 2, 2, 2><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
-  else if (p.shape == 1) mx8_tile_kernel<2, 4, 3, 1><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
-  else mx8_tile_kernel<2, 2, 2, 1><<<grid, 256, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  if (p.shape == 0) mx8_tile_kernel<OpMx8, 4, 2, 2, 2><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  else if (p.shape == 1) mx8_tile_kernel<OpMx8, 2, 4, 3, 1><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  else mx8_tile_kernel<OpMx8, 2, 2, 2, 1><<<grid, 256, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.shares == 1) return e;
   const int64_t outputs = a.n * a.t;
   mx8_join_kernel<<<dim3((unsigned)((outputs + 1023) / 1024)), 256, 0, stream>>>(k.part, k.res, k.y, outputs, p.shares);
+  return hipGetLastError();
+}
+
+hipError_t launch_tile_logits(const void* x_paired, const void* codes, const void* scales, float* logits, int64_t n,
+                              int64_t k, int64_t t, hipStream_t stream) {
+  const Mx8Kernel m{static_cast<const uint8_t*>(x_paired), nullptr, static_cast<const uint8_t*>(codes),
+                    static_cast<const uint16_t*>(scales), nullptr, nullptr, logits, (int)n, (int)k, (int)t};
+  const int tiles_n = (int)((n + 255) / 256), tiles_t = (int)((t + 63) / 64);
+  mx8_tile_kernel<OpBf16, 4, 2, 2, 1><<<dim3((unsigned)(tiles_n * tiles_t)), 512, 0, stream>>>(m, tiles_n, tiles_t, 1);
   return hipGetLastError();
 }
 

@@ -183,16 +183,16 @@ quantize_mx8_kernel(const uint16_t* x, const uint16_t* gate, uint8_t* values, ui
   }
 }
 
-// Eight values as bf16, in their own order or paired: k0 k4 k1 k5 k2 k6 k3 k7.
+// Eight bf16 in the paired order: k0 k4 k1 k5 k2 k6 k3 k7.
 __device__ __forceinline__ u32x4_t paired8(u32x4_t v) {
   return u32x4_t{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
                  __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
 }
 
-// E4M3 values and their scales as bf16: exact (four significant bits and a
+// E4M3 values and their scales as bf16 in that order: exact (four significant bits and a
 // power of two) up to bf16's range.  A thread takes eight values.
 __global__ void __launch_bounds__(256)
-mx8_to_bf16_kernel(const uint8_t* values, const uint8_t* scales, uint16_t* out, int64_t pieces, int paired) {
+mx8_to_bf16_kernel(const uint8_t* values, const uint8_t* scales, uint16_t* out, int64_t pieces) {
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (p >= pieces) return;
   const u32x2_t v = *reinterpret_cast<const u32x2_t*>(values + 8 * p);
@@ -208,8 +208,7 @@ mx8_to_bf16_kernel(const uint8_t* values, const uint8_t* scales, uint16_t* out, 
     e.v[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * scale;
     e.v[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * scale;
   }
-  const u32x4_t b = pack8(e);
-  *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired ? paired8(b) : b;
+  *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(pack8(e));
 }
 
 __global__ void __launch_bounds__(256)
@@ -252,12 +251,11 @@ hipError_t launch_quantize_mx8(const void* x, const void* gate, void* values, vo
   return hipGetLastError();
 }
 
-hipError_t launch_mx8_to_bf16(const void* values, const void* scales, void* out, int64_t k, int64_t t, bool paired,
+hipError_t launch_mx8_to_bf16(const void* values, const void* scales, void* out, int64_t k, int64_t t,
                               hipStream_t stream) {
   const int64_t pieces = t * k / 8;
   mx8_to_bf16_kernel<<<dim3((unsigned)((pieces + 255) / 256)), 256, 0, stream>>>(
-      static_cast<const uint8_t*>(values), static_cast<const uint8_t*>(scales), static_cast<uint16_t*>(out), pieces,
-      paired ? 1 : 0);
+      static_cast<const uint8_t*>(values), static_cast<const uint8_t*>(scales), static_cast<uint16_t*>(out), pieces);
   return hipGetLastError();
 }
 

@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTop = 32;  // alternatives, at most
+constexpr int64_t kEnough = 512, kWorkgroups = 1024;
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ uint32_t order_of(float l) {
@@ -411,15 +412,15 @@ logprobs_join_kernel(const T* logits, int64_t stride, int N, int shares, int top
 }
 
 // Shares of a row: enough workgroups for the chip, each at least one tile.
-// Few rows take small tiles (eight logits a thread), so that one row spreads
-// over many workgroups.
+// Where tiles of 32 logits a thread are too few for that, tiles of eight: one
+// row spreads over many workgroups.
 struct SharePlan {
   int ept, shares, share;
 };
 SharePlan plan(int64_t n, int64_t t) {
-  const int ept = t * n < (int64_t)1024 * 8192 ? 8 : 32;
+  const int ept = t * ((n + 32 * kThreads - 1) / (32 * kThreads)) < kEnough ? 8 : 32;
   const int64_t tile = (int64_t)kThreads * ept, tiles = (n + tile - 1) / tile;
-  int64_t shares = (1024 + t - 1) / t;
+  int64_t shares = (kWorkgroups + t - 1) / t;
   shares = shares < 64 ? shares : 64;
   shares = shares < tiles ? shares : tiles;
   const int64_t per = (tiles + shares - 1) / shares;  // tiles a share

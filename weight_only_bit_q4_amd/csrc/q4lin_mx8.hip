@@ -609,6 +609,7 @@ struct TileShape {
 constexpr TileShape kTiles[] = {{256, 128, 1.42, 0, 6.0}, {192, 128, 1.17, 0, 6.0}, {128, 64, 0.70, 0.84, 5.0}};
 struct TilePlan {
   int shape, tiles_n, tiles_t, shares;
+  double time;
 };
 TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
   TilePlan best{};
@@ -616,7 +617,7 @@ TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
   const int64_t stages = (k / 64 + 1) / 2;
   for (int c = 0; c < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++c) {
     const TileShape& s = kTiles[c];
-    TilePlan p{c, (int)((n + s.rows - 1) / s.rows), (int)((t + s.tokens - 1) / s.tokens), 1};
+    TilePlan p{c, (int)((n + s.rows - 1) / s.rows), (int)((t + s.tokens - 1) / s.tokens), 1, 0.0};
     const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;
     for (int shares = 1; shares <= 8 && (shares == 1 || 4 * shares <= stages); shares *= 2) {
       p.shares = shares;
@@ -630,10 +631,33 @@ TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
       if ((c == 0 && shares == 1) || time < least) {
         least = time;
         best = p;
+        best.time = time;
       }
     }
   }
   return best;
+}
+
+// The kernel for up to kStreamTokens tokens: rows per workgroup (whole rounds
+// of one workgroup per CU, the token ranges' together), and its time in the
+// tiles' terms (us; a group of a wave measured on 6144 x 5120 at 32, 64 and 128
+// tokens).  Tiles take over where its rounds are many: 20000 x 2048 at 100
+// tokens 33 us here, 34816 x 2048 at 50 31.
+struct StreamPlan {
+  int bn, ranges;
+  double time;
+};
+StreamPlan stream_plan(int64_t n, int64_t k, int64_t t) {
+  StreamPlan p{};
+  p.ranges = t <= 64 ? 1 : 2;
+  const int64_t blocks = kCUs / p.ranges, rounds = (n + 64 * blocks - 1) / (64 * blocks);
+  p.bn = (int)((n + blocks * rounds - 1) / (blocks * rounds));
+  const double group = p.bn <= 32 ? (t <= 32 ? 0.65 : 1.08) : (t <= 32 ? 1.1 : 1.87);
+  p.time = (double)rounds * (5.0 + group * (double)((k / 64 + kWaves - 1) / kWaves));
+  return p;
+}
+bool takes_stream(int64_t n, int64_t k, int64_t t) {
+  return t <= kStreamTokens && stream_plan(n, k, t).time <= tile_plan(n, k, t).time;
 }
 
 template <int RT, int TT, int CH, int NX>
@@ -644,7 +668,7 @@ void launch_stream(const Mx8Kernel& k, int bn, int ranges, hipStream_t stream) {
 }  // namespace
 
 size_t mx8_workspace_bytes(int64_t n, int64_t k, int64_t t) {
-  if (t <= kStreamTokens) return 0;
+  if (few_mx8_ok(k, t) || takes_stream(n, k, t)) return 0;
   const TilePlan p = tile_plan(n, k, t);
   return p.shares > 1 ? (size_t)p.shares * n * t * 4 : 0;
 }
@@ -656,16 +680,13 @@ hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
                     static_cast<float*>(workspace),        (int)a.n,
                     (int)a.k,                              (int)a.t};
   if (few_mx8_ok(a.k, a.t)) return launch_few_mx8(a, stream);
-  if (a.t <= kStreamTokens) {
-    // rows per workgroup: whole rounds of one workgroup per CU
-    const int64_t rounds = (a.n + 64 * kCUs - 1) / (64 * kCUs);
-    const int bn = (int)((a.n + kCUs * rounds - 1) / (kCUs * rounds));
-    const int ranges = a.t <= 64 ? 1 : 2;
+  if (takes_stream(a.n, a.k, a.t)) {
+    const StreamPlan p = stream_plan(a.n, a.k, a.t);
     const bool two = a.t > 32;
-    if (bn <= 32 && !two) launch_stream<1, 1, 4, 4>(k, bn, ranges, stream);
-    else if (bn <= 32) launch_stream<1, 2, 4, 2>(k, bn, ranges, stream);
-    else if (!two) launch_stream<2, 1, 2, 2>(k, bn, ranges, stream);
-    else launch_stream<2, 2, 2, 2>(k, bn, ranges, stream);
+    if (p.bn <= 32 && !two) launch_stream<1, 1, 4, 4>(k, p.bn, p.ranges, stream);
+    else if (p.bn <= 32) launch_stream<1, 2, 4, 2>(k, p.bn, p.ranges, stream);
+    else if (!two) launch_stream<2, 1, 2, 2>(k, p.bn, p.ranges, stream);
+    else launch_stream<2, 2, 2, 2>(k, p.bn, p.ranges, stream);
     return hipGetLastError();
   }
   const TilePlan p = tile_plan(a.n, a.k, a.t);

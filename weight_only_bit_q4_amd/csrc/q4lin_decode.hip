@@ -35,6 +35,7 @@
 //   * The eight waves' partials are combined in binary64 and rounded to bf16
 //     once.
 #include "q4lin_device.h"
+#include "q4lin_mx8.h"
 #include "q4lin_kernels.h"
 #include "q4lin_lora_tail.h"
 
@@ -165,11 +166,14 @@ __device__ __forceinline__ float piece_dot_pre(const uint32_t (&c)[16], const u3
 // cost little more than one).
 // WV: waves per workgroup (8, or 12 for long rows); GLU: LinearSwiGLU in one
 // pass (each workgroup takes the same rows of the gate and the up weight).
-// LORA: the low-rank adapters' term joins the final sum.
-template <int PL, int MAXR, int NT, int WV, bool GLU, bool LORA>
+// LORA: the low-rank adapters' term joins the final sum.  MX: x holds E4M3
+// values and xs their scales, one for each of the lane's pieces (32 weights);
+// they become the same bf16 values (exact) once every load is on its way.
+template <int PL, int MAXR, int NT, int WV, bool GLU, bool LORA, bool MX = false>
 __global__ void __launch_bounds__(64 * WV)
 decode_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
-              uint16_t* y, int N, int K, int BN, const uint16_t* res, SecondPlane p2, LoraTail lora) {
+              uint16_t* y, int N, int K, int BN, const uint16_t* res, SecondPlane p2, LoraTail lora,
+              const uint8_t* xs) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int G = K >> 6;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -224,14 +228,27 @@ decode_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ codes,
 
   // 1. the lane's activations (first: waiting for them waits for nothing else)
   u32x4_t xv[NT][PL][4];
+  u32x4_t xm[MX ? NT : 1][PL][2];
+  uint32_t xe[MX ? NT : 1][PL];
+  auto load_mx = [&](int t, int i) __device__ {
+    const int piece = 2 * gl + min(pc0 + i, max(P - 1, 0));
+    const u32x4_t* xp = reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint8_t*>(x) + (size_t)t * K + 32 * piece);
+    xm[t][i][0] = xp[0];
+    xm[t][i][1] = xp[1];
+    xe[t][i] = xs[(size_t)t * (K >> 5) + piece];
+  };
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const u32x4_t* xp =
-          reinterpret_cast<const u32x4_t*>(x + (size_t)t * K + 64 * gl + 32 * min(pc0 + i, max(P - 1, 0)));
+      if constexpr (MX) {
+        load_mx(t, i);
+      } else {
+        const u32x4_t* xp =
+            reinterpret_cast<const u32x4_t*>(x + (size_t)t * K + 64 * gl + 32 * min(pc0 + i, max(P - 1, 0)));
 #pragma unroll
-      for (int d = 0; d < 4; ++d) xv[t][i][d] = xp[d];
+        for (int d = 0; d < 4; ++d) xv[t][i][d] = xp[d];
+      }
     }
   // 2. codes of the lane's rows, in row order (the rows are waited for one by
   //    one below; values of rows past the block and pieces past the slice are
@@ -264,6 +281,11 @@ decode_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ codes,
 
   // 4. activation pairs in the order of the code pairs, and the correction
   //    sums of the all-eight codes through the very same dot chain
+  if constexpr (MX)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < PL; ++i) mx8::to_bf16(xm[t][i], xe[t][i], xv[t][i]);
   u32x4_t xb[NT][PL][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -336,10 +358,15 @@ decode_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ codes,
       if constexpr (WV != 8) {
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-          const u32x4_t* xp =
-              reinterpret_cast<const u32x4_t*>(x + (size_t)t * K + 64 * gl + 32 * min(pc0 + i, max(P - 1, 0)));
+          if constexpr (MX) {
+            load_mx(t, i);
+            mx8::to_bf16(xm[t][i], xe[t][i], xv[t][i]);
+          } else {
+            const u32x4_t* xp =
+                reinterpret_cast<const u32x4_t*>(x + (size_t)t * K + 64 * gl + 32 * min(pc0 + i, max(P - 1, 0)));
 #pragma unroll
-          for (int d = 0; d < 4; ++d) xv[t][i][d] = xp[d];
+            for (int d = 0; d < 4; ++d) xv[t][i][d] = xp[d];
+          }
         }
       }
       uint32_t m = 0;
@@ -500,6 +527,10 @@ hipError_t launch_pm(const DecodePlan& p, const GemvArgs& a, hipStream_t stream)
     if (WV != 8 || a.glu || a.n2 > 0 || a.f32) return hipErrorInvalidValue;
     kern = decode_kernel<PL, MAXR, NT, WV, false, WV == 8>;
   }
+  if (a.xs != nullptr) {  // (one token, one weight, bf16 outputs)
+    if (NT != 1 || a.glu || a.n2 > 0 || a.lora.b != nullptr) return hipErrorInvalidValue;
+    kern = decode_kernel<PL, MAXR, NT, WV, false, false, NT == 1>;
+  }
   const size_t lds = decode_lds(MAXR, NT, WV, p.bn);
   hipError_t e = allow_full_lds(reinterpret_cast<const void*>(kern));
   if (e != hipSuccess) return e;
@@ -509,7 +540,7 @@ hipError_t launch_pm(const DecodePlan& p, const GemvArgs& a, hipStream_t stream)
   kern<<<dim3((unsigned)(blocks1 + blocks2)), dim3(64 * WV), lds, stream>>>(
       static_cast<const uint16_t*>(a.x), static_cast<const uint8_t*>(a.codes), static_cast<const uint16_t*>(a.scales),
       static_cast<uint16_t*>(a.y), (int)a.n, (int)a.k, p.bn, static_cast<const uint16_t*>(a.res),
-      second_plane(a, blocks1), a.lora);
+      second_plane(a, blocks1), a.lora, static_cast<const uint8_t*>(a.xs));
   return hipGetLastError();
 }
 

@@ -41,6 +41,7 @@ struct GemvArgs {
   // rows of both and stores bf16(silu(G) * U) into y
   bool glu = false;
   LoraTail lora = {};  // single-token route (eight waves)
+  const void* xs = nullptr;  // single-token route: x holds E4M3 values, these are their E8M0 scales
 };
 
 // The second plane of a LinearPair as the kernels see it: the workgroups from

@@ -54,6 +54,27 @@ __device__ __forceinline__ v8i_t value_operand(u32x4_t b0, u32x4_t b1) {
   return v;
 }
 
+// E8M0 as binary32: 0 is the subnormal 2^-127, 255 NaN
+__device__ __forceinline__ float scale_value(uint32_t e) {
+  return __builtin_bit_cast(float, e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
+}
+// Four E4M3 values (a dword) in their block's scale as two bf16 pairs: exact
+// (four significant bits and a power of two) up to bf16's range; NaN from
+// either.  (Checked for every value and scale.)
+__device__ __forceinline__ u32x2_t to_bf16x4(uint32_t w, float scale) {
+  return u32x2_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true))};
+}
+// 32 of them, in memory order
+__device__ __forceinline__ void to_bf16(const u32x4_t (&m)[2], uint32_t e, u32x4_t (&out)[4]) {
+  const float scale = scale_value(e);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const u32x2_t a = to_bf16x4(m[d >> 1][2 * (d & 1)], scale), b = to_bf16x4(m[d >> 1][2 * (d & 1) + 1], scale);
+    out[d] = u32x4_t{a.x, a.y, b.x, b.y};
+  }
+}
+
 // D = X Q^T + C: x with the scale byte of its lane in byte SEL of xs, q codes
 template <int SEL>
 __device__ __forceinline__ f32x16_t product(v8i_t x, v8i_t q, f32x16_t c, uint32_t xs) {

@@ -15,6 +15,7 @@
 // stream's alone.  Squares are binary32 per thread, binary64 across lanes.
 #include "q4lin_kernels.h"
 #include "q4lin_device.h"
+#include "q4lin_mx8.h"
 
 namespace q4lin {
 namespace {
@@ -196,19 +197,9 @@ mx8_to_bf16_kernel(const uint8_t* values, const uint8_t* scales, uint16_t* out, 
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (p >= pieces) return;
   const u32x2_t v = *reinterpret_cast<const u32x2_t*>(values + 8 * p);
-  const uint32_t s = scales[p >> 2];
-  // 2^(s - 127): s = 0 is binary32's subnormal 2^-127, 255 is NaN
-  const float scale = __builtin_bit_cast(float, s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
-  Eight e;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int w = (int)(j ? v.y : v.x);
-    e.v[4 * j] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * scale;
-    e.v[4 * j + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * scale;
-    e.v[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * scale;
-    e.v[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * scale;
-  }
-  *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(pack8(e));
+  const float scale = mx8::scale_value(scales[p >> 2]);
+  const u32x2_t a = mx8::to_bf16x4(v.x, scale), b = mx8::to_bf16x4(v.y, scale);
+  *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(u32x4_t{a.x, a.y, b.x, b.y});
 }
 
 __global__ void __launch_bounds__(256)

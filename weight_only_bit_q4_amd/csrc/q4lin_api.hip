@@ -345,17 +345,18 @@ constexpr int64_t kMaxScoreK = int64_t(1) << 17;
 struct ScorePlan {
   bool few;
   int64_t run;
-  size_t x_bytes, logit_bytes, total;
+  size_t x_bytes, offset_bytes, logit_bytes, total;
 };
 int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, ScorePlan* p) {
   if (!shape_ok(n, k, t) || !logprobs_shape_ok(n, t, top) || k > kMaxScoreK) return Q4LIN_E_SHAPE;
-  *p = ScorePlan{q4lin::few_bf16_ok(k, t), 0, 0, 0, 0};
+  *p = ScorePlan{q4lin::few_bf16_ok(k, t), 0, 0, 0, 0, 0};
   if (t == 0) return Q4LIN_OK;
   const int64_t runs = (t + kScoreRun - 1) / kScoreRun;
   p->run = (t + runs - 1) / runs;
   p->x_bytes = al256((size_t)(t * k * 2));
+  p->offset_bytes = al256((size_t)(t * (k / 64) * 4));
   p->logit_bytes = al256((size_t)(p->run * n * 4));
-  p->total = p->x_bytes + p->logit_bytes + q4lin::logprobs_workspace_bytes(n, p->run, (int)top);
+  p->total = p->x_bytes + p->offset_bytes + p->logit_bytes + q4lin::logprobs_workspace_bytes(n, p->run, (int)top);
   return Q4LIN_OK;
 }
 
@@ -852,14 +853,16 @@ int q4lin_linear_logprobs(const void* x, const void* x_scales, const void* codes
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  float* const logits = reinterpret_cast<float*>(ws + p.x_bytes);
-  hipError_t e = x_scales ? q4lin::launch_mx8_to_bf16(x, x_scales, ws, k, t, s) : q4lin::launch_pair_bf16(x, ws, k, t, s);
+  float* const offsets = reinterpret_cast<float*>(ws + p.x_bytes);
+  float* const logits = reinterpret_cast<float*>(ws + p.x_bytes + p.offset_bytes);
+  hipError_t e = q4lin::launch_paired(x, x_scales, ws, offsets, k, t, s);
   if (e != hipSuccess) return Q4LIN_E_LAUNCH;
   for (int64_t t0 = 0; t0 < t; t0 += p.run) {
     const int64_t c = t - t0 < p.run ? t - t0 : p.run;
     const uint8_t* const xr = ws + (size_t)(t0 * k * 2);
-    e = p.few ? q4lin::launch_few_logits(xr, codes, scales, logits, n, k, c, s)
-              : q4lin::launch_tile_logits(xr, codes, scales, logits, n, k, c, s);
+    const float* const offs = offsets + (size_t)(t0 * (k / 64));
+    e = p.few ? q4lin::launch_few_logits(xr, offs, codes, scales, logits, n, k, c, s)
+              : q4lin::launch_tile_logits(xr, offs, codes, scales, logits, n, k, c, s);
     if (e != hipSuccess) return Q4LIN_E_LAUNCH;
     auto from = [&](void* base, int64_t each) -> void* {
       return base ? static_cast<uint8_t*>(base) + (size_t)(4 * each * t0) : nullptr;
@@ -867,7 +870,7 @@ int q4lin_linear_logprobs(const void* x, const void* x_scales, const void* codes
     e = q4lin::launch_logprobs(
         q4lin::LogprobsArgs{logits, true, n, from(const_cast<void*>(tokens), 1), from(logprob, 1), from(entropy, 1),
                             from(top_logprobs, top), from(top_ids, top), n, c, (int)top},
-        ws + p.x_bytes + p.logit_bytes, s);
+        ws + p.x_bytes + p.offset_bytes + p.logit_bytes, s);
     if (e != hipSuccess) return Q4LIN_E_LAUNCH;
   }
   return Q4LIN_OK;

@@ -35,9 +35,13 @@ constexpr int kChunk = 4;  // groups
 
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
+// groups of a wave whose offsets fit the table below (bf16 activations)
+constexpr int kTable = 64;
+
 struct FewKernel {
   const uint8_t* x;   // OpMx8: E4M3 [T][K]; OpBf16: bf16 [T][K], paired order
-  const uint8_t* xs;  // E8M0 [T][K/32]
+  const uint8_t* xs;     // OpMx8: E8M0 [T][K/32]
+  const float* offsets;  // OpBf16: [T][K/64]
   const uint8_t* codes;
   const uint16_t* scales;
   const uint16_t* res;  // bf16 [T][N] or nullptr
@@ -66,6 +70,11 @@ few_kernel(FewKernel a) {
   __shared__ __attribute__((aligned(16))) uint8_t l2[NS > 2 ? kWaves * SLOT : 16];
   constexpr int RED = kWaves * TOK * 32;  // a block's sums of all waves
   __shared__ __attribute__((aligned(16))) float red[2 * RED];  // [wave][row][token]
+  // bf16 activations: the offsets of the codes of each of the wave's groups
+  // (four instructions on the constant 136 in each block took 22 of 110 us at
+  // three tokens on 131072 x 5120); [wave][group][token]
+  constexpr bool TABLE = !OP::kScaled;
+  __shared__ __attribute__((aligned(16))) float table[TABLE ? kWaves * kTable * TOK : 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, lh = lane >> 5;
   const int K = a.K, G = K >> 6;
@@ -130,13 +139,23 @@ few_kernel(FewKernel a) {
 #pragma unroll
   for (int i = 0; i < REGS; ++i) acc[i] = 0.f;
   const int tok = li & (TOK - 1);
-  auto group = [&](auto jc, const uint8_t* slot, const Scales& s) __device__ {
+  // group J of the chunk whose first is `at` of the wave's
+  auto group = [&](auto jc, const uint8_t* slot, const Scales& s, int at) __device__ {
     constexpr int J = decltype(jc)::value;
     const uint32_t e = (uint32_t)(s.x >> (32 * (J >> 1))) >> (8 * lh);
     constexpr int SEL = 2 * (J & 1);
     const typename OP::X v = OP::template load_x<J>(slot + wave * SLOT + CSLOT + tok * XROW, tok & 7, lh);
     const typename OP::Q q = OP::template load_q<J>(slot + wave * SLOT + li * (kChunk * 32), li & 7, lh);
-    const f32x16_t d = OP::template product<SEL>(v, q, OP::template offset<SEL>(v, e), e);
+    f32x16_t d;
+    if constexpr (TABLE) {
+      static_assert(!TABLE || REGS == 4, "one read of a lane's tokens");
+      d = OP::template product<SEL>(v, q, f32x16_t{}, e);
+      const f32x4_t o = *reinterpret_cast<const f32x4_t*>(table + (wave * kTable + at + J) * TOK + (TOK > 4 ? 4 * lh : 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] += o[i];
+    } else {
+      d = OP::template product<SEL>(v, q, OP::template offset<SEL>(v, e), e);
+    }
     const float f = f16_bits_to_f32((uint16_t)(s.w >> (16 * J)));
 #pragma unroll
     for (int i = 0; i < REGS; ++i) {
@@ -191,6 +210,12 @@ few_kernel(FewKernel a) {
     issue(slot_of(S), sc[S], ib, ic);
     advance(ib, ic);
   });
+  if constexpr (TABLE) {
+    for (int i = lane; i < cnt * TOK; i += 64)
+      table[wave * kTable * TOK + i] = a.offsets[(size_t)min(i & (TOK - 1), a.T - 1) * G + gb + i / TOK];
+    wait_lgkm0();
+    in_order();
+  }
   int pb = blockIdx.x, pc = 0;
   // A chunk.  (Past the last one the turn of the loop goes on with copies of
   // nothing: an exit between the slots would make the compiler count the
@@ -208,10 +233,10 @@ few_kernel(FewKernel a) {
     }
     const int n = pb < a.blocks ? cnt - pc * kChunk : 0;
     if (n >= kChunk)
-      static_for<kChunk>([&](auto j) __device__ { group(j, slot_of(S), s); });
+      static_for<kChunk>([&](auto j) __device__ { group(j, slot_of(S), s, pc * kChunk); });
     else
       static_for<kChunk - 1>([&](auto j) __device__ {
-        if (decltype(j)::value < n) group(j, slot_of(S), s);
+        if (decltype(j)::value < n) group(j, slot_of(S), s, pc * kChunk);
       });
     wait_lgkm0();
     issue(slot_of(S), sc[S], ib, ic);
@@ -239,18 +264,20 @@ hipError_t launch(FewKernel k, hipStream_t stream) {
 }  // namespace
 
 bool few_mx8_ok(int64_t k, int64_t t) { return t >= 1 && t <= 16 && k >= 64 * kChunk; }
-bool few_bf16_ok(int64_t k, int64_t t) { return t >= 1 && t <= 8 && k >= 64 * kChunk; }
+bool few_bf16_ok(int64_t k, int64_t t) {
+  return t >= 1 && t <= 8 && k >= 64 * kChunk && k <= 64 * kTable * kWaves;
+}
 
 hipError_t launch_few_mx8(const Mx8Args& a, hipStream_t stream) {
-  const FewKernel k{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.xs),
+  const FewKernel k{static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.xs), nullptr,
                     static_cast<const uint8_t*>(a.codes), static_cast<const uint16_t*>(a.scales),
                     static_cast<const uint16_t*>(a.res), a.y, (int)a.n, (int)a.k, (int)a.t, 0, 0};
   return a.t <= 8 ? launch<OpMx8, 8, 3, false>(k, stream) : launch<OpMx8, 16, 2, false>(k, stream);
 }
 
-hipError_t launch_few_logits(const void* x_paired, const void* codes, const void* scales, float* logits, int64_t n,
-                             int64_t k, int64_t t, hipStream_t stream) {
-  const FewKernel f{static_cast<const uint8_t*>(x_paired), nullptr, static_cast<const uint8_t*>(codes),
+hipError_t launch_few_logits(const void* x_paired, const float* offsets, const void* codes, const void* scales,
+                             float* logits, int64_t n, int64_t k, int64_t t, hipStream_t stream) {
+  const FewKernel f{static_cast<const uint8_t*>(x_paired), nullptr, offsets, static_cast<const uint8_t*>(codes),
                     static_cast<const uint16_t*>(scales), nullptr, logits, (int)n, (int)k, (int)t, 0, 0};
   return t <= 4 ? launch<OpBf16, 4, 3, true>(f, stream) : launch<OpBf16, 8, 2, true>(f, stream);
 }

@@ -275,9 +275,9 @@ hipError_t launch_rmsnorm_mx8(const void* x, const void* residual, const void* w
                               void* scales, int64_t k, int64_t t, float eps, hipStream_t stream);
 hipError_t launch_quantize_mx8(const void* x, const void* gate, void* values, void* scales, int64_t k, int64_t t,
                                int64_t x_stride, int64_t gate_stride, hipStream_t stream);
-hipError_t launch_mx8_to_bf16(const void* values, const void* scales, void* out, int64_t k, int64_t t,
-                              hipStream_t stream);
-hipError_t launch_pair_bf16(const void* x, void* out, int64_t k, int64_t t, hipStream_t stream);
+// scales nullptr: x is bf16
+hipError_t launch_paired(const void* x, const void* scales, void* out, float* offsets, int64_t k, int64_t t,
+                         hipStream_t stream);
 
 // The Q4 product of such activations (q4lin_mx8.hip).
 struct Mx8Args {
@@ -293,17 +293,16 @@ size_t mx8_workspace_bytes(int64_t n, int64_t k, int64_t t);
 hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream);
 
 // A few tokens as one stream over the weight (q4lin_few.hip): MXFP8
-// activations, or bf16 ones in the paired order (launch_pair_bf16) with exact
-// codes and binary32 outputs.
+// activations, or those of launch_paired with exact codes and binary32 outputs.
 bool few_mx8_ok(int64_t k, int64_t t);
 bool few_bf16_ok(int64_t k, int64_t t);
 hipError_t launch_few_mx8(const Mx8Args& a, hipStream_t stream);
-hipError_t launch_few_logits(const void* x_paired, const void* codes, const void* scales, float* logits, int64_t n,
-                             int64_t k, int64_t t, hipStream_t stream);
+hipError_t launch_few_logits(const void* x_paired, const float* offsets, const void* codes, const void* scales,
+                             float* logits, int64_t n, int64_t k, int64_t t, hipStream_t stream);
 
 // The same on tiles of 256 rows x 64 tokens, any T (q4lin_mx8.hip).
-hipError_t launch_tile_logits(const void* x_paired, const void* codes, const void* scales, float* logits, int64_t n,
-                              int64_t k, int64_t t, hipStream_t stream);
+hipError_t launch_tile_logits(const void* x_paired, const float* offsets, const void* codes, const void* scales,
+                              float* logits, int64_t n, int64_t k, int64_t t, hipStream_t stream);
 
 // Log probabilities of rows of logits, bf16 or binary32 (q4lin_logprobs.hip).
 struct LogprobsArgs {

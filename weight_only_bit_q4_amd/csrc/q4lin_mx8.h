@@ -121,9 +121,9 @@ struct OpMx8 {
 };
 
 // bf16 in the codes' order (of every eight: k0 k4 k1 k5 k2 k6 k3 k7), codes as
-// the exact bf16 128 + q and their offset from the same instructions on the
-// constant 136: sums exact to binary32.  Lane half h takes k = 32 h + 8 m ..
-// + 7 in instruction m.
+// the exact bf16 128 + q; the offsets of the codes come with the activations.
+// Sums exact to binary32.  Lane half h takes k = 32 h + 8 m .. + 7 in
+// instruction m.
 struct OpBf16 {
   static constexpr int XB = 128;
   static constexpr bool kScaled = false;
@@ -146,15 +146,6 @@ struct OpBf16 {
   template <int J>
   static __device__ __forceinline__ Q load_q(const uint8_t* c, int key, int lh) {
     return *reinterpret_cast<const u32x4_t*>(c + 16 * ((2 * J + lh) ^ key));
-  }
-  template <int SEL>
-  static __device__ __forceinline__ f32x16_t offset(const X& x, uint32_t) {
-    constexpr uint32_t m136 = 0xC308C308u;  // -136, twice
-    const u32x4_t minus = {m136, m136, m136, m136};
-    f32x16_t d = {};
-#pragma unroll
-    for (int m = 0; m < 4; ++m) d = mfma(x.v[m], minus, d);
-    return d;
   }
   template <int SEL>
   static __device__ __forceinline__ f32x16_t product(const X& x, const Q& c, const f32x16_t& off, uint32_t) {

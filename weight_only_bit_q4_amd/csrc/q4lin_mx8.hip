@@ -37,8 +37,9 @@ struct Mx8Kernel {
   const uint16_t* scales;
   const uint16_t* res;  // nullptr: none
   uint16_t* y;
-  float* part;  // K split: binary32 sums [share][T][N]
+  float* part;  // K split: binary32 sums [share][T][N]; OpBf16: the outputs
   int N, K, T;
+  const float* offsets;  // OpBf16: [T][K/64]
 };
 
 // Two bytes per group (a weight row's fp16 scales, a token's two block
@@ -293,9 +294,10 @@ mx8_stream_kernel(Mx8Kernel a, int BN) {
 // row by row (whole runs of memory), one thread a row or token, and put into
 // LDS by group, where a lane finds its row's without a gather.
 // blockIdx.y: a share of K (binary32 sums to `part`).  OpBf16: bf16 activations
-// in the paired order, binary32 outputs to `part` (the logits of
-// q4lin_linear_logprobs; twice the bytes of an activation, four matrix
-// instructions of 32 clocks a tile instead of one of 64).
+// in the paired order with the offsets of their groups, binary32 outputs to
+// `part` (the logits of q4lin_linear_logprobs; twice the bytes of an
+// activation, four matrix instructions of 32 clocks a tile instead of one of
+// 64, none for the offsets).
 // ---------------------------------------------------------------------------
 constexpr int kRun = 16;   // groups between two loads of scales: eight stages
 constexpr int kSlots = 4;
@@ -321,6 +323,8 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   // a lane's rows (tokens), 32 apart, beside each other
   constexpr int RP = RT == 3 ? 4 : RT, ROWROOM = WR * RP * 32, ROOM = ROWROOM + TOKENS;
   static_assert(RT <= 4 && TT <= 2, "one read of a lane's scales");
+  // OpBf16: the tokens' offsets by group
+  __shared__ __attribute__((aligned(16))) float offs[OP::kScaled ? 4 : 2 * kRun * TOKENS];
   __shared__ __attribute__((aligned(8))) uint16_t table[2 * kRun * ROOM];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, lh = lane >> 5;
@@ -384,11 +388,24 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
 
   // this thread's line of scales (32-bit offsets from the workgroup's first)
   const bool of_rows = tid < ROWS;
-  const bool has_line = tid < (OP::kScaled ? LINES : ROWS);
+  const bool has_line = tid < (OP::kScaled ? LINES : ROWS), of_offsets = !OP::kScaled && !of_rows && tid < LINES;
+  const float* const obase = OP::kScaled ? nullptr : a.offsets + (size_t)(t0 + min(max(tid - ROWS, 0), tokens - 1)) * G;
   const uint8_t* const lbase = of_rows || !OP::kScaled ? reinterpret_cast<const uint8_t*>(a.scales + (size_t)n0 * G)
                                        : a.xs + (size_t)t0 * (K >> 5);
   const uint32_t line = (uint32_t)(of_rows ? min(tid, rows - 1) : min(tid - ROWS, tokens - 1)) * 2u * (uint32_t)G;
+  f32x4_t strip_offs[OP::kScaled ? 1 : kRun / 4];
   auto load_line = [&](Strip<kRun>& s, int g) __device__ {
+    if constexpr (!OP::kScaled)
+      if (of_offsets)
+#pragma unroll
+        for (int j = 0; j < kRun; j += 4) {
+          if (g + j + 4 <= ge) {
+            __builtin_memcpy(&strip_offs[j / 4], obase + g + j, 16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) strip_offs[j / 4][i] = g + j + i < ge ? obase[g + j + i] : 0.f;
+          }
+        }
     if (has_line) s = load_strip<kRun>(lbase, line, g, ge);
   };
   // (half: where the table's half begins, 0 or kRun ROOM; an index that the
@@ -397,6 +414,11 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
   const int place = of_rows ? at32 / RT * (RP * 32) + (tid & 31) * RP + at32 % RT
                             : ROWROOM + tok32 / TT * (TT * 32) + (tid & 31) * TT + tok32 % TT;
   auto put_line = [&](const Strip<kRun>& s, int half) __device__ {
+    if constexpr (!OP::kScaled)
+      if (of_offsets)
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+          offs[(half != 0 ? kRun * TOKENS : 0) + j * TOKENS + tid - ROWS] = strip_offs[j / 4][j % 4];
     if (has_line)
 #pragma unroll
       for (int j = 0; j < kRun; ++j) table[half + j * ROOM + place] = (uint16_t)(s.w[j / 2] >> (16 * (j & 1)));
@@ -433,7 +455,17 @@ mx8_tile_kernel(Mx8Kernel a, int tiles_n, int tiles_t, int shares) {
     static_for<TT>([&](auto tc) __device__ {
       constexpr int t = decltype(tc)::value;
       v[t] = OP::template load_x<H>(slot + CBYTES + ((wt * TT + t) * 32 + li) * XROW, xkey(li), lh);
-      off[t] = OP::template offset<2 * t>(v[t], e);
+      if constexpr (OP::kScaled) {
+        off[t] = OP::template offset<2 * t>(v[t], e);
+      } else {
+        const float* const o = offs + scales / ROOM * TOKENS + (wt * TT + t) * 32 + 4 * lh;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4_t four = *reinterpret_cast<const f32x4_t*>(o + 8 * i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) off[t][4 * i + j] = four[j];
+        }
+      }
     });
     copies(Slot<0>{});
 #pragma unroll
@@ -686,7 +718,8 @@ hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
                     static_cast<const uint8_t*>(a.codes),  static_cast<const uint16_t*>(a.scales),
                     static_cast<const uint16_t*>(a.res),   static_cast<uint16_t*>(a.y),
                     static_cast<float*>(workspace),        (int)a.n,
-                    (int)a.k,                              (int)a.t};
+                    (int)a.k,                              (int)a.t,
+                    nullptr};
   if (decode_takes(a.n, a.k, a.t)) {
     GemvArgs g{a.x, a.codes, a.scales, a.y, a.n, a.k, a.t, a.res};
     g.xs = a.xs;
@@ -714,10 +747,10 @@ hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_tile_logits(const void* x_paired, const void* codes, const void* scales, float* logits, int64_t n,
-                              int64_t k, int64_t t, hipStream_t stream) {
+hipError_t launch_tile_logits(const void* x_paired, const float* offsets, const void* codes, const void* scales,
+                              float* logits, int64_t n, int64_t k, int64_t t, hipStream_t stream) {
   const Mx8Kernel m{static_cast<const uint8_t*>(x_paired), nullptr, static_cast<const uint8_t*>(codes),
-                    static_cast<const uint16_t*>(scales), nullptr, nullptr, logits, (int)n, (int)k, (int)t};
+                    static_cast<const uint16_t*>(scales), nullptr, nullptr, logits, (int)n, (int)k, (int)t, offsets};
   const int tiles_n = (int)((n + 255) / 256), tiles_t = (int)((t + 63) / 64);
   mx8_tile_kernel<OpBf16, 4, 2, 2, 1><<<dim3((unsigned)(tiles_n * tiles_t)), 512, 0, stream>>>(m, tiles_n, tiles_t, 1);
   return hipGetLastError();

@@ -190,22 +190,32 @@ __device__ __forceinline__ u32x4_t paired8(u32x4_t v) {
                  __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
 }
 
-// E4M3 values and their scales as bf16 in that order: exact (four significant bits and a
-// power of two) up to bf16's range.  A thread takes eight values.
+// The activations of the exact products: bf16 in that order, and of each group
+// the offset of its codes, -136 times the sum (binary64, rounded once).  A
+// thread takes eight values, eight threads a group; MX: from E4M3 values and
+// their scales, exact (four significant bits and a power of two) up to bf16's
+// range.
+template <bool MX>
 __global__ void __launch_bounds__(256)
-mx8_to_bf16_kernel(const uint8_t* values, const uint8_t* scales, uint16_t* out, int64_t pieces) {
+paired_kernel(const void* x, const uint8_t* scales, uint16_t* out, float* offsets, int64_t pieces) {
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (p >= pieces) return;
-  const u32x2_t v = *reinterpret_cast<const u32x2_t*>(values + 8 * p);
-  const float scale = mx8::scale_value(scales[p >> 2]);
-  const u32x2_t a = mx8::to_bf16x4(v.x, scale), b = mx8::to_bf16x4(v.y, scale);
-  *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(u32x4_t{a.x, a.y, b.x, b.y});
-}
-
-__global__ void __launch_bounds__(256)
-pair_bf16_kernel(const uint16_t* x, uint16_t* out, int64_t pieces) {
-  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (p < pieces) *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(load16(x + 8 * p));
+  if (p >= pieces) return;  // (whole groups: pieces is a multiple of eight)
+  u32x4_t v;
+  if constexpr (MX) {
+    const u32x2_t m = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(x) + 8 * p);
+    const float scale = mx8::scale_value(scales[p >> 2]);
+    const u32x2_t a = mx8::to_bf16x4(m.x, scale), b = mx8::to_bf16x4(m.y, scale);
+    v = u32x4_t{a.x, a.y, b.x, b.y};
+  } else {
+    v = load16(static_cast<const uint16_t*>(x) + 8 * p);
+  }
+  const Eight e = unpack8(v);
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += (double)e.v[i];
+  sum = sum8_lanes(sum);
+  *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(v);
+  if ((p & 7) == 0) offsets[p >> 3] = (float)(-136.0 * sum);
 }
 
 }  // namespace
@@ -242,18 +252,15 @@ hipError_t launch_quantize_mx8(const void* x, const void* gate, void* values, vo
   return hipGetLastError();
 }
 
-hipError_t launch_mx8_to_bf16(const void* values, const void* scales, void* out, int64_t k, int64_t t,
-                              hipStream_t stream) {
+hipError_t launch_paired(const void* x, const void* scales, void* out, float* offsets, int64_t k, int64_t t,
+                         hipStream_t stream) {
   const int64_t pieces = t * k / 8;
-  mx8_to_bf16_kernel<<<dim3((unsigned)((pieces + 255) / 256)), 256, 0, stream>>>(
-      static_cast<const uint8_t*>(values), static_cast<const uint8_t*>(scales), static_cast<uint16_t*>(out), pieces);
-  return hipGetLastError();
-}
-
-hipError_t launch_pair_bf16(const void* x, void* out, int64_t k, int64_t t, hipStream_t stream) {
-  const int64_t pieces = t * k / 8;
-  pair_bf16_kernel<<<dim3((unsigned)((pieces + 255) / 256)), 256, 0, stream>>>(static_cast<const uint16_t*>(x),
-                                                                               static_cast<uint16_t*>(out), pieces);
+  const dim3 grid((unsigned)((pieces + 255) / 256));
+  uint16_t* const o = static_cast<uint16_t*>(out);
+  if (scales != nullptr)
+    paired_kernel<true><<<grid, 256, 0, stream>>>(x, static_cast<const uint8_t*>(scales), o, offsets, pieces);
+  else
+    paired_kernel<false><<<grid, 256, 0, stream>>>(x, nullptr, o, offsets, pieces);
   return hipGetLastError();
 }
 

@@ -633,38 +633,38 @@ constexpr int64_t kStreamTokens = 128;
 // Tile shapes: rows and tokens of a workgroup, the time of a stage (us; alone
 // on its CU, and two workgroups there if so many fit), of a workgroup's start
 // and end.  Measured on 6144 x 5120 at 256 to 2048 tokens and 34816 x 5120 at
-// 1024: 63 / 53 / 69 us at 1024 tokens, 61 / 49 / 39 at 512, 48 / 49 / 33 at 256.
+// 1024: 63 / 53 / 69 us at 1024 tokens, 61 / 49 / 39 at 512, 48 / 49 / 33 at
+// 256; the shape for up to 32 tokens on 5120 x 17408 and 10240 x 8704 (at 23
+// tokens 27 us streamed, 22 and 21 in six shares).
 struct TileShape {
   int rows, tokens;
   double stage, both, ends;
 };
-constexpr TileShape kTiles[] = {{256, 128, 1.42, 0, 6.0}, {192, 128, 1.17, 0, 6.0}, {128, 64, 0.70, 0.84, 5.0}};
+constexpr TileShape kTiles[] = {{256, 128, 1.42, 0, 6.0}, {192, 128, 1.17, 0, 6.0}, {128, 64, 0.70, 0.84, 5.0},
+                                {128, 32, 0.60, 1.1, 5.0}};
 struct TilePlan {
   int shape, tiles_n, tiles_t, shares;
   double time;
 };
 TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
   TilePlan best{};
-  double least = 0;
+  best.time = -1.0;
   const int64_t stages = (k / 64 + 1) / 2;
-  for (int c = 0; c < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++c) {
+  const int first = t <= 32 ? 3 : t <= 64 ? 2 : 0, last_shape = t <= 32 ? 3 : 2;
+  for (int c = first; c <= last_shape; ++c) {
     const TileShape& s = kTiles[c];
-    TilePlan p{c, (int)((n + s.rows - 1) / s.rows), (int)((t + s.tokens - 1) / s.tokens), 1, 0.0};
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;
-    for (int shares = 1; shares <= 8 && (shares == 1 || 4 * shares <= stages); shares *= 2) {
-      p.shares = shares;
+    const int64_t tiles_n = (n + s.rows - 1) / s.rows, tiles_t = (t + s.tokens - 1) / s.tokens, tiles = tiles_n * tiles_t;
+    for (int shares = 1; shares <= 8 && (shares == 1 || (4 * shares <= stages && tiles * shares <= 4 * kCUs)); ++shares) {
       const double length = (double)((stages + shares - 1) / shares);
       const int64_t all = tiles * shares, full = s.both > 0 ? all / (2 * kCUs) : 0, rest = all - full * 2 * kCUs;
       const int64_t rounds = (rest + kCUs - 1) / kCUs;
-      // the rest: one workgroup a CU, or (two fit) two on some of them
-      const double last = s.both > 0 ? (rounds == 2 ? s.both : rounds * s.stage) : rounds * s.stage;
-      const double time = length * (full * s.both + last) + (full + (s.both > 0 && rounds > 0 ? 1 : rounds)) * s.ends +
-                          (shares > 1 ? 1.5 + (double)shares * n * t * (n % 8 == 0 ? 2e-6 : 6e-6) : 0.0);
-      if ((c == 0 && shares == 1) || time < least) {
-        least = time;
-        best = p;
-        best.time = time;
-      }
+      // the rest: one workgroup a CU, or (two fit) two on some of them, where
+      // HBM limits them if the weight is read once (1.1 us for 512 x 8 KiB)
+      const double both = s.both < 1.1 / tiles_t ? 1.1 / tiles_t : s.both;
+      const double last = s.both > 0 && rounds == 2 ? both : rounds * s.stage;
+      const double time = length * (full * both + last) + (full + (s.both > 0 && rounds > 0 ? 1 : rounds)) * s.ends +
+                          (shares > 1 ? 3.0 + (double)shares * n * t * (n % 8 == 0 ? 2e-6 : 6e-6) : 0.0);
+      if (best.time < 0.0 || time < best.time) best = TilePlan{c, (int)tiles_n, (int)tiles_t, shares, time};
     }
   }
   return best;
@@ -673,7 +673,8 @@ TilePlan tile_plan(int64_t n, int64_t k, int64_t t) {
 // The kernel for up to kStreamTokens tokens: rows per workgroup (whole rounds
 // of one workgroup per CU, the token ranges' together), and its time in the
 // tiles' terms (us; a group of a wave measured on 6144 x 5120 at 32, 64 and 128
-// tokens).  Tiles take over where its rounds are many: 20000 x 2048 at 100
+// tokens, past 32 rows on 12288 x 2048 and 16384 x 5120: at 23 tokens 9 and 22
+// us, in tiles 12 and 19).  Tiles take over where its rounds are many: 20000 x 2048 at 100
 // tokens 33 us here, 34816 x 2048 at 50 31.
 struct StreamPlan {
   int bn, ranges;
@@ -684,12 +685,12 @@ StreamPlan stream_plan(int64_t n, int64_t k, int64_t t) {
   p.ranges = t <= 64 ? 1 : 2;
   const int64_t blocks = kCUs / p.ranges, rounds = (n + 64 * blocks - 1) / (64 * blocks);
   p.bn = (int)((n + blocks * rounds - 1) / (blocks * rounds));
-  const double group = p.bn <= 32 ? (t <= 32 ? 0.65 : 1.08) : (t <= 32 ? 1.1 : 1.87);
+  const double group = p.bn <= 32 ? (t <= 32 ? 0.65 : 1.08) : (t <= 32 ? 1.7 : 2.2);
   p.time = (double)rounds * (5.0 + group * (double)((k / 64 + kWaves - 1) / kWaves));
   return p;
 }
-bool takes_stream(int64_t n, int64_t k, int64_t t) {
-  return t <= kStreamTokens && stream_plan(n, k, t).time <= tile_plan(n, k, t).time;
+bool takes_stream(int64_t n, int64_t k, int64_t t, const TilePlan& tiles) {
+  return t <= kStreamTokens && stream_plan(n, k, t).time <= tiles.time;
 }
 
 template <int RT, int TT, int CH, int NX>
@@ -708,9 +709,9 @@ bool decode_takes(int64_t n, int64_t k, int64_t t) {
 }  // namespace
 
 size_t mx8_workspace_bytes(int64_t n, int64_t k, int64_t t) {
-  if (decode_takes(n, k, t) || few_mx8_ok(k, t) || takes_stream(n, k, t)) return 0;
+  if (decode_takes(n, k, t) || few_mx8_ok(k, t)) return 0;
   const TilePlan p = tile_plan(n, k, t);
-  return p.shares > 1 ? (size_t)p.shares * n * t * 4 : 0;
+  return p.shares > 1 && !takes_stream(n, k, t, p) ? (size_t)p.shares * n * t * 4 : 0;
 }
 
 hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
@@ -726,20 +727,21 @@ hipError_t launch_mx8(const Mx8Args& a, void* workspace, hipStream_t stream) {
     return launch_decode(g, stream);
   }
   if (few_mx8_ok(a.k, a.t)) return launch_few_mx8(a, stream);
-  if (takes_stream(a.n, a.k, a.t)) {
-    const StreamPlan p = stream_plan(a.n, a.k, a.t);
+  const TilePlan p = tile_plan(a.n, a.k, a.t);
+  if (takes_stream(a.n, a.k, a.t, p)) {
+    const StreamPlan f = stream_plan(a.n, a.k, a.t);
     const bool two = a.t > 32;
-    if (p.bn <= 32 && !two) launch_stream<1, 1, 4, 4>(k, p.bn, p.ranges, stream);
-    else if (p.bn <= 32) launch_stream<1, 2, 4, 2>(k, p.bn, p.ranges, stream);
-    else if (!two) launch_stream<2, 1, 2, 2>(k, p.bn, p.ranges, stream);
-    else launch_stream<2, 2, 2, 2>(k, p.bn, p.ranges, stream);
+    if (f.bn <= 32 && !two) launch_stream<1, 1, 4, 4>(k, f.bn, f.ranges, stream);
+    else if (f.bn <= 32) launch_stream<1, 2, 4, 2>(k, f.bn, f.ranges, stream);
+    else if (!two) launch_stream<2, 1, 2, 2>(k, f.bn, f.ranges, stream);
+    else launch_stream<2, 2, 2, 2>(k, f.bn, f.ranges, stream);
     return hipGetLastError();
   }
-  const TilePlan p = tile_plan(a.n, a.k, a.t);
   const dim3 grid((unsigned)(p.tiles_n * p.tiles_t), (unsigned)p.shares);
   if (p.shape == 0) mx8_tile_kernel<OpMx8, 4, 2, 2, 2><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
   else if (p.shape == 1) mx8_tile_kernel<OpMx8, 2, 4, 3, 1><<<grid, 512, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
-  else mx8_tile_kernel<OpMx8, 2, 2, 2, 1><<<grid, 256, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  else if (p.shape == 2) mx8_tile_kernel<OpMx8, 2, 2, 2, 1><<<grid, 256, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
+  else mx8_tile_kernel<OpMx8, 4, 1, 1, 1><<<grid, 256, 0, stream>>>(k, p.tiles_n, p.tiles_t, p.shares);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.shares == 1) return e;
   const int64_t outputs = a.n * a.t;

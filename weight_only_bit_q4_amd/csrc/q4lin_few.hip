@@ -78,7 +78,9 @@ few_kernel(FewKernel a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, lh = lane >> 5;
   const int K = a.K, G = K >> 6;
-  const int gb = (int)((int64_t)G * wave / kWaves), cnt = (int)((int64_t)G * (wave + 1) / kWaves) - gb;
+  // (whole chunks to a wave: lines of codes belong to one wave)
+  const int all = (G + kChunk - 1) / kChunk;
+  const int gb = all * wave / kWaves * kChunk, cnt = min(G, all * (wave + 1) / kWaves * kChunk) - gb;
   const int chunks = cnt > kChunk ? (cnt + kChunk - 1) / kChunk : 1;  // (a wave without groups still meets the others)
   const uint32_t crow = (uint32_t)K >> 1;
   const rsrc_t rx = make_rsrc(a.x, (uint32_t)a.T * (uint32_t)K * (OP::XB / 64));

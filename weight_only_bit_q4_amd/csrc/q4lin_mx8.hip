@@ -100,7 +100,7 @@ constexpr int kThreads = 64 * kWaves;
 
 template <int RT, int TT, int CH, int NX>
 __global__ void __launch_bounds__(kThreads, 2)
-mx8_stream_kernel(Mx8Kernel a, int BN) {
+mx8_stream_kernel(Mx8Kernel a, int BN, int ranges) {
   static_assert(NX <= CH && (2 * CH) % NX == 0, "slots");
   constexpr int CROW = CH * 32;                // bytes of a row in a chunk
   constexpr int CPC = CROW / 16;               // 16-byte pieces of it
@@ -118,8 +118,11 @@ mx8_stream_kernel(Mx8Kernel a, int BN) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, lh = lane >> 5;
   const int K = a.K, G = K >> 6;
-  const int n0 = blockIdx.x * BN, rows = min(BN, a.N - n0);
-  const int t0 = blockIdx.y * (32 * TT), tokens = min(32 * TT, a.T - t0);
+  // (the two ranges of tokens of a block of rows on one XCD, eight apart)
+  const int block = ranges == 1 ? blockIdx.x : (int)(blockIdx.x >> 4) * 8 + (int)(blockIdx.x & 7);
+  const int n0 = block * BN, rows = min(BN, a.N - n0);
+  if (rows <= 0) return;
+  const int t0 = ranges == 1 ? 0 : (int)(blockIdx.x >> 3 & 1) * (32 * TT), tokens = min(32 * TT, a.T - t0);
   const int gb = (int)((int64_t)G * wave / kWaves), cnt = (int)((int64_t)G * (wave + 1) / kWaves) - gb;
   const uint32_t crow = (uint32_t)K >> 1;
 
@@ -695,7 +698,8 @@ bool takes_stream(int64_t n, int64_t k, int64_t t, const TilePlan& tiles) {
 
 template <int RT, int TT, int CH, int NX>
 void launch_stream(const Mx8Kernel& k, int bn, int ranges, hipStream_t stream) {
-  mx8_stream_kernel<RT, TT, CH, NX><<<dim3((unsigned)((k.N + bn - 1) / bn), (unsigned)ranges), kThreads, 0, stream>>>(k, bn);
+  const unsigned blocks = (unsigned)((k.N + bn - 1) / bn);
+  mx8_stream_kernel<RT, TT, CH, NX><<<dim3(ranges == 1 ? blocks : (blocks + 7) / 8 * 16), kThreads, 0, stream>>>(k, bn, ranges);
 }
 
 // One token: the bf16 product's single-token kernel on the same values where

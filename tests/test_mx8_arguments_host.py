@@ -85,8 +85,8 @@ def test_workspaces():
 
 def test_scoring_holds_a_run_of_tokens_only():
     """The logits' room does not grow with the prompt, only the activations' does."""
-    one = q.q4lin_linear_logprobs_workspace_bytes(100000, 512, 128, 5)
-    assert q.q4lin_linear_logprobs_workspace_bytes(100000, 512, 128 * 64, 5) == one + (2 * 512 + 4 * 8) * 128 * 63
+    one = q.q4lin_linear_logprobs_workspace_bytes(131072, 512, 256, 5)
+    assert q.q4lin_linear_logprobs_workspace_bytes(131072, 512, 256 * 64, 5) == one + (2 * 512 + 4 * 8) * 256 * 63
 
 
 @pytest.mark.parametrize("k", [64, 4096, 20480, 65536, 1 << 17])

@@ -227,7 +227,8 @@ def test_linear_nan_and_infinite_scales(t, k):
 
 
 @pytest.mark.parametrize("n,k,t", [(300, 32768, 3), (300, 32832, 3), (70, 1 << 17, 2), (70, 1 << 17, 9), (500, 256, 8),
-                                   (500, 192, 4), (1, 64, 1), (1, 320, 200), (255, 128, 64), (257, 1088, 65)])
+                                   (500, 192, 4), (1, 64, 1), (1, 320, 200), (255, 128, 64), (257, 1088, 65),
+                                   (131085, 64, 300)])  # (the last: runs of tokens)
 @pytest.mark.parametrize("form", ["mx8", "bf16"])
 def test_linear_logprobs_at_the_kernels_borders(n, k, t, form):
     top = min(n, 3)

@@ -9,6 +9,7 @@
 // there is no policy argument.
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -340,7 +341,10 @@ int check_workspace(const void* workspace, size_t workspace_bytes, size_t need) 
 // exact codes and are exact to binary32: the many-token route of the plain
 // product rounds the weights to 11 bits, the scaled matrix instructions cut
 // small terms of a group, and either would show in a log probability.
-constexpr int64_t kScoreRun = 128;                // tokens (their logits stay in the caches)
+// A run's logits: 128 MiB, which the cache behind the L2s holds until they are
+// read (65000 x 2048, 512 tokens: 128 a run 314 us, 256 267, all 261; 1024 on
+// 8000 x 2048: 303, 167, all 87), at least kScoreRun tokens.
+constexpr int64_t kScoreRun = 128, kScoreLogits = int64_t(1) << 25;
 constexpr int64_t kMaxScoreK = int64_t(1) << 17;
 struct ScorePlan {
   bool few;
@@ -351,7 +355,8 @@ int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, ScorePlan* p) {
   if (!shape_ok(n, k, t) || !logprobs_shape_ok(n, t, top) || k > kMaxScoreK) return Q4LIN_E_SHAPE;
   *p = ScorePlan{q4lin::few_bf16_ok(k, t), 0, 0, 0, 0, 0};
   if (t == 0) return Q4LIN_OK;
-  const int64_t runs = (t + kScoreRun - 1) / kScoreRun;
+  const int64_t most = std::max(kScoreRun, n > 0 ? kScoreLogits / n : kScoreLogits);
+  const int64_t runs = (t + most - 1) / most;
   p->run = (t + runs - 1) / runs;
   p->x_bytes = al256((size_t)(t * k * 2));
   p->offset_bytes = al256((size_t)(t * (k / 64) * 4));

@@ -14,8 +14,9 @@
  *   X   bfloat16 activations, Y bfloat16 outputs; products are summed in
  *       binary32 and Y is rounded to nearest even ("q4-linear.md", setup
  *       table: BF16 input and output; the note under the metric definitions:
- *       BF16 inputs with FP32 accumulation).  Only the A16 policy exists, so
- *       the call carries no policy argument.
+ *       BF16 inputs with FP32 accumulation).  This is the A16 policy (8-bit
+ *       activations are q4lin_linear_mx8 below), so the call carries no
+ *       policy argument.
  *
  * Memory layout (all buffers are device memory owned by the caller):
  *   codes   uint8  [N][K/2], row-major.  Byte j of a row holds the code of

@@ -11,6 +11,9 @@ it.
 ``linear`` is a convenience over torch tensors (device memory and streams
 only): it checks dtypes/shapes, allocates the output and workspace when the
 caller does not pass them, and calls ``q4lin_linear`` on the current stream.
+The other operators have the like: ``rmsnorm_mx8``, ``quantize_mx8`` and
+``linear_mx8`` for activations in 8 bits, ``logprobs`` and ``linear_logprobs``
+for what follows the last product.
 """
 from __future__ import annotations
 

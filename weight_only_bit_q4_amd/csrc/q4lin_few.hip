@@ -11,6 +11,11 @@
 // its first block's start to its last block's end.  A block's sums meet in one
 // of two LDS buffers behind one barrier; no wave waits for its own stores.
 //
+// Measured: 34816 x 5120 at two tokens 23 us (4.1 TB/s), at eight 26, at
+// sixteen (two slots instead of three) 34; the logits of three tokens on
+// 131072 x 5120 73 (4.9 TB/s).  Shares of K that split a line of codes between
+// two waves read 492 MB there for 357, and took 87.
+//
 // On the matrix cores 32 rows x 32 tokens are one instruction's outputs; the
 // tokens past T are not scaled or stored (tokens 0..3 and 4..7 are four
 // registers of a lane).

@@ -12,6 +12,12 @@
 // group's largest are cut: measured 1e-5 of an output's standard deviation
 // per group), the sums over groups binary32 (and binary64 across waves).
 //
+// Measured: 6144 x 5120 at 32, 64, 128 and 1024 tokens 11.6, 15.8, 21.7 and 53
+// to 57 us (bf16 activations 14.0, 18.3, 23.5 and 73); 8192 x 5120 at 1024
+// tokens 69 (1240 TFLOP/s).  From 129 tokens on the bound is instruction
+// issue: sixteen multiply-adds with the group's scale beside each matrix
+// instruction, and the codes' unpacking.
+//
 // Tokens are the rows of D and weight rows its columns, so that a lane holds
 // one weight row and its scale is one register.
 #include "q4lin_kernels.h"

@@ -13,6 +13,9 @@
 // read a second time, then from the caches).  v is binary32 and is not
 // rounded to bf16 on its way into the norm: h's rounding is the residual
 // stream's alone.  Squares are binary32 per thread, binary64 across lanes.
+//
+// Measured: 4096 rows of 5120 with the residual 28 to 29 us (147 MB: the rate
+// of a large copy), 2048 rows of 6144 quantized 7.9 (38 MB), one row 2.6.
 #include "q4lin_kernels.h"
 #include "q4lin_device.h"
 #include "q4lin_mx8.h"

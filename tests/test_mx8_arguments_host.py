@@ -50,9 +50,11 @@ def test_misaligned(call, name, off):
 
 @pytest.mark.parametrize("call,args", [
     (norm, {"k": 96}), (norm, {"k": 0}), (norm, {"t": -1}), (norm, {"k": (1 << 20) + 64}), (norm, {"t": (1 << 21) + 1}),
-    (quant, {"k": 32}), (quant, {"xs": 132}), (quant, {"gs": -128}), (quant, {"xs": 1 << 40}), (linear, {"k": 100}),
+    (quant, {"k": 32}), (quant, {"xs": 132}), (quant, {"gs": -128}), (quant, {"xs": 1 << 40}), (quant, {"xs": 1 << 62}),
+    (quant, {"gs": 1 << 62}), (linear, {"k": 100}),
     (linear, {"n": -1}), (linear, {"n": (1 << 24) + 1}), (logprobs, {"n": 0}), (logprobs, {"top": 33}),
     (logprobs, {"top": -1}), (logprobs, {"n": 2, "top": 3}), (logprobs, {"t": -1}), (logprobs, {"stride": -1}),
+    (logprobs, {"stride": 1 << 61}),
     (logprobs, {"n": (1 << 24) + 1}), (scores, {"n": 0}), (scores, {"n": 2}), (scores, {"k": 100}), (scores, {"top": 40})])
 def test_shape(call, args):
     assert call(**args) == q.Q4LIN_E_SHAPE

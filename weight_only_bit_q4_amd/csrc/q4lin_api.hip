@@ -782,8 +782,8 @@ int q4lin_quantize_mx8(const void* x, int64_t x_stride, const void* gate, int64_
   if (!shape_ok(0, k, t)) return Q4LIN_E_SHAPE;
   if (t == 0) return Q4LIN_OK;
   // rows are whole 16-byte pieces; a stride may be anything for a single row
-  if (t > 1 && (x_stride < 0 || x_stride % 8 != 0 || x_stride * t * 2 >= kMaxBytes)) return Q4LIN_E_SHAPE;
-  if (t > 1 && gate && (gate_stride < 0 || gate_stride % 8 != 0 || gate_stride * t * 2 >= kMaxBytes))
+  if (t > 1 && (x_stride < 0 || x_stride >= kMaxBytes || x_stride % 8 != 0 || x_stride * t * 2 >= kMaxBytes)) return Q4LIN_E_SHAPE;
+  if (t > 1 && gate && (gate_stride < 0 || gate_stride >= kMaxBytes || gate_stride % 8 != 0 || gate_stride * t * 2 >= kMaxBytes))
     return Q4LIN_E_SHAPE;
   if (!x || !values || !scales) return Q4LIN_E_NULL;
   if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(values, 16)) return Q4LIN_E_ALIGN;
@@ -823,7 +823,7 @@ int q4lin_logprobs(const void* logits, int f32, int64_t stride, const void* toke
                    size_t workspace_bytes, void* stream) {
   if (!logprobs_shape_ok(n, t, top)) return Q4LIN_E_SHAPE;
   if (t == 0) return Q4LIN_OK;
-  if (t > 1 && (stride < 0 || stride * t * 4 >= kMaxBytes)) return Q4LIN_E_SHAPE;
+  if (t > 1 && (stride < 0 || stride >= kMaxBytes || stride * t * 4 >= kMaxBytes)) return Q4LIN_E_SHAPE;
   if (!logits) return Q4LIN_E_NULL;
   if (!aligned(logits, f32 ? 4 : 2)) return Q4LIN_E_ALIGN;
   int st = check_logprobs(tokens, logprob, entropy, top_logprobs, top_ids, top);

@@ -396,8 +396,9 @@ Q4LIN_API int64_t q4lin_logprobs_workspace_bytes(int64_t n, int64_t t, int64_t t
  * projection), which are binary32, not rounded, and only held for a run of
  * tokens, in the workspace.  W as for q4lin_linear; x bf16 [T][K], or (x_scales
  * not NULL) E4M3 values with their scales as above; exact codes in every
- * product, sums in binary32; K up to 2^17.  workspace: q4lin_linear_logprobs_workspace_bytes()
- * bytes, 256-byte aligned.  Errors as for q4lin_linear. */
+ * product, sums in binary32; activations below 2^100 in magnitude (past it a
+ * token's numbers may be NaN); K up to 2^17.  workspace:
+ * q4lin_linear_logprobs_workspace_bytes() bytes, 256-byte aligned.  Errors as for q4lin_linear. */
 Q4LIN_API int q4lin_linear_logprobs(const void *x, const void *x_scales, const void *codes, const void *scales,
                       const void *tokens, void *logprob, void *entropy, void *top_logprobs, void *top_ids,
                       int64_t n, int64_t k, int64_t t, int64_t top, void *workspace, size_t workspace_bytes,

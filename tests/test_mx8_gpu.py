@@ -42,6 +42,18 @@ def test_norm(t, k, form):
         assert len(out) == 2
 
 
+@pytest.mark.parametrize("k", [256, 5120, 40000 // 64 * 64])
+def test_norm_of_very_large_and_small_rows(k):
+    """Squares that leave binary32 on either side: the formula holds where the values are finite."""
+    x = bf16((5, k), k).double()
+    x = (x * torch.tensor([1e30, 3e37, 1e-25, 1e-36, 1.0], dtype=torch.float64)[:, None]).to(torch.bfloat16)
+    values, scales = (v.cpu() for v in q4.rmsnorm_mx8(x.cuda(), eps=0.0))
+    v = x.double()
+    y = v / torch.sqrt(v.square().mean(-1, keepdim=True))
+    # (1 / sqrt near 2^-127 is subnormal: 2^-21 of it at worst)
+    mx8.check_mx8(values, scales, y, mx8.FORM_ERROR["norm"] + 2.0 ** -20, "norm of rows of any size")
+
+
 def test_norm_in_place():
     x, r = bf16((9, 1024), 1).cuda(), bf16((9, 1024), 2).cuda()
     want = q4.rmsnorm_mx8(x, None, residual=r)

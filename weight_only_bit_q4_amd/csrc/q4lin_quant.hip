@@ -12,9 +12,9 @@
 // the sum of squares and the store (longer rows than kMaxPieces a thread are
 // read a second time, then from the caches).  v is binary32 and is not
 // rounded to bf16 on its way into the norm: h's rounding is the residual
-// stream's alone.  Squares are binary32 per thread, binary64 across lanes.
+// stream's alone.  Squares and their sum are binary64, which the bytes hide.
 //
-// Measured: 4096 rows of 5120 with the residual 28 to 29 us (147 MB: the rate
+// Measured: 4096 rows of 5120 with the residual 28 to 30 us (147 MB: the rate
 // of a large copy), 2048 rows of 6144 quantized 7.9 (38 MB), one row 2.6.
 #include "q4lin_kernels.h"
 #include "q4lin_device.h"
@@ -131,7 +131,7 @@ rmsnorm_mx8_kernel(NormArgs a) {
   const int pieces = a.K >> 3;
   const size_t row = blockIdx.x, at = row * (size_t)a.K;
   Eight kept[KEEP ? KEEP : 1];
-  float sum = 0.f;
+  double sum = 0.0;  // (squares of values past 2^63 leave binary32)
   if constexpr (KEEP > 0) {
 #pragma unroll
     for (int j = 0; j < KEEP; ++j) {
@@ -142,15 +142,15 @@ rmsnorm_mx8_kernel(NormArgs a) {
     for (int j = 0; j < KEEP; ++j)
       if (tid + j * threads < pieces)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(kept[j].v[i], kept[j].v[i], sum);
+        for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)kept[j].v[i], (double)kept[j].v[i], sum);
   } else {
     for (int p = tid; p < pieces; p += threads) {
       const Eight v = summed(a, at + 8 * (size_t)p);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v.v[i], v.v[i], sum);
+      for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)v.v[i], (double)v.v[i], sum);
     }
   }
-  double total = sum64_lanes((double)sum);
+  double total = sum64_lanes(sum);
   if ((tid & 63) == 0) part[tid >> 6] = total;
   __syncthreads();
   total = 0.0;

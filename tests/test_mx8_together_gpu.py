@@ -197,6 +197,9 @@ def test_two_graphs_share_a_workspace():
 BORDERS = [(1001, 576, t) for t in (1, 2, 8, 9, 16, 17, 32, 33, 64, 65, 96, 97, 128, 129, 191, 256, 257)]
 BORDERS += [(16500, 192, 16), (8193, 128, 33), (12288, 1024, 20), (12288, 1024, 64), (9000, 4096, 23), (9001, 4160, 40),
             (131, 20480, 23), (70, 8256, 48), (200, 4160, 100), (385, 2112, 129), (1, 320, 31), (3, 64, 300), (5120, 4416, 32)]
+# one token: rows of every number of pieces a lane and of waves
+BORDERS += [(n, k, 1) for n, k in ((300, 64), (6144, 16384), (513, 16448), (2000, 20480), (300, 24576),
+                                     (300, 24640), (70, 32832), (9, 1 << 17), (34816, 192), (65000, 576))]
 
 
 @pytest.mark.parametrize("n,k,t", BORDERS)

@@ -527,9 +527,9 @@ hipError_t launch_pm(const DecodePlan& p, const GemvArgs& a, hipStream_t stream)
     if (WV != 8 || a.glu || a.n2 > 0 || a.f32) return hipErrorInvalidValue;
     kern = decode_kernel<PL, MAXR, NT, WV, false, WV == 8>;
   }
-  if (a.xs != nullptr) {  // (one token, one weight, bf16 outputs)
-    if (NT != 1 || a.glu || a.n2 > 0 || a.lora.b != nullptr) return hipErrorInvalidValue;
-    kern = decode_kernel<PL, MAXR, NT, WV, false, false, NT == 1>;
+  if (a.xs != nullptr) {  // (one token, a piece a lane, one weight, bf16 outputs)
+    if (NT != 1 || PL != 1 || a.glu || a.n2 > 0 || a.lora.b != nullptr) return hipErrorInvalidValue;
+    kern = decode_kernel<PL, MAXR, NT, WV, false, false, NT == 1 && PL == 1>;
   }
   const size_t lds = decode_lds(MAXR, NT, WV, p.bn);
   hipError_t e = allow_full_lds(reinterpret_cast<const void*>(kern));

@@ -361,7 +361,11 @@ int score_plan(int64_t n, int64_t k, int64_t t, int64_t top, ScorePlan* p) {
   p->x_bytes = al256((size_t)(t * k * 2));
   p->offset_bytes = al256((size_t)(t * (k / 64) * 4));
   p->logit_bytes = al256((size_t)(p->run * n * 4));
-  p->total = p->x_bytes + p->offset_bytes + p->logit_bytes + q4lin::logprobs_workspace_bytes(n, p->run, (int)top);
+  // (a shorter last run is cut into more shares a row, and may need more than a whole one)
+  const int64_t last = t - (runs - 1) * p->run;
+  p->total = p->x_bytes + p->offset_bytes + p->logit_bytes +
+             std::max(q4lin::logprobs_workspace_bytes(n, p->run, (int)top),
+                      q4lin::logprobs_workspace_bytes(n, last, (int)top));
   return Q4LIN_OK;
 }
 

@@ -181,6 +181,17 @@ rmsnorm_mx8_kernel(NormArgs a) {
   }
 }
 
+// silu(gate) x.  Below kLowGate e^-gate leaves binary32 where the product need
+// not (x up to 2^128): there silu is gate e^gate to 2^-126 of itself, taken as
+// four factors e^(gate/4), x among them, so that nothing passes an end of
+// binary32 before the product itself does.
+constexpr float kLowGate = -88.f;
+__device__ __forceinline__ float gated(float g, float x) {
+  if (!(g < kLowGate)) return x * (g / (1.f + __expf(-g)));
+  const float q = __expf(0.25f * g);
+  return g * q * x * q * q * q;
+}
+
 // A thread takes eight values of a row.
 __global__ void __launch_bounds__(256)
 quantize_mx8_kernel(const uint16_t* x, const uint16_t* gate, uint8_t* values, uint8_t* scales, int64_t K,
@@ -191,8 +202,16 @@ quantize_mx8_kernel(const uint16_t* x, const uint16_t* gate, uint8_t* values, ui
     Eight y = unpack8(load16(x + t * x_stride + 8 * p));
     if (gate != nullptr) {
       const Eight g = unpack8(load16(gate + t * gate_stride + 8 * p));
+      float least = g.v[0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y.v[i] *= g.v[i] / (1.f + __expf(-g.v[i]));
+      for (int i = 1; i < 8; ++i) least = fminf(least, g.v[i]);
+      if (least >= kLowGate) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y.v[i] *= g.v[i] / (1.f + __expf(-g.v[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y.v[i] = gated(g.v[i], y.v[i]);
+      }
     }
     u32x2_t out;
     const uint32_t scale = to_mx8(y, out);

@@ -234,24 +234,25 @@ __device__ __forceinline__ u32x4_t paired8(u32x4_t v) {
 template <bool MX>
 __global__ void __launch_bounds__(256)
 paired_kernel(const void* x, const uint8_t* scales, uint16_t* out, float* offsets, int64_t pieces) {
-  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (p >= pieces) return;  // (whole groups: pieces is a multiple of eight)
-  u32x4_t v;
-  if constexpr (MX) {
-    const u32x2_t m = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(x) + 8 * p);
-    const float scale = mx8::scale_value(scales[p >> 2]);
-    const u32x2_t a = mx8::to_bf16x4(m.x, scale), b = mx8::to_bf16x4(m.y, scale);
-    v = u32x4_t{a.x, a.y, b.x, b.y};
-  } else {
-    v = load16(static_cast<const uint16_t*>(x) + 8 * p);
-  }
-  const Eight e = unpack8(v);
-  double sum = 0.0;
+  // (whole groups: pieces is a multiple of eight, and so is the grid's step)
+  for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < pieces; p += (int64_t)gridDim.x * 256) {
+    u32x4_t v;
+    if constexpr (MX) {
+      const u32x2_t m = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(x) + 8 * p);
+      const float scale = mx8::scale_value(scales[p >> 2]);
+      const u32x2_t a = mx8::to_bf16x4(m.x, scale), b = mx8::to_bf16x4(m.y, scale);
+      v = u32x4_t{a.x, a.y, b.x, b.y};
+    } else {
+      v = load16(static_cast<const uint16_t*>(x) + 8 * p);
+    }
+    const Eight e = unpack8(v);
+    double sum = 0.0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum += (double)e.v[i];
-  sum = sum8_lanes(sum);
-  *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(v);
-  if ((p & 7) == 0) offsets[p >> 3] = (float)(-136.0 * sum);
+    for (int i = 0; i < 8; ++i) sum += (double)e.v[i];
+    sum = sum8_lanes(sum);
+    *reinterpret_cast<u32x4_t*>(out + 8 * p) = paired8(v);
+    if ((p & 7) == 0) offsets[p >> 3] = (float)(-136.0 * sum);
+  }
 }
 
 }  // namespace
@@ -290,8 +291,10 @@ hipError_t launch_quantize_mx8(const void* x, const void* gate, void* values, vo
 
 hipError_t launch_paired(const void* x, const void* scales, void* out, float* offsets, int64_t k, int64_t t,
                          hipStream_t stream) {
-  const int64_t pieces = t * k / 8;
-  const dim3 grid((unsigned)((pieces + 255) / 256));
+  const int64_t pieces = t * k / 8, blocks = (pieces + 255) / 256;
+  // (a grid whose threads pass 2^32 in one dimension is cut without an error)
+  constexpr int64_t kMost = 1 << 20;
+  const dim3 grid((unsigned)(blocks < kMost ? blocks : kMost));
   uint16_t* const o = static_cast<uint16_t*>(out);
   if (scales != nullptr)
     paired_kernel<true><<<grid, 256, 0, stream>>>(x, static_cast<const uint8_t*>(scales), o, offsets, pieces);

@@ -338,6 +338,7 @@ Q4LIN_API int64_t q4lin_moe_workspace_bytes(int64_t inner, int64_t k, int64_t ex
  * v is binary32 and enters the norm unrounded.  residual NULL: v = x, h is not
  * written; weight NULL: ones.  q4lin_quantize_mx8 writes y = x, or y = silu(gate)
  * * x (gate NULL: none; x and gate may be the halves of one product's rows).
+ * v and y are numbers of binary32: past its range they are infinite.
  *
  *   x, residual, gate, h   bf16 [T][K], 16-byte aligned (x and gate of
  *            q4lin_quantize_mx8: x_stride and gate_stride elements from token
@@ -353,10 +354,14 @@ Q4LIN_API int q4lin_quantize_mx8(const void *x, int64_t x_stride, const void *ga
 
 /* Y = W x X (+ R) with the activations in 8 bits as above: W, Y and the shapes
  * as for q4lin_linear, residual as for q4lin_linear_add (NULL: none; may be
- * y).  Each scaled matrix instruction sums a group's 64 products with the
- * offset of its codes, in binary32 (terms below 2^-17 of the group's largest
- * are cut there); the groups' sums are scaled and added in binary32 and y is
- * rounded once.  Activations below 2^100 in magnitude; past it, or with a NaN
+ * y).  Each scaled matrix instruction sums a group's 64 products q x (q the
+ * code, 0..15) with the offset -8 sum x, in binary32 with terms below 2^-17 of the
+ * group's largest cut, which may be one that the offset takes away again:
+ * activations 1000 times the others', all of them on zero weights, leave an error
+ * of 1 % of the outputs' standard deviation; on ordinary weights none shows beside
+ * the rounding.  (One token takes exact products where its rows suit the
+ * single-token kernel.)  The groups' sums are scaled and added in binary32 and y
+ * is rounded once.  Activations below 2^100 in magnitude; past it, or with a NaN
  * in x, outputs of that token alone may be infinite or NaN.  (For products
  * exact to binary32, decode the values, which bf16 holds exactly, and call
  * q4lin_linear.)  workspace: q4lin_linear_mx8_workspace_bytes() bytes, 256-byte
@@ -395,8 +400,9 @@ Q4LIN_API int64_t q4lin_logprobs_workspace_bytes(int64_t n, int64_t t, int64_t t
 /* LinearLogprobs: q4lin_logprobs of the logits W x X (a vocabulary's
  * projection), which are binary32, not rounded, and only held for a run of
  * tokens, in the workspace.  W as for q4lin_linear; x bf16 [T][K], or (x_scales
- * not NULL) E4M3 values with their scales as above; exact codes in every
- * product, sums in binary32; activations below 2^100 in magnitude (past it a
+ * not NULL) E4M3 values with their scales as above.  Every product (128 + q) x is
+ * exact, their sums and the offsets -136 sum x are binary32 (terms up to some 30
+ * times those of W x X, so 2^-24 of such terms an addition); activations below 2^100 in magnitude (past it a
  * token's numbers may be NaN); K up to 2^17.  workspace:
  * q4lin_linear_logprobs_workspace_bytes() bytes, 256-byte aligned.  Errors as for q4lin_linear. */
 Q4LIN_API int q4lin_linear_logprobs(const void *x, const void *x_scales, const void *codes, const void *scales,

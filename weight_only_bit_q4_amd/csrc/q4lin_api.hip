@@ -337,8 +337,8 @@ int check_workspace(const void* workspace, size_t workspace_bytes, size_t need) 
 }
 
 // LinearLogprobs: runs of `run` tokens whose logits lie in the workspace as
-// binary32, after all activations in the kernels' order.  The products have
-// exact codes and are exact to binary32: the many-token route of the plain
+// binary32, after all activations in the kernels' order.  The products are of
+// exact codes and summed in binary32: the many-token route of the plain
 // product rounds the weights to 11 bits, the scaled matrix instructions cut
 // small terms of a group, and either would show in a log probability.
 // A run's logits: 128 MiB, which the cache behind the L2s holds until they are

@@ -270,12 +270,13 @@ hipError_t launch_moe(const MoeArgs& a, void* workspace, hipStream_t stream);
 
 // Activations in 8 bits (q4lin_quant.hip): E4M3 values [t][k] and E8M0 scales
 // [t][k/32] of the norm of x (+ residual; then h = bf16 of the sum), of x or
-// of silu(gate) x (row strides in elements), and back to bf16.
+// of silu(gate) x (row strides in elements).
 hipError_t launch_rmsnorm_mx8(const void* x, const void* residual, const void* weight, void* h, void* values,
                               void* scales, int64_t k, int64_t t, float eps, hipStream_t stream);
 hipError_t launch_quantize_mx8(const void* x, const void* gate, void* values, void* scales, int64_t k, int64_t t,
                                int64_t x_stride, int64_t gate_stride, hipStream_t stream);
-// scales nullptr: x is bf16
+// The activations of the exact products: bf16 in the codes' order and each
+// group's offset of the codes, of E4M3 values and their scales (nullptr: x is bf16).
 hipError_t launch_paired(const void* x, const void* scales, void* out, float* offsets, int64_t k, int64_t t,
                          hipStream_t stream);
 

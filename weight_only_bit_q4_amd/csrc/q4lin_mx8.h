@@ -122,7 +122,8 @@ struct OpMx8 {
 
 // bf16 in the codes' order (of every eight: k0 k4 k1 k5 k2 k6 k3 k7), codes as
 // the exact bf16 128 + q; the offsets of the codes come with the activations.
-// Sums exact to binary32.  Lane half h takes k = 32 h + 8 m .. + 7 in
+// Exact products, binary32 sums (of terms some 30 times those of q - 8: the
+// offset, -136 times the activations' sum, takes most of them away).  Lane half h takes k = 32 h + 8 m .. + 7 in
 // instruction m.
 struct OpBf16 {
   static constexpr int XB = 128;

@@ -7,16 +7,21 @@
 // A matrix instruction's K is one 64-group: per group and 32 x 32 outputs
 // one v_mfma_scale_f32_32x32x64_f8f6f4 (64 clocks) and sixteen multiply-adds
 // with the group's scale (64 clocks of the vector ALU), against four bf16
-// instructions of 32 clocks for bf16 activations.  The products' own sums are
-// binary32 with the instruction's alignment (terms below about 2^-17 of a
-// group's largest are cut: measured 1e-5 of an output's standard deviation
-// per group), the sums over groups binary32 (and binary64 across waves).
+// instructions of 32 clocks for bf16 activations.  One instruction more for
+// each group and 32 tokens of a wave forms the codes' offsets (-8 times the
+// activations' sum): one of three in the 256- and 128-row tiles, of four in the
+// 192-row ones, of two where a wave has 32 rows.  The products' own sums are
+// binary32 with the instruction's alignment: terms below about 2^-17 of a
+// group's largest q x are cut, also where the offset takes that one away again
+// (measured 1e-5 of an output's standard deviation per group; 1e-2 of it in all
+// for activations 1000 times the others' on weights that are all zero); the
+// sums over groups are binary32 (and binary64 across waves).
 //
-// Measured: 6144 x 5120 at 32, 64, 128 and 1024 tokens 11.6, 15.8, 21.7 and 53
-// to 57 us (bf16 activations 14.0, 18.3, 23.5 and 73); 8192 x 5120 at 1024
-// tokens 69 (1240 TFLOP/s).  From 129 tokens on the bound is instruction
-// issue: sixteen multiply-adds with the group's scale beside each matrix
-// instruction, and the codes' unpacking.
+// Measured, replayed with weights from memory: 6144 x 5120 at 32, 64, 128 and
+// 1024 tokens 12.0, 16.4, 24.1 and 54 us (bf16 activations 14.4, 19.1, 24.3 and
+// 74); 8192 x 5120 at 1024 tokens 70 (1230 TFLOP/s).  From 129 tokens on the
+// bound is instruction issue: sixteen multiply-adds with the group's scale
+// beside each matrix instruction, and the codes' unpacking.
 //
 // Tokens are the rows of D and weight rows its columns, so that a lane holds
 // one weight row and its scale is one register.
@@ -49,7 +54,7 @@ struct Mx8Kernel {
 };
 
 // Two bytes per group (a weight row's fp16 scales, a token's two block
-// scales) of G8 groups from group g on, groups at or past `end` as zeros.
+// scales) of GROUPS groups from group g on, groups at or past `end` as zeros.
 // The rows need not be aligned.
 template <int GROUPS>
 struct Strip {
@@ -99,7 +104,10 @@ __device__ __forceinline__ uint16_t finished(double v, const uint16_t* res, size
 // no barrier until the eight waves' sums meet.
 //
 // Every copy of the loop is issued whether or not its group exists (past the
-// wave's share it reads nothing), so that the counts of the waits hold.
+// wave's share it reads nothing), so that the counts of the waits hold.  They
+// hold within a chunk only: the scales' loads branch at a row's end, and where
+// the branches join the compiler waits for all that is in flight, so that each
+// chunk begins with a latency of memory.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
@@ -161,7 +169,7 @@ mx8_stream_kernel(Mx8Kernel a, int BN, int ranges) {
     const bool in = c * CH + cgroup < cnt;
 #pragma unroll
     for (int j = 0; j < NC; ++j)
-      dma16<2>(rc, in ? coff[j] + (uint32_t)c * CROW : kNowhere, 0, slot + wave * CSLOT + j * 1024);
+      dma16<mfma16::kOnce>(rc, in ? coff[j] + (uint32_t)c * CROW : kNowhere, 0, slot + wave * CSLOT + j * 1024);
   };
   auto issue_x = [&](uint8_t* slot, int q) __device__ {
     const bool in = q < cnt;
@@ -306,7 +314,8 @@ mx8_stream_kernel(Mx8Kernel a, int BN, int ranges) {
 // in the paired order with the offsets of their groups, binary32 outputs to
 // `part` (the logits of q4lin_linear_logprobs; twice the bytes of an
 // activation, four matrix instructions of 32 clocks a tile instead of one of
-// 64, none for the offsets).
+// 64, none for the offsets).  Registers: 134 to 211, in the 256 x 128 tiles all
+// 256 with one spilled.
 // ---------------------------------------------------------------------------
 constexpr int kRun = 16;   // groups between two loads of scales: eight stages
 constexpr int kSlots = 4;
